@@ -20,3 +20,15 @@ from .binding import (  # noqa: F401
     library,
     status_string,
 )
+from .cache_ops import (  # noqa: F401
+    fa_cache_compact,
+    fa_cache_select,
+    fa_fwd_tree,
+    fa_key_weights,
+    fa_key_weights_workspace_bytes,
+    fa_rope,
+    fa_rope_append,
+    fa_rope_bwd,
+    fa_rope_frequencies,
+    fa_tree_workspace_bytes,
+)

@@ -81,6 +81,30 @@ def library(path: str | None = None):
             lib.fa_fwd_decode.argtypes = [vp, p64, vp, p64, vp, p64, vp, p64, vp, vp, i, i, i, i, i, i, f, vp, sz,
                                           vp]
             lib.fa_fwd_decode.restype = i
+            i64, dbl = ctypes.c_int64, ctypes.c_double
+            lib.fa_rope_frequencies.argtypes = [vp, vp, i, dbl, i, dbl, i, dbl, dbl]
+            lib.fa_rope_frequencies.restype = i
+            for name in ("fa_rope", "fa_rope_bwd"):
+                getattr(lib, name).argtypes = [vp, p64, vp, p64, vp, p64, vp, p64, vp, i64, vp, i, i, i, i, i, i, i, f,
+                                               vp]
+                getattr(lib, name).restype = i
+            lib.fa_rope_append.argtypes = [vp, p64, vp, p64, vp, p64, vp, p64, vp, p64, vp, p64, vp, vp, i64, vp,
+                                           i, i, i, i, i, i, i, i, f, vp]
+            lib.fa_rope_append.restype = i
+            lib.fa_tree_workspace_bytes.argtypes = [i, i, i, i, i, i]
+            lib.fa_tree_workspace_bytes.restype = sz
+            lib.fa_fwd_tree.argtypes = [vp, p64, vp, p64, vp, p64, vp, p64, vp, vp, i64, vp, i, i, i, i, i, i, f, vp,
+                                        sz, vp]
+            lib.fa_fwd_tree.restype = i
+            lib.fa_key_weights_workspace_bytes.argtypes = [i, i, i, i, i, i]
+            lib.fa_key_weights_workspace_bytes.restype = sz
+            lib.fa_key_weights.argtypes = [vp, p64, vp, p64, vp, vp, vp, vp, i, i, i, i, i, i, i, f, vp, sz, vp]
+            lib.fa_key_weights.restype = i
+            lib.fa_cache_select.argtypes = [vp, vp, vp, vp, i, i, i, i, i, i, vp]
+            lib.fa_cache_select.restype = i
+            lib.fa_cache_compact.argtypes = [vp, p64, vp, p64, vp, vp, p64, vp, p64, vp, vp, i64, i64, vp,
+                                             i, i, i, i, i, i, vp]
+            lib.fa_cache_compact.restype = i
             lib.fa_status_string.argtypes = [i]
             lib.fa_status_string.restype = ctypes.c_char_p
             _lib = lib

@@ -8,6 +8,7 @@
 #include <mutex>
 
 #include "../../include/fa.h"
+#include "fa_host.h"
 #include "fa_internal.h"
 
 namespace fa {
@@ -33,24 +34,25 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// A [B, H, N, d] bf16 tensor with element strides s (d contiguous) viewed
-// as 4-D (d, N, H, B); one box is 64 columns (128 bytes, the swizzle span) x
-// 128 rows of one head.  Rows past N read as 0.
-bool encode_map(CUtensorMap *map, const void *base, int B, int H, int N, int d, const Strides &s,
-                unsigned box_rows = 128) {
+}  // namespace
+
+bool encode_map(CUtensorMap *map, const void *base, int B, int H, int N, int d, const Strides &s, unsigned box_rows,
+                unsigned box_heads) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(H),
                         static_cast<cuuint64_t>(B)};
   cuuint64_t strides[3] = {static_cast<cuuint64_t>(s.n) * 2, static_cast<cuuint64_t>(s.h) * 2,
                            static_cast<cuuint64_t>(s.b) * 2};
-  cuuint32_t box[4] = {64, box_rows, 1, 1};
+  cuuint32_t box[4] = {64, box_rows, box_heads, 1};
   cuuint32_t estride[4] = {1, 1, 1, 1};
   CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, estride,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
+
+namespace {
 
 // An [B, H, N, d] e4m3 tensor (one byte per element, element strides s)
 // as 4-D (d, N, H, B); one box is a whole 128-byte row x box_rows rows of
@@ -74,10 +76,8 @@ Strides contiguous(int H, int N, int d) {
   return Strides{static_cast<long long>(H) * N * d, static_cast<long long>(N) * d, d};
 }
 
-// A caller's strides made usable: the stride of an extent-1 dimension is
-// never used, so it is replaced by a harmless valid value; then every
-// stride must be positive and a multiple of 8 elements (16 bytes: TMA and
-// the 16-byte row accesses).  False if the layout is not supported.
+}  // namespace
+
 bool normalise(const int64_t *in, int B, int H, int N, int d, Strides *out) {
   if (!in) return false;
   Strides s{in[0], in[1], in[2]};
@@ -91,7 +91,6 @@ bool normalise(const int64_t *in, int B, int H, int N, int d, Strides *out) {
   return true;
 }
 
-// Address span [lo, hi) of the elements of a strided tensor.
 void span(const void *base, int B, int H, int N, int d, const Strides &s, uintptr_t *lo, uintptr_t *hi) {
   const uintptr_t b0 = reinterpret_cast<uintptr_t>(base);
   const long long last = (B - 1) * s.b + (H - 1) * s.h + (N - 1) * s.n + d;
@@ -99,8 +98,6 @@ void span(const void *base, int B, int H, int N, int d, const Strides &s, uintpt
   *hi = b0 + static_cast<uintptr_t>(last) * 2;
 }
 
-// No two elements of the tensor share an address (each stride covers the
-// extent of the smaller ones): required of the outputs.
 bool injective(int B, int H, int N, int d, const Strides &s) {
   struct Dim { long long stride, extent; } dims[3] = {{s.b, B}, {s.h, H}, {s.n, N}};
   for (int i = 0; i < 3; ++i)
@@ -121,46 +118,65 @@ bool injective(int B, int H, int N, int d, const Strides &s) {
 
 bool spans_overlap(uintptr_t alo, uintptr_t ahi, uintptr_t blo, uintptr_t bhi) { return alo < bhi && blo < ahi; }
 
-// Two tensors with the same strides s, whose layout is injective (each
-// stride at least the extent of the smaller ones), and bases `delta`
-// elements apart share an element iff delta = sum_k a_k s_k + c with
-// |a_k| < extent_k and |c| < d.  With nested strides only the two integer
-// quotients next to delta / s_k can work at each level, so this small
-// search is exact.  (It lets the slices of one packed buffer, such as the
-// q, k, v gradients of a [B, N, 3, H, d] projection, be outputs together.)
-bool lattice_hit(long long rem, const long long (*dims)[2], int k, int d) {
+namespace {
+
+// Two tensors with the same strides, nested (each stride at least the extent
+// of the smaller ones), and bases `rem` elements apart share an element iff
+// rem = sum_k a_k s_k + c with a_k in [-(extent of the second - 1), extent of
+// the first - 1] and |c| < d.  With nested strides only the two integer
+// quotients next to rem / s_k can work at each level, so this small search
+// is exact.  (It lets the slices of one packed buffer, such as the q, k, v
+// gradients of a [B, N, 3, H, d] projection, be outputs together.)
+struct LatticeDim {
+  long long stride, ea, eb;
+};
+bool lattice_hit(long long rem, const LatticeDim *dims, int k, int d) {
   if (k == 3) return rem > -d && rem < d;
-  const long long st = dims[k][0], ext = dims[k][1];
-  if (ext == 1) return lattice_hit(rem, dims, k + 1, d);  // only a = 0: skip it
+  const long long st = dims[k].stride, ea = dims[k].ea, eb = dims[k].eb;
+  if (ea == 1 && eb == 1) return lattice_hit(rem, dims, k + 1, d);  // only a = 0: skip it
   const long long q = rem / st;
   for (long long a = q - 1; a <= q + 1; ++a)
-    if (a > -ext && a < ext && lattice_hit(rem - a * st, dims, k + 1, d)) return true;
+    if (a > -eb && a < ea && lattice_hit(rem - a * st, dims, k + 1, d)) return true;
   return false;
 }
 
-// Whether two tensors of [B, H, N, d] may share an element.  Exact when
-// both have the same injective strides; otherwise whether their address
-// spans overlap.
-bool may_overlap(const void *a, const Strides &sa, const void *b, const Strides &sb, int B, int H, int N, int d) {
+}  // namespace
+
+bool may_overlap(const void *a, Strides sa, int Ha, int Na, const void *b, Strides sb, int Hb, int Nb, int B, int d) {
   uintptr_t alo, ahi, blo, bhi;
-  span(a, B, H, N, d, sa, &alo, &ahi);
-  span(b, B, H, N, d, sb, &blo, &bhi);
+  span(a, B, Ha, Na, d, sa, &alo, &ahi);
+  span(b, B, Hb, Nb, d, sb, &blo, &bhi);
   if (!spans_overlap(alo, ahi, blo, bhi)) return false;
+  const int H = Ha > Hb ? Ha : Hb, N = Na > Nb ? Na : Nb;
+  // the stride of an extent-1 dimension is not used: it may as well be the other tensor's
+  if (B == 1) sa.b = sb.b;
+  if (Ha == 1) sa.h = sb.h;
+  if (Hb == 1) sb.h = sa.h;
+  if (Na == 1) sa.n = sb.n;
+  if (Nb == 1) sb.n = sa.n;
   const bool same = sa.b == sb.b && sa.h == sb.h && sa.n == sb.n;
   if (!same || !injective(B, H, N, d, sa)) return true;
-  long long dims[3][2] = {{sa.b, B}, {sa.h, H}, {sa.n, N}};
+  LatticeDim dims[3] = {{sa.b, B, B}, {sa.h, Ha, Hb}, {sa.n, Na, Nb}};
   for (int i = 0; i < 3; ++i)  // descending strides
     for (int j = i + 1; j < 3; ++j)
-      if (dims[j][0] > dims[i][0])
-        for (int c = 0; c < 2; ++c) {
-          const long long t = dims[i][c];
-          dims[i][c] = dims[j][c];
-          dims[j][c] = t;
-        }
+      if (dims[j].stride > dims[i].stride) {
+        const LatticeDim t = dims[i];
+        dims[i] = dims[j];
+        dims[j] = t;
+      }
   const long long delta_bytes = static_cast<long long>(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a));
   if (delta_bytes % 2) return true;
   return lattice_hit(delta_bytes / 2, dims, 0, d);
 }
+
+namespace {
+
+// The same for two tensors of equal extents.
+bool may_overlap(const void *a, const Strides &sa, const void *b, const Strides &sb, int B, int H, int N, int d) {
+  return may_overlap(a, sa, H, N, b, sb, H, N, B, d);
+}
+
+}  // namespace
 
 int *status_ptr() {
   void *p = nullptr;
@@ -169,6 +185,8 @@ int *status_ptr() {
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+namespace {
 
 constexpr long long kMaxGridX = 2147483647LL;  // largest x extent of a launch grid
 // Causal backward: pairs of mirror blocks per CTA up to this many blocks per
@@ -221,9 +239,6 @@ fa_status_t check_common(int B, int H, int N, int d, int causal, float scale) {
 // Events the next fa_bwd call of this thread records around its kernels.
 thread_local cudaEvent_t t_bwd_ev[3] = {nullptr, nullptr, nullptr};
 
-size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
-
-
 }  // namespace
 }  // namespace fa
 
@@ -259,7 +274,8 @@ struct RowAxis {
   int rows() const { return cu ? T : N; }
 };
 
-// SMs of the current device (cached per host thread and device), 0 if unknown.
+}  // namespace
+
 int sm_count() {
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
@@ -269,6 +285,8 @@ int sm_count() {
   if (dev >= 0 && dev < 64) cached[dev] = n;
   return n;
 }
+
+namespace {
 
 fa_status_t fwd_impl(const void *q, const Strides &sq, const void *k, const Strides &sk, const void *v,
                      const Strides &sv, void *o, const Strides &so, float *lse, const RowAxis &ax, int H, int d,

@@ -1,0 +1,93 @@
+// fa_cache.h -- parameter blocks and launchers of the operators around the
+// key/value cache (rotary positions, drafted-tree attention, key weights,
+// eviction).  Not part of the ABI.
+#pragma once
+
+#include "fa_internal.h"
+
+namespace fa {
+
+// Rotary positions.  The row (b, n) of every head of up to three tensors:
+// heads [0, H) are q, [H, H + Hkv) are k, [H + Hkv, H + 2 Hkv) are v (append
+// form only, copied).  In the append form k and v rows go to cache row
+// cache_len[b] - N + n and are skipped where that row lies outside [0, Nk).
+struct RopeParams {
+  const __nv_bfloat16 *q, *k, *v;
+  __nv_bfloat16 *qo, *ko, *vo;
+  Strides sq, sk, sv, sqo, sko, svo;
+  const int *positions;       // [B] rows of N with stride pos_b, or null
+  long long pos_b;
+  const float *inv_freq;      // [rot / 2] radians per position
+  const int *cache_len;       // append form: [B]; else null
+  int B, H, Hkv, N, Nk, d, rot;
+  float factor;
+  float sign;                 // +1 forward, -1 backward (the transposed rotation)
+  int copy_rest;              // 0: in place, the columns past rot stay where they are
+  int heads;                  // H + Hkv (+ Hkv)
+  int head_groups;            // CTAs along the head axis
+};
+cudaError_t launch_rope(bool interleaved, const RopeParams &p, cudaStream_t stream);
+
+// Attention of a tree of Nt drafted tokens per sequence over a cache.
+struct TreeParams {
+  const __nv_bfloat16 *q, *k, *v;
+  __nv_bfloat16 *o;
+  float *lse;                 // [B, H, Nt] contiguous
+  Strides sq, sk, sv, so;
+  const int *parents;         // [B] rows of Nt with stride par_b
+  long long par_b;
+  const int *cache_len;       // [B] or null
+  int *status;
+  int B, H, Hkv, G, Nt, Nk, d;
+  float scale_log2;
+  int neg;
+};
+cudaError_t launch_tree(const TreeParams &p, cudaStream_t stream);
+
+// Accumulated attention weight per key.
+struct KeyWeightParams {
+  const __nv_bfloat16 *q, *k;
+  const float *lse;           // [B, H, Nq] contiguous
+  const float *w_in;          // [B, Hkv, Nk] or null
+  float *w;
+  Strides sq, sk;
+  const int *cache_len;       // [B] or null
+  int *status;
+  int B, H, Hkv, G, Nq, Nk, d, causal;
+  float scale_log2;
+};
+cudaError_t launch_key_weights(const KeyWeightParams &p, cudaStream_t stream);
+
+// Rows to keep of each cache: ascending row numbers, -1 behind them.
+struct SelectParams {
+  const float *w;             // [B, Hkv, Nk]
+  const int *cache_len;       // [B] or null
+  int *kept;                  // [B, Hkv, keep]
+  int *new_len;               // [B]
+  int B, Hkv, Nk, keep, first, recent;
+};
+cudaError_t launch_cache_select(const SelectParams &p, cudaStream_t stream);
+
+// Rows moved inside (or out of) a cache.
+struct CompactParams {
+  const __nv_bfloat16 *k, *v;
+  const float *w;             // [B, Hkv, Nk] or null
+  __nv_bfloat16 *ko, *vo;
+  float *wo;                  // [B, Hkv, Nout] or null
+  Strides sk, sv, sko, svo;
+  const int *kept;            // row lists of M entries, strides kept_b and kept_h
+  long long kept_b, kept_h;
+  const int *base;            // [B] or null
+  int B, Hkv, Nk, Nout, M, d;
+  int in_place;
+};
+cudaError_t launch_cache_compact(const CompactParams &p, cudaStream_t stream);
+
+// Valid rows of the cache of batch entry b, clamped into [0, Nk].
+__device__ inline int cache_rows(const int *cache_len, int b, int Nk) {
+  if (!cache_len) return Nk;
+  const int n = cache_len[b];
+  return n < 0 ? 0 : (n > Nk ? Nk : n);
+}
+
+}  // namespace fa

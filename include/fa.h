@@ -263,6 +263,195 @@ FA_API fa_status_t fa_fwd_decode(const void *q, const int64_t *q_strides, const 
                                  cudaStream_t stream);
 
 /*
+ * Operators around the key/value cache: rotary positions, attention for a
+ * tree of drafted tokens, the accumulated attention weight of each cached
+ * key, and eviction by it.  The glossary page "FlashAttention"
+ * (blog.brdg.mn) places the method in model serving next to the management
+ * of that cache; the pages describe none of these calls, their definitions
+ * are this library's.
+ *
+ * Conventions they share, beside those at the top of this file: tensors are
+ * bf16 with element strides as in the *_strided calls; a cache is
+ * [B, Hkv, Nk, d] with cache_seqlens as in fa_fwd_decode (int32 [B], 4-byte
+ * aligned, NULL for all Nk rows; it counts the new rows; clamped into
+ * [0, Nk]); queries may have H = G * Hkv heads, G of them sharing a cache
+ * head (query head h uses cache head h / G).  B * H < 2^24; Nk, the query
+ * rows and the tokens of a call (B * N) are at most 2^30.  Values behind a
+ * sequence's last row are read as memory but never used, whatever they are
+ * (infinities and NaN included), and rows that no argument names are left
+ * as they were.  Every call may be captured into a graph.
+ */
+
+/*
+ * Rotary positions.  In the first `rot` columns of every row, pair i turns
+ * by the angle a = position * inv_freq[i] and is scaled by `factor`:
+ *     y1 = factor * (x1 cos a - x2 sin a),  y2 = factor * (x2 cos a + x1 sin a)
+ * with pairs (i, i + rot/2), or (2i, 2i + 1) if interleaved = 1; the columns
+ * past rot are copied.  Computed in fp32 (the angle exactly modulo a turn,
+ * for any 32-bit position) and rounded once.
+ *   q, k           : inputs  [B, H, N, d] and [B, Hkv, N, d]; k and k_out are
+ *                    NULL and Hkv = 0 when there is only q
+ *   q_out, k_out   : outputs of the same shapes; each is its own input
+ *                    (same pointer and strides: in place) or shares no
+ *                    element with any argument
+ *   positions      : int32, row (b, n) at positions[b * positions_stride + n]
+ *                    (stride 0: shared by the batch), any value; NULL: n
+ *   inv_freq       : fp32 [rot / 2], radians per position, finite
+ *   rot            : a multiple of 16 up to d (FA_ERR_UNSUPPORTED otherwise)
+ * fa_rope_bwd is the gradient: given dL/dq_out and dL/dk_out (same
+ * positions, frequencies and factor) it writes dL/dq and dL/dk, the same
+ * rotation by -a; the copied columns' gradients are copied.
+ */
+FA_API fa_status_t fa_rope(const void *q, const int64_t *q_strides, const void *k, const int64_t *k_strides,
+                           void *q_out, const int64_t *q_out_strides, void *k_out, const int64_t *k_out_strides,
+                           const int *positions, int64_t positions_stride, const float *inv_freq, int B, int H,
+                           int Hkv, int N, int d, int rot, int interleaved, float factor, cudaStream_t stream);
+
+FA_API fa_status_t fa_rope_bwd(const void *dq_out, const int64_t *dq_out_strides, const void *dk_out,
+                               const int64_t *dk_out_strides, void *dq, const int64_t *dq_strides, void *dk,
+                               const int64_t *dk_strides, const int *positions, int64_t positions_stride,
+                               const float *inv_freq, int B, int H, int Hkv, int N, int d, int rot, int interleaved,
+                               float factor, cudaStream_t stream);
+
+/*
+ * Rotary positions and the cache's new rows in one launch: q is rotated into
+ * q_out (which may be q), k is rotated into k_cache and v copied into
+ * v_cache.  The N tokens are the LAST N rows of the sequence, as in
+ * fa_fwd_decode: token n of batch entry b goes to cache row
+ * cache_seqlens[b] - N + n.  A row outside [0, Nk) is not written (here
+ * cache_seqlens is not clamped).  positions NULL: the cache row; a drafted
+ * tree or a cache that rows were evicted from passes its own.
+ *   q [B, H, N, d]; k, v [B, Hkv, N, d]; k_cache, v_cache [B, Hkv, Nk, d];
+ *   cache_seqlens is required.  No output shares an element with an input
+ *   (but q_out with q) or with another output.
+ */
+FA_API fa_status_t fa_rope_append(const void *q, const int64_t *q_strides, const void *k, const int64_t *k_strides,
+                                  const void *v, const int64_t *v_strides, void *q_out, const int64_t *q_out_strides,
+                                  void *k_cache, const int64_t *k_cache_strides, void *v_cache,
+                                  const int64_t *v_cache_strides, const int *cache_seqlens, const int *positions,
+                                  int64_t positions_stride, const float *inv_freq, int B, int H, int Hkv, int N,
+                                  int Nk, int d, int rot, int interleaved, float factor, cudaStream_t stream);
+
+/* How fa_rope_frequencies scales for contexts longer than the training length. */
+enum {
+    FA_ROPE_PLAIN = 0,    /* inv_freq[i] = base^(-2i / rot) */
+    FA_ROPE_LINEAR = 1,   /* positions divided: inv_freq[i] / factor */
+    FA_ROPE_BASE = 2,     /* base enlarged: base * factor^(rot / (rot - 2)) */
+    FA_ROPE_BY_PARTS = 3  /* see below */
+};
+
+/*
+ * Host function: fills inv_freq (host memory, rot / 2 values) and
+ * *factor_out (the `factor` of the calls above).  FA_ROPE_BY_PARTS keeps the
+ * frequencies that make fast_turns turns or more over original_len
+ * positions, divides those that make slow_turns or fewer by `factor`, blends
+ * linearly in the turns between, and sets *factor_out = 1 + 0.1 ln factor;
+ * the other schemes set 1.  factor >= 1 (unused by FA_ROPE_PLAIN),
+ * base > 1, rot even (above 2 for FA_ROPE_BASE); original_len >= 1 and
+ * fast_turns > slow_turns > 0 are used by FA_ROPE_BY_PARTS only.
+ */
+FA_API fa_status_t fa_rope_frequencies(float *inv_freq, float *factor_out, int rot, double base, int scaling,
+                                       double factor, int original_len, double fast_turns, double slow_turns);
+
+/*
+ * Attention of a tree of Nt drafted tokens per sequence over its cache.  The
+ * tree's nodes are the LAST Nt rows of the sequence (node i is cache row
+ * len_b - Nt + i, its key and value already stored); parents[b, i] is the
+ * node that node i follows, parents[b, i] < i, or -1 for the last row before
+ * the tree.  Query row i sees every row before the tree, its own row and
+ * its ancestors' rows:
+ *     o = softmax(scale * q k^T) v and lse over the rows it sees.
+ * A node whose parent is not in [-1, i), or whose cache row would be
+ * negative (len_b < Nt), is padding, and so is every node below it: its
+ * result is o = 0, lse = -inf, and no row sees it, whatever its cache row
+ * holds.  (A value row that some node sees must be finite: one that is not
+ * may reach the results of the nodes that do not see it.)
+ *   q, o   : [B, H, Nt, d]; k, v : [B, Hkv, Nk, d]; lse : fp32 [B, H, Nt]
+ *   parents: int32, node (b, i) at parents[b * parents_stride + i] (stride
+ *            0: one tree for the whole batch)
+ *   1 <= Nt <= 128; Nt = 1 with parent -1 is a decode step with grouped
+ *   heads, a chain (parent i - 1) is the causal decode of several rows.
+ *   workspace: fa_tree_workspace_bytes() bytes (may be 0), 256-byte
+ *   aligned, or NULL to take it with cudaMallocAsync on `stream`.
+ * Work is split over the keys; the split depends on the shape and on
+ * cache_seqlens only, so results are bitwise reproducible.
+ */
+FA_API size_t fa_tree_workspace_bytes(int B, int H, int Hkv, int Nt, int Nk, int d);
+
+FA_API fa_status_t fa_fwd_tree(const void *q, const int64_t *q_strides, const void *k, const int64_t *k_strides,
+                               const void *v, const int64_t *v_strides, void *o, const int64_t *o_strides,
+                               float *lse, const int *parents, int64_t parents_stride, const int *cache_seqlens,
+                               int B, int H, int Hkv, int Nt, int Nk, int d, float scale, void *workspace,
+                               size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Accumulated attention weight of each cached key: for every row j < len_b
+ *     weights[b, hk, j] = weights_in[b, hk, j]
+ *         + sum over the G heads h of hk and the query rows i that see j of
+ *           exp(scale * q[b, h, i] . k[b, hk, j] - lse[b, h, i]),
+ * the column sums of the attention matrix whose logsumexp fa_fwd,
+ * fa_fwd_decode or fa_fwd_tree returned.  The Nq query rows are the LAST Nq
+ * positions: with causal = 1 row i sees j <= len_b - Nq + i, with 0 every
+ * j < len_b.  A query row whose lse is -inf adds nothing, whatever q holds.
+ * Rows j >= len_b get weights_in's value.
+ *   q : [B, H, Nq, d]; k : [B, Hkv, Nk, d]; lse : fp32 [B, H, Nq]
+ *   weights_in : fp32 [B, Hkv, Nk] or NULL (zeros); may be weights itself
+ *   weights    : fp32 [B, Hkv, Nk], all of it written
+ *   workspace  : fa_key_weights_workspace_bytes() bytes (may be 0), 256-byte
+ *   aligned, or NULL to take it with cudaMallocAsync on `stream`.
+ * Sums are fp32, in an order that the shape and cache_seqlens fix (no
+ * atomics).
+ */
+FA_API size_t fa_key_weights_workspace_bytes(int B, int H, int Hkv, int Nq, int Nk, int d);
+
+FA_API fa_status_t fa_key_weights(const void *q, const int64_t *q_strides, const void *k, const int64_t *k_strides,
+                                  const float *lse, const float *weights_in, float *weights,
+                                  const int *cache_seqlens, int B, int H, int Hkv, int Nq, int Nk, int d, int causal,
+                                  float scale, void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Which rows of each cache head to keep.  A sequence of len_b <= keep rows
+ * keeps them all.  A longer one keeps its `first` first rows, its `recent`
+ * last rows and, of the rows between, the keep - first - recent with the
+ * greatest weight (of equal weights the lower row; 0 and -0 are equal; a
+ * NaN ranks below every number).
+ *   weights    : fp32 [B, Hkv, Nk]
+ *   kept       : int32 [B, Hkv, keep]: the kept rows, ascending; -1 behind
+ *                them where the sequence is shorter than keep
+ *   new_seqlens: int32 [B]: min(len_b, keep); not cache_seqlens itself
+ *   0 <= first, recent; first + recent <= keep; 1 <= keep <= Nk
+ */
+FA_API fa_status_t fa_cache_select(const float *weights, const int *cache_seqlens, int *kept, int *new_seqlens,
+                                   int B, int Hkv, int Nk, int keep, int first, int recent, cudaStream_t stream);
+
+/*
+ * Moves cache rows together: for every head and every i in [0, M) with
+ * kept[i] >= 0, row base_b + i of k_out, v_out (and weights_out) becomes row
+ * base_b + kept[i] of k, v (and weights).  A row of either side outside its
+ * tensor is skipped.  Rows are moved bit by bit.
+ *   k, v         : [B, Hkv, Nk, d]; weights : fp32 [B, Hkv, Nk] or NULL
+ *   k_out, v_out : [B, Hkv, Nk_out, d]; weights_out : fp32 [B, Hkv, Nk_out],
+ *                  NULL exactly if weights is
+ *   kept         : int32, list of (b, h) at kept[b * kept_b_stride + h *
+ *                  kept_h_stride] (strides 0: shared), M entries each
+ *   base         : int32 [B] or NULL (zeros)
+ * Either every output is its input (same pointers and strides, Nk_out = Nk:
+ * in place), and then the non-negative entries of a list must ascend
+ * strictly and none may be below its place, kept[i] >= i (otherwise rows
+ * hold wrong values; no other memory is touched), or no output shares an
+ * element with an argument, and then the lists may be in any order.
+ * With fa_cache_select's lists this evicts; with base_b the row before which
+ * a drafted tree starts and kept the nodes of the accepted branch, it makes
+ * that branch the sequence's next rows.
+ */
+FA_API fa_status_t fa_cache_compact(const void *k, const int64_t *k_strides, const void *v,
+                                    const int64_t *v_strides, const float *weights, void *k_out,
+                                    const int64_t *k_out_strides, void *v_out, const int64_t *v_out_strides,
+                                    float *weights_out, const int *kept, int64_t kept_b_stride,
+                                    int64_t kept_h_stride, const int *base, int B, int Hkv, int Nk, int Nk_out,
+                                    int M, int d, cudaStream_t stream);
+
+/*
  * Size in bytes of the fixed device array that fa_bwd_noalloc uses as its
  * scratch (8 MiB).  Every GPU that loads the library holds this array until
  * the process exits.  It covers B * H * Np <= 1,048,576 padded rows, where
