@@ -28,21 +28,40 @@ struct RopeParams {
 };
 cudaError_t launch_rope(bool interleaved, const RopeParams &p, cudaStream_t stream);
 
-// Attention of a tree of Nt drafted tokens per sequence over a cache.
+// Attention of a tree of Nt drafted tokens per sequence over a cache.  The G
+// query heads of a cache head are cut into row tiles of `gpt` whole heads
+// (gpt * Nt <= 128 rows); a CTA works on one row tile (`split`: its two
+// softmax warpgroups take alternate key tiles) or on two.  The 128-key tiles
+// of all (b, hk) units, one after the other, are cut into `ranges` equal
+// runs; CTA x takes run x / groups for row tiles 2 * (x % groups) and + 1.
+// A unit that ends up in several runs leaves a partial result for each.
 struct TreeParams {
-  const __nv_bfloat16 *q, *k, *v;
   __nv_bfloat16 *o;
   float *lse;                 // [B, H, Nt] contiguous
-  Strides sq, sk, sv, so;
+  Strides so;
   const int *parents;         // [B] rows of Nt with stride par_b
   long long par_b;
   const int *cache_len;       // [B] or null
   int *status;
+  float *part_o;              // [2 * ctas][slot_rows][d], normalised
+  float *part_lse;            // [2 * ctas][slot_rows], log2 units; +inf marks padding
   int B, H, Hkv, G, Nt, Nk, d;
+  int gpt, row_tiles, groups, ranges, split;
   float scale_log2;
   int neg;
 };
-cudaError_t launch_tree(const TreeParams &p, cudaStream_t stream);
+
+// How a call is cut up: a function of the shape alone.
+struct TreePlan {
+  int gpt, row_tiles, groups, ranges, split;
+  bool merge;                 // some unit may end up in several runs
+  size_t part_rows;           // rows of partial results
+};
+TreePlan plan_tree(int B, int H, int Hkv, int Nt, int Nk);
+
+// tq: q with boxes of Nt rows x gpt heads.
+cudaError_t launch_tree(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const TreeParams &p,
+                        bool merge, cudaStream_t stream);
 
 // Accumulated attention weight per key.
 struct KeyWeightParams {

@@ -55,6 +55,31 @@ Range range_of(const View &v, int B, int d) { return range_of(v.p, B, v.H, v.N, 
 const __nv_bfloat16 *in(const View &v) { return static_cast<const __nv_bfloat16 *>(v.p); }
 __nv_bfloat16 *out(const View &v) { return const_cast<__nv_bfloat16 *>(in(v)); }
 
+// A call's workspace: the caller's, or taken on the stream for the call.
+struct Scratch {
+  void *ptr;
+  size_t bytes, need;
+  bool owned = false;
+  Scratch(void *workspace, size_t workspace_bytes, size_t need_bytes)
+      : ptr(need_bytes ? workspace : nullptr), bytes(workspace_bytes), need(need_bytes) {}
+  // The caller's: large enough, aligned, apart from the call's other memory.
+  fa_status_t check(const Range *used, int n) const {
+    if (!ptr) return FA_OK;
+    if (bytes < need) return FA_ERR_WORKSPACE;
+    if (reinterpret_cast<uintptr_t>(ptr) & 255u) return FA_ERR_INVALID_ARGUMENT;
+    const Range r = range_of(ptr, static_cast<long long>(need));
+    for (int i = 0; i < n; ++i)
+      if (meet(r, used[i])) return FA_ERR_INVALID_ARGUMENT;
+    return FA_OK;
+  }
+  bool take(cudaStream_t stream) {
+    if (!need || ptr) return true;
+    owned = cudaMallocAsync(&ptr, need, stream) == cudaSuccess;
+    return owned;
+  }
+  bool give_back(cudaStream_t stream) { return !owned || cudaFreeAsync(ptr, stream) == cudaSuccess; }
+};
+
 fa_status_t check_d(int d) {
   if (d == 64 || d == 128) return FA_OK;
   return d < 1 ? FA_ERR_INVALID_ARGUMENT : FA_ERR_UNSUPPORTED;
@@ -283,7 +308,8 @@ fa_status_t fa_rope_append(const void *q, const int64_t *q_strides, const void *
 
 size_t fa_tree_workspace_bytes(int B, int H, int Hkv, int Nt, int Nk, int d) {
   if (check_tree(B, H, Hkv, Nt, Nk, d, 1.0f) != FA_OK) return 0;
-  return 0;
+  const TreePlan pl = plan_tree(B, H, Hkv, Nt, Nk);
+  return pl.merge ? round256(pl.part_rows * d * 4) + round256(pl.part_rows * 4) : 0;
 }
 
 fa_status_t fa_fwd_tree(const void *q, const int64_t *q_strides, const void *k, const int64_t *k_strides,
@@ -307,21 +333,28 @@ fa_status_t fa_fwd_tree(const void *q, const int64_t *q_strides, const void *k, 
   if (meet(rl, ro) || meet(par, ro) || meet(len, ro) || meet(par, rl) || meet(len, rl) ||
       meet(range_of(vq, B, d), rl) || meet(range_of(vk, B, d), rl) || meet(range_of(vv, B, d), rl))
     return FA_ERR_INVALID_ARGUMENT;
+  const TreePlan pl = plan_tree(B, H, Hkv, Nt, Nk);
+  const size_t need = fa_tree_workspace_bytes(B, H, Hkv, Nt, Nk, d);
+  Scratch ws(workspace, workspace_bytes, need);
+  const Range used[7] = {range_of(vq, B, d), range_of(vk, B, d), range_of(vv, B, d), ro, rl, par, len};
+  const fa_status_t wst = ws.check(used, 7);
+  if (wst != FA_OK) return wst;
+  CUtensorMap tq, tk, tv;
+  if (!encode_map(&tq, q, B, H, Nt, d, vq.s, Nt, pl.gpt) || !encode_map(&tk, k, B, Hkv, Nk, d, vk.s) ||
+      !encode_map(&tv, v, B, Hkv, Nk, d, vv.s))
+    return FA_ERR_CUDA;
   TreeParams p{};
-  p.q = in(vq);
-  p.k = in(vk);
-  p.v = in(vv);
+  p.status = status_ptr();
+  if (!p.status || !ws.take(stream)) return FA_ERR_CUDA;
   p.o = out(vo);
   p.lse = lse;
-  p.sq = vq.s;
-  p.sk = vk.s;
-  p.sv = vv.s;
   p.so = vo.s;
   p.parents = parents;
   p.par_b = parents_stride;
   p.cache_len = cache_seqlens;
-  p.status = status_ptr();
-  if (!p.status) return FA_ERR_CUDA;
+  p.part_o = static_cast<float *>(ws.ptr);
+  p.part_lse = need ? reinterpret_cast<float *>(static_cast<uint8_t *>(ws.ptr) + round256(pl.part_rows * d * 4))
+                    : nullptr;
   p.B = B;
   p.H = H;
   p.Hkv = Hkv;
@@ -329,9 +362,15 @@ fa_status_t fa_fwd_tree(const void *q, const int64_t *q_strides, const void *k, 
   p.Nt = Nt;
   p.Nk = Nk;
   p.d = d;
+  p.gpt = pl.gpt;
+  p.row_tiles = pl.row_tiles;
+  p.groups = pl.groups;
+  p.ranges = pl.ranges;
+  p.split = pl.split;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.neg = scale < 0.0f ? 1 : 0;
-  return launch_tree(p, stream) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  const bool launched = launch_tree(tq, tk, tv, p, pl.merge, stream) == cudaSuccess;
+  return ws.give_back(stream) && launched ? FA_OK : FA_ERR_CUDA;
 }
 
 size_t fa_key_weights_workspace_bytes(int B, int H, int Hkv, int Nq, int Nk, int d) {

@@ -30,6 +30,8 @@ enum WaitSite : int {
   kSiteMmaDone,
   kSiteKvEmpty,
   kSiteQEmpty,
+  kSiteMaskFull,
+  kSiteMaskEmpty,
 };
 
 // Element strides of a [B, H, N, d] bf16 tensor whose d elements are
