@@ -63,19 +63,34 @@ TreePlan plan_tree(int B, int H, int Hkv, int Nt, int Nk);
 cudaError_t launch_tree(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const TreeParams &p,
                         bool merge, cudaStream_t stream);
 
-// Accumulated attention weight per key.
+// Accumulated attention weight per key.  A unit is a block of 256 keys of one
+// cache head; the query rows of the head's group come in column tiles: whole
+// heads packed together (`gpt` heads of Nq rows) or, for Nq > 128, 128 rows
+// of one head.  With splits > 1 each unit's column tiles are dealt to that
+// many units whose partial sums a second kernel adds.
 struct KeyWeightParams {
-  const __nv_bfloat16 *q, *k;
   const float *lse;           // [B, H, Nq] contiguous
   const float *w_in;          // [B, Hkv, Nk] or null
   float *w;
-  Strides sq, sk;
+  float *part;                // [splits][B, Hkv, Nk] (splits > 1)
   const int *cache_len;       // [B] or null
   int *status;
-  int B, H, Hkv, G, Nq, Nk, d, causal;
+  int B, H, Hkv, G, Nq, Nk, causal;
+  int gpt, tiles_per_head, head_groups;  // tiles of a head group; groups of gpt heads
+  int splits;
+  long long units;            // B * Hkv * ceil(Nk / 256) * splits
   float scale_log2;
 };
-cudaError_t launch_key_weights(const KeyWeightParams &p, cudaStream_t stream);
+
+struct KeyWeightPlan {
+  int cols;                   // columns of a tile: 16, 32, 64 or 128
+  int box_rows, gpt, tiles_per_head, head_groups, splits;
+};
+KeyWeightPlan plan_key_weights(int B, int H, int Hkv, int Nq, int Nk);
+
+// tq: q with boxes of box_rows rows x gpt heads.
+cudaError_t launch_key_weights(int d, int cols, const CUtensorMap &tq, const CUtensorMap &tk,
+                               const KeyWeightParams &p, int sms, cudaStream_t stream);
 
 // Rows to keep of each cache: ascending row numbers, -1 behind them.
 struct SelectParams {

@@ -375,7 +375,8 @@ fa_status_t fa_fwd_tree(const void *q, const int64_t *q_strides, const void *k, 
 
 size_t fa_key_weights_workspace_bytes(int B, int H, int Hkv, int Nq, int Nk, int d) {
   if (check_key_weights(B, H, Hkv, Nq, Nk, d, 0, 1.0f) != FA_OK) return 0;
-  return 0;
+  const KeyWeightPlan pl = plan_key_weights(B, H, Hkv, Nq, Nk);
+  return pl.splits > 1 ? round256(static_cast<size_t>(pl.splits) * B * Hkv * Nk * 4) : 0;
 }
 
 fa_status_t fa_key_weights(const void *q, const int64_t *q_strides, const void *k, const int64_t *k_strides,
@@ -394,27 +395,40 @@ fa_status_t fa_key_weights(const void *q, const int64_t *q_strides, const void *
   if (meet(rw, range_of(vq, B, d)) || meet(rw, range_of(vk, B, d)) || meet(rw, range_of(lse, 4ll * B * H * Nq)) ||
       meet(rw, range_of(cache_seqlens, 4ll * B)) || (weights_in != weights && meet(rw, range_of(weights_in, wbytes))))
     return FA_ERR_INVALID_ARGUMENT;
+  const KeyWeightPlan pl = plan_key_weights(B, H, Hkv, Nq, Nk);
+  Scratch ws(workspace, workspace_bytes, fa_key_weights_workspace_bytes(B, H, Hkv, Nq, Nk, d));
+  const Range used[6] = {range_of(vq, B, d), range_of(vk, B, d), range_of(lse, 4ll * B * H * Nq), rw,
+                         range_of(weights_in, wbytes), range_of(cache_seqlens, 4ll * B)};
+  const fa_status_t wst = ws.check(used, 6);
+  if (wst != FA_OK) return wst;
+  const int sms = sm_count();
+  CUtensorMap tq, tk;
+  if (sms <= 0 || !encode_map(&tq, q, B, H, Nq, d, vq.s, pl.box_rows, pl.gpt) ||
+      !encode_map(&tk, k, B, Hkv, Nk, d, vk.s))
+    return FA_ERR_CUDA;
   KeyWeightParams p{};
-  p.q = in(vq);
-  p.k = in(vk);
+  p.status = status_ptr();
+  if (!p.status || !ws.take(stream)) return FA_ERR_CUDA;
   p.lse = lse;
   p.w_in = weights_in;
   p.w = weights;
-  p.sq = vq.s;
-  p.sk = vk.s;
+  p.part = static_cast<float *>(ws.ptr);
   p.cache_len = cache_seqlens;
-  p.status = status_ptr();
-  if (!p.status) return FA_ERR_CUDA;
   p.B = B;
   p.H = H;
   p.Hkv = Hkv;
   p.G = H / Hkv;
   p.Nq = Nq;
   p.Nk = Nk;
-  p.d = d;
   p.causal = causal;
+  p.gpt = pl.gpt;
+  p.tiles_per_head = pl.tiles_per_head;
+  p.head_groups = pl.head_groups;
+  p.splits = pl.splits;
+  p.units = static_cast<long long>(B) * Hkv * ((Nk + 255) / 256) * pl.splits;
   p.scale_log2 = scale * 1.4426950408889634f;
-  return launch_key_weights(p, stream) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  const bool launched = launch_key_weights(d, pl.cols, tq, tk, p, sms, stream) == cudaSuccess;
+  return ws.give_back(stream) && launched ? FA_OK : FA_ERR_CUDA;
 }
 
 fa_status_t fa_cache_select(const float *weights, const int *cache_seqlens, int *kept, int *new_seqlens, int B,

@@ -32,6 +32,8 @@ enum WaitSite : int {
   kSiteQEmpty,
   kSiteMaskFull,
   kSiteMaskEmpty,
+  kSiteLseFull,
+  kSiteLseEmpty,
 };
 
 // Element strides of a [B, H, N, d] bf16 tensor whose d elements are
