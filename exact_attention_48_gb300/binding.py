@@ -40,6 +40,8 @@ class FaError(RuntimeError):
 def library(path: str | None = None):
     """Load (once) and return the ctypes handle of libfa.so."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             p = path or LIB
@@ -85,24 +87,24 @@ def library(path: str | None = None):
             lib.fa_rope_frequencies.argtypes = [vp, vp, i, dbl, i, dbl, i, dbl, dbl]
             lib.fa_rope_frequencies.restype = i
             for name in ("fa_rope", "fa_rope_bwd"):
-                getattr(lib, name).argtypes = [vp, p64, vp, p64, vp, p64, vp, p64, vp, i64, vp, i, i, i, i, i, i, i, f,
+                getattr(lib, name).argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, vp, i, i, i, i, i, i, i, f,
                                                vp]
                 getattr(lib, name).restype = i
-            lib.fa_rope_append.argtypes = [vp, p64, vp, p64, vp, p64, vp, p64, vp, p64, vp, p64, vp, vp, i64, vp,
+            lib.fa_rope_append.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, vp,
                                            i, i, i, i, i, i, i, i, f, vp]
             lib.fa_rope_append.restype = i
             lib.fa_tree_workspace_bytes.argtypes = [i, i, i, i, i, i]
             lib.fa_tree_workspace_bytes.restype = sz
-            lib.fa_fwd_tree.argtypes = [vp, p64, vp, p64, vp, p64, vp, p64, vp, vp, i64, vp, i, i, i, i, i, i, f, vp,
+            lib.fa_fwd_tree.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, vp, i, i, i, i, i, i, f, vp,
                                         sz, vp]
             lib.fa_fwd_tree.restype = i
             lib.fa_key_weights_workspace_bytes.argtypes = [i, i, i, i, i, i]
             lib.fa_key_weights_workspace_bytes.restype = sz
-            lib.fa_key_weights.argtypes = [vp, p64, vp, p64, vp, vp, vp, vp, i, i, i, i, i, i, i, f, vp, sz, vp]
+            lib.fa_key_weights.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, f, vp, sz, vp]
             lib.fa_key_weights.restype = i
             lib.fa_cache_select.argtypes = [vp, vp, vp, vp, i, i, i, i, i, i, vp]
             lib.fa_cache_select.restype = i
-            lib.fa_cache_compact.argtypes = [vp, p64, vp, p64, vp, vp, p64, vp, p64, vp, vp, i64, i64, vp,
+            lib.fa_cache_compact.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, vp,
                                              i, i, i, i, i, i, vp]
             lib.fa_cache_compact.restype = i
             lib.fa_status_string.argtypes = [i]

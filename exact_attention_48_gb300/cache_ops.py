@@ -9,76 +9,96 @@ belong to that stream.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import functools
 import math
 
 import torch
 
-from .binding import FA_OK, FaError, _check_view, library
+from .binding import FA_OK, FaError, library
 
 ROPE_SCALING = {"plain": 0, "linear": 1, "base": 2, "by_parts": 3}
+
+# A decode step makes these calls per layer and token, so the checks are kept
+# lean: one stride() per tensor, stride arrays built once per layout, and the
+# raw stream handle instead of a Stream object.
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 @functools.lru_cache(maxsize=4096)
 def _c_strides(strides):
-    return (ctypes.c_int64 * 3)(*strides)
+    """Address of the first three strides as int64, and the array that holds them."""
+    a = (ctypes.c_int64 * 3)(*strides[:3])
+    return ctypes.addressof(a), a
 
 
-def _strides(t):
-    return _c_strides(t.stride()[:3])
+def _view(name, t, dev=None, shape=None):
+    """A [B, H, N, d] bf16 view with contiguous d: its pointer and strides."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name} must be bfloat16, got {t.dtype}")
+    st = t.stride()
+    if len(st) != 4 or st[3] != 1:
+        raise ValueError(f"{name} must be a [B, H, N, d] view with contiguous d")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if dev is not None and t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    return t.data_ptr(), _c_strides(st)
 
 
-def _check_plain(name, t, dtype, shape, device):
-    """A contiguous tensor of the given type, shape and device."""
-    if not isinstance(t, torch.Tensor) or t.device != device or t.dtype != dtype or tuple(t.shape) != tuple(shape) \
+def _plain(name, t, dtype, shape, dev):
+    """A contiguous tensor of the given type, shape and device: its pointer."""
+    if not isinstance(t, torch.Tensor) or t.device != dev or t.dtype is not dtype or t.shape != shape \
             or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on {device}")
-    return t
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on {dev}")
+    return t.data_ptr()
 
 
-def _check_views(device, **views):
-    for name, (t, shape) in views.items():
-        _check_view(name, t, shape)
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
-
-
-def _row_ints(name, t, B, N, device):
+def _row_ints(name, t, B, N, dev):
     """int32 [B, N] (any batch stride) or [N] (shared by the batch): pointer and batch stride."""
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.device != device:
-        raise ValueError(f"{name} must be an int32 tensor on {device}")
-    if tuple(t.shape) not in ((B, N), (N,)) or (N > 1 and t.stride(-1) != 1):
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.device != dev:
+        raise ValueError(f"{name} must be an int32 tensor on {dev}")
+    if t.shape not in ((B, N), (N,)) or (N > 1 and t.stride(-1) != 1):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({B}, {N}) or ({N},) with contiguous rows")
     return t.data_ptr(), t.stride(0) if t.dim() == 2 and B > 1 else 0
 
 
-def _lens(t, B, device):
-    return None if t is None else _check_plain("cache_seqlens", t, torch.int32, (B,), device).data_ptr()
+def _lens(t, B, dev):
+    return None if t is None else _plain("cache_seqlens", t, torch.int32, (B,), dev)
 
 
-def _workspace(t, device):
+def _table(inv_freq, dev):
+    """Pointer of the frequency table and the columns it turns."""
+    if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be an fp32 tensor [rot / 2]")
+    n = inv_freq.shape[0]
+    return _plain("inv_freq", inv_freq, torch.float32, (n,), dev), 2 * n
+
+
+def _workspace(t, need, like):
+    """The caller's workspace, or one from PyTorch's allocator (on the launching stream): pointer, bytes, owner."""
     if t is None:
-        return None, 0
-    if not isinstance(t, torch.Tensor) or t.device != device or not t.is_contiguous():
+        if not need:
+            return None, 0, None
+        t = like.new_empty(need, dtype=torch.uint8)
+    elif not isinstance(t, torch.Tensor) or t.device != like.device or not t.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
-    return t.data_ptr(), t.numel() * t.element_size()
+    return t.data_ptr(), t.numel() * t.element_size(), t
 
 
-@contextlib.contextmanager
-def _on(device, stream):
-    """The tensors' device made current, and the stream (its handle) that outputs are allocated for."""
-    if stream is not None and stream.device != device:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-    with contextlib.ExitStack() as stack:
-        if torch.cuda.current_device() != device.index:
-            stack.enter_context(torch.cuda.device(device))
-        if stream is not None:
-            stack.enter_context(torch.cuda.stream(stream))
-        else:
-            stream = torch.cuda.current_stream(device)
-        yield int(stream.cuda_stream)
+def _on(dev, stream, body):
+    """body(stream handle) with the tensors' device current and outputs allocated for that stream."""
+    if stream is None:
+        if dev.index == torch.cuda.current_device():
+            return body(_raw_stream(dev.index))
+        with torch.cuda.device(dev):
+            return body(_raw_stream(dev.index))
+    if stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+    with torch.cuda.stream(stream):
+        return body(int(stream.cuda_stream))
 
 
 def _done(rc, where):
@@ -86,14 +106,12 @@ def _done(rc, where):
         raise FaError(rc, where)
 
 
-def _heads(q, k, names=("q", "k")):
-    """Shapes of grouped queries against a cache: B, H, Nq, d, Hkv, Nk."""
-    _check_view(names[0], q)
-    _check_view(names[1], k)
+def _heads(q, k):
+    """Shapes of grouped queries q against a cache k."""
     B, H, Nq, d = q.shape
-    Hkv, Nk = k.shape[1], k.shape[2]
-    if k.shape[0] != B or k.shape[3] != d:
-        raise ValueError(f"{names[1]} has shape {tuple(k.shape)}, expected ({B}, Hkv, Nk, {d})")
+    Bk, Hkv, Nk, dk = k.shape
+    if Bk != B or dk != d:
+        raise ValueError(f"k has shape {tuple(k.shape)}, expected ({B}, Hkv, Nk, {d})")
     if Hkv < 1 or H % Hkv:
         raise ValueError(f"{H} query heads cannot share {Hkv} cache heads")
     return B, H, Nq, d, Hkv, Nk
@@ -117,32 +135,32 @@ def fa_rope_frequencies(rot: int, base: float = 10000.0, scaling: str = "plain",
 
 
 def _rope(where, names, q, k, inv_freq, positions, interleaved, factor, q_out, k_out, stream):
-    _check_view(names[0], q)
-    B, H, N, d = q.shape
-    dev, Hkv = q.device, 0
+    qp, qs = _view(names[0], q)
+    shape = q.shape
+    B, H, N, d = shape
+    dev, Hkv, kp, ks = q.device, 0, None, (None, None)
     if k is not None:
-        _check_view(names[1], k)
+        kp, ks = _view(names[1], k, dev)
         Hkv = k.shape[1]
-        _check_views(dev, **{names[1]: (k, (B, Hkv, N, d))})
+        if k.shape != (B, Hkv, N, d):
+            raise ValueError(f"{names[1]} has shape {tuple(k.shape)}, expected ({B}, Hkv, {N}, {d})")
     elif k_out is not None:
         raise ValueError(f"{names[3]} given without {names[1]}")
-    if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
-        raise ValueError("inv_freq must be an fp32 tensor [rot / 2]")
-    rot = 2 * inv_freq.shape[0]
-    _check_plain("inv_freq", inv_freq, torch.float32, (rot // 2,), dev)
+    freq, rot = _table(inv_freq, dev)
     pos, pos_b = (None, 0) if positions is None else _row_ints("positions", positions, B, N, dev)
-    with _on(dev, stream) as handle:
-        q_out = torch.empty(q.shape, device=dev, dtype=q.dtype) if q_out is None else q_out
-        _check_views(dev, **{names[2]: (q_out, q.shape)})
-        kp = kop = ks = kos = None
+
+    def run(handle):
+        qo = q.new_empty(shape) if q_out is None else q_out
+        qop, qos = _view(names[2], qo, dev, shape)
+        ko, kop, kos = k_out, None, (None, None)
         if k is not None:
-            k_out = torch.empty(k.shape, device=dev, dtype=k.dtype) if k_out is None else k_out
-            _check_views(dev, **{names[3]: (k_out, k.shape)})
-            kp, ks, kop, kos = k.data_ptr(), _strides(k), k_out.data_ptr(), _strides(k_out)
-        _done(getattr(library(), where)(q.data_ptr(), _strides(q), kp, ks, q_out.data_ptr(), _strides(q_out), kop, kos,
-                                        pos, pos_b, inv_freq.data_ptr(), B, H, Hkv, N, d, rot, int(bool(interleaved)),
-                                        float(factor), handle), where)
-    return q_out, k_out
+            ko = k.new_empty(k.shape) if ko is None else ko
+            kop, kos = _view(names[3], ko, dev, k.shape)
+        _done(getattr(library(), where)(qp, qs[0], kp, ks[0], qop, qos[0], kop, kos[0], pos, pos_b, freq, B, H, Hkv, N,
+                                        d, rot, 1 if interleaved else 0, factor, handle), where)
+        return qo, ko
+
+    return _on(dev, stream, run)
 
 
 def fa_rope(q, k, inv_freq, positions=None, interleaved: bool = False, factor: float = 1.0, q_out=None, k_out=None,
@@ -171,29 +189,30 @@ def fa_rope_append(q, k, v, k_cache, v_cache, cache_seqlens, inv_freq, positions
     ``q_out=q`` in place), k [B, Hkv, N, d] rotated into k_cache and v copied
     into v_cache [B, Hkv, Nk, d], at the last N of the cache_seqlens[b] rows
     (int32 [B], the new rows counted).  positions default to those rows."""
-    _check_view("q", q)
-    B, H, N, d = q.shape
-    dev = q.device
-    _check_view("k", k)
-    _check_view("k_cache", k_cache)
+    qp, qs = _view("q", q)
+    shape, dev = q.shape, q.device
+    B, H, N, d = shape
+    kp, ks = _view("k", k, dev)
+    kcp, kcs = _view("k_cache", k_cache, dev)
     Hkv, Nk = k.shape[1], k_cache.shape[2]
-    _check_views(dev, k=(k, (B, Hkv, N, d)), v=(v, (B, Hkv, N, d)), k_cache=(k_cache, (B, Hkv, Nk, d)),
-                 v_cache=(v_cache, (B, Hkv, Nk, d)))
-    if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
-        raise ValueError("inv_freq must be an fp32 tensor [rot / 2]")
-    rot = 2 * inv_freq.shape[0]
-    _check_plain("inv_freq", inv_freq, torch.float32, (rot // 2,), dev)
-    _check_plain("cache_seqlens", cache_seqlens, torch.int32, (B,), dev)
+    if k.shape != (B, Hkv, N, d) or k_cache.shape != (B, Hkv, Nk, d):
+        raise ValueError(f"k and k_cache have shapes {tuple(k.shape)} and {tuple(k_cache.shape)}, expected ({B}, Hkv, "
+                         f"{N}, {d}) and ({B}, Hkv, Nk, {d})")
+    vp, vs = _view("v", v, dev, k.shape)
+    vcp, vcs = _view("v_cache", v_cache, dev, k_cache.shape)
+    freq, rot = _table(inv_freq, dev)
+    lens = _plain("cache_seqlens", cache_seqlens, torch.int32, (B,), dev)
     pos, pos_b = (None, 0) if positions is None else _row_ints("positions", positions, B, N, dev)
-    with _on(dev, stream) as handle:
-        q_out = torch.empty(q.shape, device=dev, dtype=q.dtype) if q_out is None else q_out
-        _check_views(dev, q_out=(q_out, q.shape))
-        _done(library().fa_rope_append(
-            q.data_ptr(), _strides(q), k.data_ptr(), _strides(k), v.data_ptr(), _strides(v), q_out.data_ptr(),
-            _strides(q_out), k_cache.data_ptr(), _strides(k_cache), v_cache.data_ptr(), _strides(v_cache),
-            cache_seqlens.data_ptr(), pos, pos_b, inv_freq.data_ptr(), B, H, Hkv, N, Nk, d, rot,
-            int(bool(interleaved)), float(factor), handle), "fa_rope_append")
-    return q_out
+
+    def run(handle):
+        qo = q.new_empty(shape) if q_out is None else q_out
+        qop, qos = _view("q_out", qo, dev, shape)
+        _done(library().fa_rope_append(qp, qs[0], kp, ks[0], vp, vs[0], qop, qos[0], kcp, kcs[0], vcp, vcs[0], lens,
+                                       pos, pos_b, freq, B, H, Hkv, N, Nk, d, rot, 1 if interleaved else 0, factor,
+                                       handle), "fa_rope_append")
+        return qo
+
+    return _on(dev, stream, run)
 
 
 def fa_tree_workspace_bytes(B: int, H: int, Hkv: int, Nt: int, Nk: int, d: int) -> int:
@@ -209,22 +228,26 @@ def fa_fwd_tree(q, k, v, parents, cache_seqlens=None, scale: float | None = None
     the tree, anything else for padding (o = 0, lse = -inf).  A node sees the
     rows before the tree, itself and its ancestors.  Returns (o [B, H, Nt, d]
     bf16, lse [B, H, Nt] fp32)."""
-    B, H, Nt, d, Hkv, Nk = _heads(q, k)
+    qp, qs = _view("q", q)
     dev = q.device
-    _check_views(dev, k=(k, k.shape), v=(v, k.shape))
+    kp, ks = _view("k", k, dev)
+    B, H, Nt, d, Hkv, Nk = _heads(q, k)
+    vp, vs = _view("v", v, dev, k.shape)
     par, par_b = _row_ints("parents", parents, B, Nt, dev)
     cl = _lens(cache_seqlens, B, dev)
-    scale = 1.0 / math.sqrt(d) if scale is None else scale
-    ws, ws_bytes = _workspace(workspace, dev)
-    with _on(dev, stream) as handle:
-        o = torch.empty(q.shape, device=dev, dtype=q.dtype) if o is None else o
-        _check_views(dev, o=(o, q.shape))
-        lse = torch.empty((B, H, Nt), device=dev, dtype=torch.float32) if lse is None else lse
-        _check_plain("lse", lse, torch.float32, (B, H, Nt), dev)
-        _done(library().fa_fwd_tree(q.data_ptr(), _strides(q), k.data_ptr(), _strides(k), v.data_ptr(), _strides(v),
-                                    o.data_ptr(), _strides(o), lse.data_ptr(), par, par_b, cl, B, H, Hkv, Nt, Nk, d,
-                                    float(scale), ws, ws_bytes, handle), "fa_fwd_tree")
-    return o, lse
+
+    def run(handle):
+        out = q.new_empty(q.shape) if o is None else o
+        op, os_ = _view("o", out, dev, q.shape)
+        ls = q.new_empty((B, H, Nt), dtype=torch.float32) if lse is None else lse
+        lp = _plain("lse", ls, torch.float32, (B, H, Nt), dev)
+        lib = library()
+        ws, ws_bytes, own = _workspace(workspace, lib.fa_tree_workspace_bytes(B, H, Hkv, Nt, Nk, d), q)
+        _done(lib.fa_fwd_tree(qp, qs[0], kp, ks[0], vp, vs[0], op, os_[0], lp, par, par_b, cl, B, H, Hkv, Nt, Nk, d,
+                              1.0 / math.sqrt(d) if scale is None else scale, ws, ws_bytes, handle), "fa_fwd_tree")
+        return out, ls
+
+    return _on(dev, stream, run)
 
 
 def fa_key_weights_workspace_bytes(B: int, H: int, Hkv: int, Nq: int, Nk: int, d: int) -> int:
@@ -238,23 +261,26 @@ def fa_key_weights(q, k, lse, cache_seqlens=None, causal: bool = False, scale: f
     sum over the query rows q [B, H, Nq, d] that see j (the last Nq
     positions; causal: up to their own) and the heads that share the cache
     head of exp(scale q.k_j - lse).  ``weights=weights_in`` adds in place."""
-    B, H, Nq, d, Hkv, Nk = _heads(q, k)
+    qp, qs = _view("q", q)
     dev = q.device
-    _check_views(dev, k=(k, k.shape))
-    _check_plain("lse", lse, torch.float32, (B, H, Nq), dev)
+    kp, ks = _view("k", k, dev)
+    B, H, Nq, d, Hkv, Nk = _heads(q, k)
+    lp = _plain("lse", lse, torch.float32, (B, H, Nq), dev)
     cl = _lens(cache_seqlens, B, dev)
-    if weights_in is not None:
-        _check_plain("weights_in", weights_in, torch.float32, (B, Hkv, Nk), dev)
-    scale = 1.0 / math.sqrt(d) if scale is None else scale
-    ws, ws_bytes = _workspace(workspace, dev)
-    with _on(dev, stream) as handle:
-        weights = torch.empty((B, Hkv, Nk), device=dev, dtype=torch.float32) if weights is None else weights
-        _check_plain("weights", weights, torch.float32, (B, Hkv, Nk), dev)
-        _done(library().fa_key_weights(q.data_ptr(), _strides(q), k.data_ptr(), _strides(k), lse.data_ptr(),
-                                       None if weights_in is None else weights_in.data_ptr(), weights.data_ptr(), cl,
-                                       B, H, Hkv, Nq, Nk, d, int(bool(causal)), float(scale), ws, ws_bytes, handle),
+    shape = (B, Hkv, Nk)
+    wi = None if weights_in is None else _plain("weights_in", weights_in, torch.float32, shape, dev)
+
+    def run(handle):
+        w = lse.new_empty(shape) if weights is None else weights
+        wp = _plain("weights", w, torch.float32, shape, dev)
+        lib = library()
+        ws, ws_bytes, own = _workspace(workspace, lib.fa_key_weights_workspace_bytes(B, H, Hkv, Nq, Nk, d), q)
+        _done(lib.fa_key_weights(qp, qs[0], kp, ks[0], lp, wi, wp, cl, B, H, Hkv, Nq, Nk, d, 1 if causal else 0,
+                                 1.0 / math.sqrt(d) if scale is None else scale, ws, ws_bytes, handle),
               "fa_key_weights")
-    return weights
+        return w
+
+    return _on(dev, stream, run)
 
 
 def fa_cache_select(weights, keep: int, cache_seqlens=None, first: int = 0, recent: int = 0, kept=None,
@@ -268,18 +294,20 @@ def fa_cache_select(weights, keep: int, cache_seqlens=None, first: int = 0, rece
         raise TypeError("weights must be an fp32 CUDA tensor [B, Hkv, Nk]")
     B, Hkv, Nk = weights.shape
     dev, keep = weights.device, int(keep)
-    _check_plain("weights", weights, torch.float32, (B, Hkv, Nk), dev)
+    wp = _plain("weights", weights, torch.float32, (B, Hkv, Nk), dev)
     cl = _lens(cache_seqlens, B, dev)
     if not 1 <= keep <= Nk:
         raise ValueError(f"keep must be in [1, {Nk}], got {keep}")
-    with _on(dev, stream) as handle:
-        kept = torch.empty((B, Hkv, keep), device=dev, dtype=torch.int32) if kept is None else kept
-        _check_plain("kept", kept, torch.int32, (B, Hkv, keep), dev)
-        new_seqlens = torch.empty(B, device=dev, dtype=torch.int32) if new_seqlens is None else new_seqlens
-        _check_plain("new_seqlens", new_seqlens, torch.int32, (B,), dev)
-        _done(library().fa_cache_select(weights.data_ptr(), cl, kept.data_ptr(), new_seqlens.data_ptr(), B, Hkv, Nk,
-                                        keep, int(first), int(recent), handle), "fa_cache_select")
-    return kept, new_seqlens
+
+    def run(handle):
+        rows = weights.new_empty((B, Hkv, keep), dtype=torch.int32) if kept is None else kept
+        lens = weights.new_empty((B,), dtype=torch.int32) if new_seqlens is None else new_seqlens
+        _done(library().fa_cache_select(wp, cl, _plain("kept", rows, torch.int32, (B, Hkv, keep), dev),
+                                        _plain("new_seqlens", lens, torch.int32, (B,), dev), B, Hkv, Nk, keep, first,
+                                        recent, handle), "fa_cache_select")
+        return rows, lens
+
+    return _on(dev, stream, run)
 
 
 def fa_cache_compact(k, v, kept, weights=None, base=None, k_out=None, v_out=None, weights_out=None, stream=None):
@@ -289,30 +317,35 @@ def fa_cache_compact(k, v, kept, weights=None, base=None, k_out=None, v_out=None
     [B, Hkv, M], or [B, M] for all heads.  Without outputs the cache is
     changed in place (the entries must then ascend, none below its place).
     Returns (k_out, v_out, weights_out)."""
-    _check_view("k", k)
+    kp, ks = _view("k", k)
     B, Hkv, Nk, d = k.shape
     dev = k.device
-    _check_views(dev, v=(v, k.shape))
+    vp, vs = _view("v", v, dev, k.shape)
     if k_out is None and v_out is None and weights_out is None:
         k_out, v_out, weights_out = k, v, weights
     if k_out is None or v_out is None or (weights is None) != (weights_out is None):
         raise ValueError("give all outputs (weights_out exactly if weights is given) or none")
-    _check_view("k_out", k_out)
+    kop, kos = _view("k_out", k_out, dev)
     Nout = k_out.shape[2]
-    _check_views(dev, k_out=(k_out, (B, Hkv, Nout, d)), v_out=(v_out, (B, Hkv, Nout, d)))
+    if k_out.shape != (B, Hkv, Nout, d):
+        raise ValueError(f"k_out has shape {tuple(k_out.shape)}, expected ({B}, {Hkv}, Nk_out, {d})")
+    vop, vos = _view("v_out", v_out, dev, k_out.shape)
     wi = wo = None
     if weights is not None:
-        wi = _check_plain("weights", weights, torch.float32, (B, Hkv, Nk), dev).data_ptr()
-        wo = _check_plain("weights_out", weights_out, torch.float32, (B, Hkv, Nout), dev).data_ptr()
-    if not isinstance(kept, torch.Tensor) or kept.dtype != torch.int32 or kept.device != dev or kept.dim() not in (2, 3):
+        wi = _plain("weights", weights, torch.float32, (B, Hkv, Nk), dev)
+        wo = _plain("weights_out", weights_out, torch.float32, (B, Hkv, Nout), dev)
+    if not isinstance(kept, torch.Tensor) or kept.dtype is not torch.int32 or kept.device != dev \
+            or kept.dim() not in (2, 3):
         raise ValueError("kept must be an int32 tensor [B, Hkv, M] or [B, M]")
-    M = kept.shape[-1]
-    if tuple(kept.shape) not in ((B, Hkv, M), (B, M)) or (M > 1 and kept.stride(-1) != 1):
+    st, M = kept.stride(), kept.shape[-1]
+    if kept.shape not in ((B, Hkv, M), (B, M)) or (M > 1 and st[-1] != 1):
         raise ValueError(f"kept has shape {tuple(kept.shape)}, expected ({B}, {Hkv}, M) or ({B}, M), contiguous lists")
-    kb, kh = kept.stride(0), kept.stride(1) if kept.dim() == 3 else 0
-    bp = None if base is None else _check_plain("base", base, torch.int32, (B,), dev).data_ptr()
-    with _on(dev, stream) as handle:
-        _done(library().fa_cache_compact(k.data_ptr(), _strides(k), v.data_ptr(), _strides(v), wi, k_out.data_ptr(),
-                                         _strides(k_out), v_out.data_ptr(), _strides(v_out), wo, kept.data_ptr(), kb,
-                                         kh, bp, B, Hkv, Nk, Nout, M, d, handle), "fa_cache_compact")
-    return k_out, v_out, weights_out
+    bp = None if base is None else _plain("base", base, torch.int32, (B,), dev)
+
+    def run(handle):
+        _done(library().fa_cache_compact(kp, ks[0], vp, vs[0], wi, kop, kos[0], vop, vos[0], wo, kept.data_ptr(),
+                                         st[0], st[1] if len(st) == 3 else 0, bp, B, Hkv, Nk, Nout, M, d, handle),
+              "fa_cache_compact")
+        return k_out, v_out, weights_out
+
+    return _on(dev, stream, run)
