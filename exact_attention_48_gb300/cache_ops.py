@@ -77,12 +77,16 @@ def _table(inv_freq, dev):
     return _plain("inv_freq", inv_freq, torch.float32, (n,), dev), 2 * n
 
 
+def _empty(shape, dtype, dev):
+    return torch.empty(shape, dtype=dtype, device=dev)
+
+
 def _workspace(t, need, like):
     """The caller's workspace, or one from PyTorch's allocator (on the launching stream): pointer, bytes, owner."""
     if t is None:
         if not need:
             return None, 0, None
-        t = like.new_empty(need, dtype=torch.uint8)
+        t = _empty(need, torch.uint8, like.device)
     elif not isinstance(t, torch.Tensor) or t.device != like.device or not t.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
     return t.data_ptr(), t.numel() * t.element_size(), t
@@ -150,11 +154,11 @@ def _rope(where, names, q, k, inv_freq, positions, interleaved, factor, q_out, k
     pos, pos_b = (None, 0) if positions is None else _row_ints("positions", positions, B, N, dev)
 
     def run(handle):
-        qo = q.new_empty(shape) if q_out is None else q_out
+        qo = _empty(shape, torch.bfloat16, dev) if q_out is None else q_out
         qop, qos = _view(names[2], qo, dev, shape)
         ko, kop, kos = k_out, None, (None, None)
         if k is not None:
-            ko = k.new_empty(k.shape) if ko is None else ko
+            ko = _empty(k.shape, torch.bfloat16, dev) if ko is None else ko
             kop, kos = _view(names[3], ko, dev, k.shape)
         _done(getattr(library(), where)(qp, qs[0], kp, ks[0], qop, qos[0], kop, kos[0], pos, pos_b, freq, B, H, Hkv, N,
                                         d, rot, 1 if interleaved else 0, factor, handle), where)
@@ -205,7 +209,7 @@ def fa_rope_append(q, k, v, k_cache, v_cache, cache_seqlens, inv_freq, positions
     pos, pos_b = (None, 0) if positions is None else _row_ints("positions", positions, B, N, dev)
 
     def run(handle):
-        qo = q.new_empty(shape) if q_out is None else q_out
+        qo = _empty(shape, torch.bfloat16, dev) if q_out is None else q_out
         qop, qos = _view("q_out", qo, dev, shape)
         _done(library().fa_rope_append(qp, qs[0], kp, ks[0], vp, vs[0], qop, qos[0], kcp, kcs[0], vcp, vcs[0], lens,
                                        pos, pos_b, freq, B, H, Hkv, N, Nk, d, rot, 1 if interleaved else 0, factor,
@@ -237,9 +241,9 @@ def fa_fwd_tree(q, k, v, parents, cache_seqlens=None, scale: float | None = None
     cl = _lens(cache_seqlens, B, dev)
 
     def run(handle):
-        out = q.new_empty(q.shape) if o is None else o
+        out = _empty(q.shape, torch.bfloat16, dev) if o is None else o
         op, os_ = _view("o", out, dev, q.shape)
-        ls = q.new_empty((B, H, Nt), dtype=torch.float32) if lse is None else lse
+        ls = _empty((B, H, Nt), torch.float32, dev) if lse is None else lse
         lp = _plain("lse", ls, torch.float32, (B, H, Nt), dev)
         lib = library()
         ws, ws_bytes, own = _workspace(workspace, lib.fa_tree_workspace_bytes(B, H, Hkv, Nt, Nk, d), q)
@@ -271,7 +275,7 @@ def fa_key_weights(q, k, lse, cache_seqlens=None, causal: bool = False, scale: f
     wi = None if weights_in is None else _plain("weights_in", weights_in, torch.float32, shape, dev)
 
     def run(handle):
-        w = lse.new_empty(shape) if weights is None else weights
+        w = _empty(shape, torch.float32, dev) if weights is None else weights
         wp = _plain("weights", w, torch.float32, shape, dev)
         lib = library()
         ws, ws_bytes, own = _workspace(workspace, lib.fa_key_weights_workspace_bytes(B, H, Hkv, Nq, Nk, d), q)
@@ -300,8 +304,8 @@ def fa_cache_select(weights, keep: int, cache_seqlens=None, first: int = 0, rece
         raise ValueError(f"keep must be in [1, {Nk}], got {keep}")
 
     def run(handle):
-        rows = weights.new_empty((B, Hkv, keep), dtype=torch.int32) if kept is None else kept
-        lens = weights.new_empty((B,), dtype=torch.int32) if new_seqlens is None else new_seqlens
+        rows = _empty((B, Hkv, keep), torch.int32, dev) if kept is None else kept
+        lens = _empty((B,), torch.int32, dev) if new_seqlens is None else new_seqlens
         _done(library().fa_cache_select(wp, cl, _plain("kept", rows, torch.int32, (B, Hkv, keep), dev),
                                         _plain("new_seqlens", lens, torch.int32, (B,), dev), B, Hkv, Nk, keep, first,
                                         recent, handle), "fa_cache_select")

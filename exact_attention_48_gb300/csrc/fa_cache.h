@@ -22,8 +22,8 @@ struct RopeParams {
   int B, H, Hkv, N, Nk, d, rot;
   float factor;
   float sign;                 // +1 forward, -1 backward (the transposed rotation)
-  int copy_rest;              // 0: in place, the columns past rot stay where they are
   int heads;                  // H + Hkv (+ Hkv)
+  int tokens;                 // tokens of a CTA, a power of two up to 256 / (d / 16)
   int head_groups;            // CTAs along the head axis
 };
 cudaError_t launch_rope(bool interleaved, const RopeParams &p, cudaStream_t stream);

@@ -100,12 +100,19 @@ fa_status_t check_rope(int B, int H, int Hkv, int N, int d, int rot, int interle
   return FA_OK;
 }
 
-// CTAs along the head axis.
-int rope_head_groups(long long tokens, int d, int heads) {
-  const long long blocks = (tokens * (d >> 4) + 255) / 256;
-  long long groups = (152 * 16 + blocks - 1) / blocks;
-  if (groups > heads) groups = heads;
-  return groups < 1 ? 1 : (groups > 65535 ? 65535 : static_cast<int>(groups));
+// Tokens of a CTA and CTAs along the head axis: up to 8 (d = 128) or 16
+// tokens, fewer while that leaves SMs without two CTAs, then the heads cut.
+void plan_rope(RopeParams *p) {
+  const long long all = static_cast<long long>(p->B) * p->N;
+  int tokens = p->d == 128 ? 8 : 16;
+  while (tokens > 1 && all / tokens < 2 * 152) tokens /= 2;
+  const int at_once = 256 / (p->d / 16 * tokens);
+  const long long blocks = (all + tokens - 1) / tokens;
+  long long groups = (p->heads + at_once - 1) / at_once;
+  const long long want = (4 * 152 + blocks - 1) / blocks;
+  if (groups > want) groups = want;
+  p->tokens = tokens;
+  p->head_groups = groups > 65535 ? 65535 : static_cast<int>(groups);
 }
 
 fa_status_t rope_impl(const void *q, const int64_t *q_strides, const void *k, const int64_t *k_strides, void *q_out,
@@ -160,7 +167,7 @@ fa_status_t rope_impl(const void *q, const int64_t *q_strides, const void *k, co
   p.factor = factor;
   p.sign = sign;
   p.heads = H + Hkv;
-  p.head_groups = rope_head_groups(static_cast<long long>(B) * N, d, p.heads);
+  plan_rope(&p);
   return launch_rope(interleaved != 0, p, stream) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -302,7 +309,7 @@ fa_status_t fa_rope_append(const void *q, const int64_t *q_strides, const void *
   p.factor = factor;
   p.sign = 1.0f;
   p.heads = H + 2 * Hkv;
-  p.head_groups = rope_head_groups(static_cast<long long>(B) * N, d, p.heads);
+  plan_rope(&p);
   return launch_rope(interleaved != 0, p, stream) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

@@ -7,9 +7,11 @@
 // backward pass is the transposed rotation (the angle negated).
 //
 // The pass reads and writes every row once and does six flops a pair, so HBM
-// bounds it.  A thread owns eight pairs (16 columns) of one token and keeps
-// their cosines and sines in registers over the heads it walks, so the
-// angles cost once per token and head group, not once per head.
+// bounds it.  A CTA takes a few tokens and all their heads (or, with few
+// tokens, a part of the heads): its threads first share the cosines and sines
+// of those tokens out among themselves through shared memory, one angle per
+// token and pair and not per head, then each keeps the eight pairs of its
+// (token, piece) in registers over the heads it walks.
 //
 // Angles.  The product p * f has to be exact to about 2^-20 of a turn for
 // positions in the millions, which fp32 cannot hold and fp64 (a sixty-fourth
@@ -47,36 +49,6 @@ __device__ __forceinline__ uint64_t turn_fraction(float f) {
   return (bits >> 31) ? 0 - r : r;
 }
 
-// Where row (b, n) of head h comes from and goes to; false if it goes nowhere.
-struct RopeRow {
-  const __nv_bfloat16 *src;
-  __nv_bfloat16 *dst;
-  bool turn;
-};
-
-template <bool APPEND>
-__device__ __forceinline__ bool rope_row(const RopeParams &p, int h, int b, int n, int row, RopeRow *r) {
-  if (h < p.H) {
-    r->src = p.q + b * p.sq.b + h * p.sq.h + n * p.sq.n;
-    r->dst = p.qo + b * p.sqo.b + h * p.sqo.h + n * p.sqo.n;
-    r->turn = true;
-    return true;
-  }
-  if (APPEND && (row < 0 || row >= p.Nk)) return false;
-  h -= p.H;
-  if (h < p.Hkv) {
-    r->src = p.k + b * p.sk.b + h * p.sk.h + n * p.sk.n;
-    r->dst = p.ko + b * p.sko.b + h * p.sko.h + row * p.sko.n;
-    r->turn = true;
-    return true;
-  }
-  h -= p.Hkv;
-  r->src = p.v + b * p.sv.b + h * p.sv.h + n * p.sv.n;
-  r->dst = p.vo + b * p.svo.b + h * p.svo.h + row * p.svo.n;
-  r->turn = false;
-  return true;
-}
-
 __device__ __forceinline__ float2 unpack2(uint32_t u) {
   return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
 }
@@ -85,65 +57,137 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// grid: x = blocks of tokens, y = head groups (heads h = y, y + groups, ...)
+// A thread's two 16-byte pieces of a row.  Neighbouring threads take
+// neighbouring pieces, so that a warp's accesses fill whole sectors.
+struct Pieces {
+  int c0, c1;      // first columns
+  int p0, p1;      // pairs p0 .. p0 + 3 and p1 .. p1 + 3 (of the two pieces, or of both together)
+  bool t0, t1;     // the pieces turn
+};
+
+template <bool INTERLEAVED>
+__device__ __forceinline__ Pieces pieces_of(const RopeParams &p, int c) {
+  Pieces x;
+  if (INTERLEAVED) {  // a piece holds four whole pairs
+    x.c0 = c * 8;
+    x.c1 = p.d / 2 + c * 8;
+    x.p0 = x.c0 / 2;
+    x.p1 = x.c1 / 2;
+    x.t0 = x.c0 < p.rot;
+    x.t1 = x.c1 < p.rot;
+  } else if (c * 16 < p.rot) {  // the two halves of eight pairs
+    x.c0 = c * 8;
+    x.c1 = p.rot / 2 + c * 8;
+    x.p0 = c * 8;
+    x.p1 = c * 8 + 4;
+    x.t0 = x.t1 = true;
+  } else {  // two pieces past rot
+    x.c0 = p.rot + (c * 16 - p.rot) / 2;
+    x.c1 = x.c0 + (p.d - p.rot) / 2;
+    x.p0 = x.p1 = 0;
+    x.t0 = x.t1 = false;
+  }
+  return x;
+}
+
+// grid: x = blocks of `tokens` tokens, y = head groups.  Thread: piece c of
+// d / 16, token of the block, and first head.
 template <bool INTERLEAVED, bool APPEND>
 __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeParams p) {
-  const int per_row = p.d >> 4;  // threads of a row, 16 columns each
-  const int c = threadIdx.x & (per_row - 1);
-  const int tokens = kRopeThreads / per_row;
-  const int t = blockIdx.x * tokens + static_cast<int>(threadIdx.x) / per_row;
-  if (t >= p.B * p.N) return;
-  const int b = t / p.N, n = t - b * p.N;
-  int row = n;
-  if (APPEND) row = p.cache_len[b] - p.N + n;
-
-  // columns [c0, c0 + 8) and [c1, c1 + 8): eight pairs, or the columns past rot
-  const bool turns = c * 16 < p.rot;
-  const bool halves = !INTERLEAVED && turns;
-  const int c0 = halves ? c * 8 : c * 16, c1 = halves ? c * 8 + (p.rot >> 1) : c * 16 + 8;
-
-  float cs[8], sn[8];
-  if (turns) {
-    const long long pos = p.positions ? p.positions[b * p.pos_b + n] : row;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint64_t a = static_cast<uint64_t>(pos) * turn_fraction(p.inv_freq[c * 8 + i]);
-      const float half_turns = static_cast<float>(static_cast<int32_t>(a >> 32)) * 4.656612873077393e-10f;  // 2^-31
-      sincospif(half_turns, &sn[i], &cs[i]);
-      cs[i] *= p.factor;
-      sn[i] *= p.factor * p.sign;
-    }
+  extern __shared__ float table[];  // cos, then sin: [tokens][rot / 2]
+  const int per_row = p.d >> 4, half = p.rot >> 1;
+  const int t0 = blockIdx.x * p.tokens, all = p.B * p.N;
+  float *cos_t = table, *sin_t = table + p.tokens * half;
+  for (int e = threadIdx.x; e < p.tokens * half; e += kRopeThreads) {
+    const int t = t0 + e / half, i = e % half;
+    if (t >= all) break;
+    const int b = t / p.N, n = t - b * p.N;
+    const long long pos =
+        p.positions ? p.positions[b * p.pos_b + n] : (APPEND ? static_cast<long long>(p.cache_len[b]) - p.N + n : n);
+    const uint64_t a = static_cast<uint64_t>(pos) * turn_fraction(p.inv_freq[i]);
+    const float half_turns = static_cast<float>(static_cast<int32_t>(a >> 32)) * 4.656612873077393e-10f;  // 2^-31
+    float sn, cs;
+    sincospif(half_turns, &sn, &cs);
+    cos_t[e] = cs * p.factor;
+    sin_t[e] = sn * (p.factor * p.sign);
   }
+  __syncthreads();
 
-  for (int h0 = blockIdx.y; h0 < p.heads; h0 += kRopeUnroll * p.head_groups) {
-    RopeRow r[kRopeUnroll];
-    uint4 x0[kRopeUnroll], x1[kRopeUnroll];
-    bool on[kRopeUnroll];
+  const int c = threadIdx.x & (per_row - 1);
+  const int tl = (static_cast<int>(threadIdx.x) / per_row) & (p.tokens - 1);
+  const int lanes = per_row * p.tokens;           // threads of a head
+  const int heads_at_once = kRopeThreads / lanes;
+  const int t = t0 + tl;
+  if (t >= all) return;
+  const int b = t / p.N, n = t - b * p.N;
+  const Pieces x = pieces_of<INTERLEAVED>(p, c);
+  float cs[8], sn[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (x.t0) cs[i] = cos_t[tl * half + x.p0 + i], sn[i] = sin_t[tl * half + x.p0 + i];
+    if (x.t1) cs[i + 4] = cos_t[tl * half + x.p1 + i], sn[i + 4] = sin_t[tl * half + x.p1 + i];
+  }
+  // rows of the three tensors' first heads
+  const __nv_bfloat16 *src[3] = {p.q + b * p.sq.b + n * p.sq.n, p.k + b * p.sk.b + n * p.sk.n, nullptr};
+  __nv_bfloat16 *dst[3] = {p.qo + b * p.sqo.b + n * p.sqo.n, nullptr, nullptr};
+  bool row_on = true;
+  if (APPEND) {
+    const long long row = static_cast<long long>(p.cache_len[b]) - p.N + n;
+    row_on = row >= 0 && row < p.Nk;
+    src[2] = p.v + b * p.sv.b + n * p.sv.n;
+    dst[1] = p.ko + b * p.sko.b + row * p.sko.n;
+    dst[2] = p.vo + b * p.svo.b + row * p.svo.n;
+  } else {
+    dst[1] = p.ko + b * p.sko.b + n * p.sko.n;
+  }
+  const int step = heads_at_once * gridDim.y;
+  for (int h0 = blockIdx.y * heads_at_once + static_cast<int>(threadIdx.x) / lanes; h0 < p.heads;
+       h0 += kRopeUnroll * step) {
+    uint4 w0[kRopeUnroll], w1[kRopeUnroll];
+    __nv_bfloat16 *to[kRopeUnroll];
+    bool turn[kRopeUnroll];
 #pragma unroll
     for (int u = 0; u < kRopeUnroll; ++u) {
-      const int h = h0 + u * p.head_groups;
-      on[u] = h < p.heads && rope_row<APPEND>(p, h, b, n, row, &r[u]);
-      // in place, columns that do not turn stay where they are
-      if (on[u] && !(turns && r[u].turn) && r[u].src == r[u].dst) on[u] = false;
-      if (on[u]) {
-        const int a0 = r[u].turn ? c0 : c * 16, a1 = r[u].turn ? c1 : c * 16 + 8;
-        x0[u] = *reinterpret_cast<const uint4 *>(r[u].src + a0);
-        x1[u] = *reinterpret_cast<const uint4 *>(r[u].src + a1);
+      int h = h0 + u * step;
+      const __nv_bfloat16 *from;
+      bool on = h < p.heads;
+      turn[u] = true;
+      if (h < p.H) {
+        from = src[0] + h * p.sq.h;
+        to[u] = dst[0] + h * p.sqo.h;
+      } else if (!APPEND || h < p.H + p.Hkv) {
+        h -= p.H;
+        on = on && row_on;
+        from = src[1] + h * p.sk.h;
+        to[u] = dst[1] + h * p.sko.h;
+      } else {
+        h -= p.H + p.Hkv;
+        on = on && row_on;
+        from = src[2] + h * p.sv.h;
+        to[u] = dst[2] + h * p.svo.h;
+        turn[u] = false;
       }
+      // (in place, pieces that do not turn stay where they are)
+      if (!on || (from == to[u] && !(turn[u] && (x.t0 || x.t1)))) {
+        to[u] = nullptr;
+        continue;
+      }
+      w0[u] = __ldcs(reinterpret_cast<const uint4 *>(from + x.c0));
+      w1[u] = __ldcs(reinterpret_cast<const uint4 *>(from + x.c1));
     }
 #pragma unroll
     for (int u = 0; u < kRopeUnroll; ++u) {
-      if (!on[u]) continue;
-      const int a0 = r[u].turn ? c0 : c * 16, a1 = r[u].turn ? c1 : c * 16 + 8;
-      uint32_t w[8] = {x0[u].x, x0[u].y, x0[u].z, x0[u].w, x1[u].x, x1[u].y, x1[u].z, x1[u].w};
-      if (turns && r[u].turn) {
+      if (!to[u]) continue;
+      uint32_t w[8] = {w0[u].x, w0[u].y, w0[u].z, w0[u].w, w1[u].x, w1[u].y, w1[u].z, w1[u].w};
+      if (turn[u]) {
         if (INTERLEAVED) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const float2 x = unpack2(w[i]);
-            w[i] = pack2(x.x * cs[i] - x.y * sn[i], x.y * cs[i] + x.x * sn[i]);
+            if (!(i < 4 ? x.t0 : x.t1)) continue;
+            const float2 y = unpack2(w[i]);
+            w[i] = pack2(y.x * cs[i] - y.y * sn[i], y.y * cs[i] + y.x * sn[i]);
           }
-        } else {
+        } else if (x.t0) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float2 a = unpack2(w[i]), z = unpack2(w[i + 4]);
@@ -152,8 +196,8 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeParams 
           }
         }
       }
-      *reinterpret_cast<uint4 *>(r[u].dst + a0) = make_uint4(w[0], w[1], w[2], w[3]);
-      *reinterpret_cast<uint4 *>(r[u].dst + a1) = make_uint4(w[4], w[5], w[6], w[7]);
+      __stcs(reinterpret_cast<uint4 *>(to[u] + x.c0), make_uint4(w[0], w[1], w[2], w[3]));
+      __stcs(reinterpret_cast<uint4 *>(to[u] + x.c1), make_uint4(w[4], w[5], w[6], w[7]));
     }
   }
 }
@@ -161,18 +205,18 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeParams 
 }  // namespace
 
 cudaError_t launch_rope(bool interleaved, const RopeParams &p, cudaStream_t stream) {
-  const int tokens = kRopeThreads / (p.d >> 4);
-  const dim3 grid((p.B * p.N + tokens - 1) / tokens, p.head_groups);
+  const dim3 grid((p.B * p.N + p.tokens - 1) / p.tokens, p.head_groups);
+  const size_t smem = sizeof(float) * p.tokens * p.rot;
   if (p.cache_len) {
     if (interleaved)
-      fa_rope_kernel<true, true><<<grid, kRopeThreads, 0, stream>>>(p);
+      fa_rope_kernel<true, true><<<grid, kRopeThreads, smem, stream>>>(p);
     else
-      fa_rope_kernel<false, true><<<grid, kRopeThreads, 0, stream>>>(p);
+      fa_rope_kernel<false, true><<<grid, kRopeThreads, smem, stream>>>(p);
   } else {
     if (interleaved)
-      fa_rope_kernel<true, false><<<grid, kRopeThreads, 0, stream>>>(p);
+      fa_rope_kernel<true, false><<<grid, kRopeThreads, smem, stream>>>(p);
     else
-      fa_rope_kernel<false, false><<<grid, kRopeThreads, 0, stream>>>(p);
+      fa_rope_kernel<false, false><<<grid, kRopeThreads, smem, stream>>>(p);
   }
   return cudaGetLastError();
 }
