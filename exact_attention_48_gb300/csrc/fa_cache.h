@@ -64,10 +64,10 @@ cudaError_t launch_tree(const CUtensorMap &tq, const CUtensorMap &tk, const CUte
                         bool merge, cudaStream_t stream);
 
 // Accumulated attention weight per key.  A unit is a block of 256 keys of one
-// cache head; the query rows of the head's group come in column tiles: whole
-// heads packed together (`gpt` heads of Nq rows) or, for Nq > 128, 128 rows
-// of one head.  With splits > 1 each unit's column tiles are dealt to that
-// many units whose partial sums a second kernel adds.
+// cache head.  Up to 64 query rows of the head's group are one column tile;
+// more come in tiles of up to 128: whole heads packed together (`gpt` heads of
+// Nq rows) or, for Nq > 128, 128 rows of one head.  With splits > 1 each unit's
+// tiles are dealt to that many units whose partial sums a second kernel adds.
 struct KeyWeightParams {
   const float *lse;           // [B, H, Nq] contiguous
   const float *w_in;          // [B, Hkv, Nk] or null
@@ -78,17 +78,19 @@ struct KeyWeightParams {
   int B, H, Hkv, G, Nq, Nk, causal;
   int gpt, tiles_per_head, head_groups;  // tiles of a head group; groups of gpt heads
   int splits;
-  long long units;            // B * Hkv * ceil(Nk / 256) * splits
+  int window;                 // cache heads worked on at a time
+  uint32_t units;             // B * Hkv * ceil(Nk / 256) * splits, below 2^31
   float scale_log2;
 };
 
 struct KeyWeightPlan {
   int cols;                   // columns of a tile: 16, 32, 64 or 128
-  int box_rows, gpt, tiles_per_head, head_groups, splits;
+  int box_rows, gpt, tiles_per_head, head_groups, splits, window;
 };
-KeyWeightPlan plan_key_weights(int B, int H, int Hkv, int Nq, int Nk);
+KeyWeightPlan plan_key_weights(int B, int H, int Hkv, int Nq, int Nk, int d);
 
-// tq: q with boxes of box_rows rows x gpt heads.
+// tq: q with boxes of box_rows rows x gpt heads; tk: k with boxes of 128 rows,
+// 256 when cols is 128.
 cudaError_t launch_key_weights(int d, int cols, const CUtensorMap &tq, const CUtensorMap &tk,
                                const KeyWeightParams &p, int sms, cudaStream_t stream);
 

@@ -195,6 +195,8 @@ fa_status_t check_key_weights(int B, int H, int Hkv, int Nq, int Nk, int d, int 
   const fa_status_t st = check_cache(B, H, Hkv, Nk, d);
   if (st != FA_OK) return st;
   if (Nq < 1 || Nq > kMaxRows || (causal != 0 && causal != 1)) return FA_ERR_INVALID_ARGUMENT;
+  // 256-key blocks are counted in 31 bits (weights of 2 TiB)
+  if (static_cast<long long>(B) * Hkv * ((Nk + 255) / 256) >= (1LL << 31)) return FA_ERR_INVALID_ARGUMENT;
   return std::isfinite(scale) ? FA_OK : FA_ERR_INVALID_ARGUMENT;
 }
 
@@ -382,7 +384,7 @@ fa_status_t fa_fwd_tree(const void *q, const int64_t *q_strides, const void *k, 
 
 size_t fa_key_weights_workspace_bytes(int B, int H, int Hkv, int Nq, int Nk, int d) {
   if (check_key_weights(B, H, Hkv, Nq, Nk, d, 0, 1.0f) != FA_OK) return 0;
-  const KeyWeightPlan pl = plan_key_weights(B, H, Hkv, Nq, Nk);
+  const KeyWeightPlan pl = plan_key_weights(B, H, Hkv, Nq, Nk, d);
   return pl.splits > 1 ? round256(static_cast<size_t>(pl.splits) * B * Hkv * Nk * 4) : 0;
 }
 
@@ -402,7 +404,7 @@ fa_status_t fa_key_weights(const void *q, const int64_t *q_strides, const void *
   if (meet(rw, range_of(vq, B, d)) || meet(rw, range_of(vk, B, d)) || meet(rw, range_of(lse, 4ll * B * H * Nq)) ||
       meet(rw, range_of(cache_seqlens, 4ll * B)) || (weights_in != weights && meet(rw, range_of(weights_in, wbytes))))
     return FA_ERR_INVALID_ARGUMENT;
-  const KeyWeightPlan pl = plan_key_weights(B, H, Hkv, Nq, Nk);
+  const KeyWeightPlan pl = plan_key_weights(B, H, Hkv, Nq, Nk, d);
   Scratch ws(workspace, workspace_bytes, fa_key_weights_workspace_bytes(B, H, Hkv, Nq, Nk, d));
   const Range used[6] = {range_of(vq, B, d), range_of(vk, B, d), range_of(lse, 4ll * B * H * Nq), rw,
                          range_of(weights_in, wbytes), range_of(cache_seqlens, 4ll * B)};
@@ -411,7 +413,7 @@ fa_status_t fa_key_weights(const void *q, const int64_t *q_strides, const void *
   const int sms = sm_count();
   CUtensorMap tq, tk;
   if (sms <= 0 || !encode_map(&tq, q, B, H, Nq, d, vq.s, pl.box_rows, pl.gpt) ||
-      !encode_map(&tk, k, B, Hkv, Nk, d, vk.s))
+      !encode_map(&tk, k, B, Hkv, Nk, d, vk.s, pl.cols == 128 ? 256 : 128))
     return FA_ERR_CUDA;
   KeyWeightParams p{};
   p.status = status_ptr();
@@ -432,7 +434,8 @@ fa_status_t fa_key_weights(const void *q, const int64_t *q_strides, const void *
   p.tiles_per_head = pl.tiles_per_head;
   p.head_groups = pl.head_groups;
   p.splits = pl.splits;
-  p.units = static_cast<long long>(B) * Hkv * ((Nk + 255) / 256) * pl.splits;
+  p.window = pl.window;
+  p.units = static_cast<uint32_t>(static_cast<long long>(B) * Hkv * ((Nk + 255) / 256) * pl.splits);
   p.scale_log2 = scale * 1.4426950408889634f;
   const bool launched = launch_key_weights(d, pl.cols, tq, tk, p, sms, stream) == cudaSuccess;
   return ws.give_back(stream) && launched ? FA_OK : FA_ERR_CUDA;
