@@ -43,17 +43,18 @@ struct TreeParams {
   long long par_b;
   const int *cache_len;       // [B] or null
   int *status;
-  float *part_o;              // [2 * ctas][slot_rows][d], normalised
+  float *part_o;              // [2 * ctas][d][slot_rows], normalised
   float *part_lse;            // [2 * ctas][slot_rows], log2 units; +inf marks padding
   int B, H, Hkv, G, Nt, Nk, d;
   int gpt, row_tiles, groups, ranges, split;
+  int whole;                  // runs end at units' ends: no partial results
   float scale_log2;
   int neg;
 };
 
 // How a call is cut up: a function of the shape alone.
 struct TreePlan {
-  int gpt, row_tiles, groups, ranges, split;
+  int gpt, row_tiles, groups, ranges, split, whole;
   bool merge;                 // some unit may end up in several runs
   size_t part_rows;           // rows of partial results
 };

@@ -376,6 +376,7 @@ fa_status_t fa_fwd_tree(const void *q, const int64_t *q_strides, const void *k, 
   p.groups = pl.groups;
   p.ranges = pl.ranges;
   p.split = pl.split;
+  p.whole = pl.whole;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.neg = scale < 0.0f ? 1 : 0;
   const bool launched = launch_tree(tq, tk, tv, p, pl.merge, stream) == cudaSuccess;

@@ -83,6 +83,18 @@ __device__ __forceinline__ int bit_row(int i) {
 // that its rows get written).
 __device__ __forceinline__ int tiles_of(int n) { return n > 0 ? (n + kKeys - 1) / kKeys : 1; }
 
+// First tile of run c of `runs` over `total` tiles (a 64-bit division takes
+// hundreds of cycles of a CTA's start: 32 bits when they do).
+__device__ __forceinline__ long long run_start(long long total, long long c, long long runs) {
+  const unsigned long long x = static_cast<unsigned long long>(total) * c;
+  if (x >> 32) return static_cast<long long>(x / runs);
+  return static_cast<uint32_t>(x) / static_cast<uint32_t>(runs);
+}
+__device__ __forceinline__ long long divide(long long a, long long b) {
+  if ((a | b) >> 32) return a / b;
+  return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+}
+
 // Where a CTA's run of tiles starts and ends, in the list of all units' tiles.
 struct RunStart {
   long long t, end;    // [t, end)
@@ -100,7 +112,7 @@ struct Walk {
   bool tail;             // it holds the unit's last tile
   __device__ Walk(const TreeParams &pp, const RunStart &s) : p(pp), t(s.t), end(s.end), b(s.b) {
     load();
-    hk = static_cast<int>((t - s.b_start) / tiles);
+    hk = static_cast<int>(divide(t - s.b_start, tiles));
     u0 = s.b_start + static_cast<long long>(hk) * tiles;
     k1 = 0;
     tail = false;
@@ -143,21 +155,58 @@ __device__ __forceinline__ long long runs_of(const TreeParams &p, long long tota
   return total < p.ranges ? total : p.ranges;
 }
 
+// First tile of the unit that holds tile t (t >= b_start, the first tile of a
+// sequence of `tiles` tiles a unit).
+__device__ __forceinline__ long long unit_start(long long t, long long b_start, int tiles) {
+  return b_start + divide(t - b_start, tiles) * tiles;
+}
+
 // Run c over the tiles of all units, located by the whole block (every thread
-// calls it; ends with a barrier).  False: there is no run c.
+// calls it; ends with a barrier).  With p.whole a run's ends are moved back to
+// their units' starts, so that no unit is cut.  False: there is no run c, or
+// nothing is left of it.
 __device__ __forceinline__ bool find_run(const TreeParams &p, int c, RunStart *out, long long *scan) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (!p.cache_len) {
-    const long long per_b = static_cast<long long>(p.Hkv) * tiles_of(p.Nk), total = per_b * p.B;
+    const int tiles = tiles_of(p.Nk);
+    const long long per_b = static_cast<long long>(p.Hkv) * tiles, total = per_b * p.B;
     const long long runs = runs_of(p, total);
     if (tid == 0 && c < runs) {
-      out->t = total * c / runs;
-      out->end = total * (c + 1) / runs;
-      out->b = static_cast<int>(out->t / per_b);
+      long long t = run_start(total, c, runs), end = run_start(total, c + 1, runs);
+      if (p.whole) t = unit_start(t, 0, tiles), end = unit_start(end, 0, tiles);
+      out->t = t;
+      out->end = end;
+      out->b = static_cast<int>(divide(t, per_b));
       out->b_start = out->b * per_b;
     }
     __syncthreads();
-    return c < runs;
+    return c < runs && out->t < out->end;
+  }
+  if (p.B <= 32) {  // a lane per sequence, by one warp
+    if (warp == 0) {
+      const int tiles = lane < p.B ? tiles_of(cache_rows(p.cache_len, lane, p.Nk)) : 0;
+      const long long n = static_cast<long long>(p.Hkv) * tiles;
+      long long incl = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += x;
+      }
+      const long long total = __shfl_sync(0xffffffffu, incl, 31), runs = runs_of(p, total);
+      const long long t = run_start(total, c, runs), end = run_start(total, c + 1, runs);
+      const int first = __ffs(__ballot_sync(0xffffffffu, t < incl)) - 1;  // (none past the last run)
+      const int last = __ffs(__ballot_sync(0xffffffffu, end < incl)) - 1;
+      if (lane == 0) out->t = out->end = total;
+      __syncwarp();
+      if (lane == first) {
+        out->t = p.whole ? unit_start(t, incl - n, tiles) : t;
+        out->b = lane;
+        out->b_start = incl - n;
+      }
+      if (lane == last) out->end = p.whole ? unit_start(end, incl - n, tiles) : end;
+    }
+    __syncthreads();
+    return out->t < out->end;
   }
   // each thread sums a block of batch entries, then a scan over the threads
   const int chunk = (p.B + kThreads - 1) / kThreads;
@@ -172,30 +221,39 @@ __device__ __forceinline__ bool find_run(const TreeParams &p, int c, RunStart *o
     if (lane >= o) incl += x;
   }
   if (lane == 31) scan[warp] = incl;
+  if (tid == 0) out->t = out->end = 0x7fffffffffffffffll;  // (past the last tile)
   __syncthreads();
   long long before = 0, total = 0;
   for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) before += scan[w];
     total += scan[w];
   }
-  long long at = before + incl - mine;  // first tile of entry b0
   const long long runs = runs_of(p, total);
-  const long long t = total * c / runs;
-  if (c < runs && t >= at && t < at + mine) {  // exactly one thread
+  const long long ends[2] = {run_start(total, c, runs), run_start(total, c + 1, runs)};
+  for (int e = 0; e < 2; ++e) {
+    long long at = before + incl - mine;  // first tile of entry b0
+    if (ends[e] < at || ends[e] >= at + mine) continue;  // exactly one thread goes on, none past the last tile
     for (int b = b0;; ++b) {
-      const long long n = static_cast<long long>(p.Hkv) * tiles_of(cache_rows(p.cache_len, b, p.Nk));
-      if (t < at + n) {
-        out->t = t;
-        out->end = total * (c + 1) / runs;
-        out->b = b;
-        out->b_start = at;
+      const int tiles = tiles_of(cache_rows(p.cache_len, b, p.Nk));
+      const long long n = static_cast<long long>(p.Hkv) * tiles;
+      if (ends[e] < at + n) {
+        const long long t = p.whole ? unit_start(ends[e], at, tiles) : ends[e];
+        if (e == 0) {
+          out->t = t;
+          out->b = b;
+          out->b_start = at;
+        } else {
+          out->end = t;
+        }
         break;
       }
       at += n;
     }
   }
   __syncthreads();
-  return c < runs;
+  if (tid == 0 && out->end > total) out->end = total;
+  __syncthreads();
+  return out->t < out->end;
 }
 
 // The visibility table of one unit's tree, by one warp: bit rows, and the
@@ -204,9 +262,11 @@ __device__ __forceinline__ bool find_run(const TreeParams &p, int c, RunStart *o
 __device__ __forceinline__ void build_table(const TreeParams &p, int b, int base, uint32_t *bits, uint32_t *dead,
                                             volatile int8_t *jump) {
   const int lane = threadIdx.x & 31;
-  const int n = p.Nt;
+  const int n = p.Nt, words = (n + 31) >> 5;
   uint32_t bad[4] = {0, 0, 0, 0};  // this lane's copy of the padding bits
+#pragma unroll
   for (int w = 0; w < 4; ++w) {
+    if (w >= words) break;
     const int i = w * 32 + lane;
     int up = -1;
     bool live = false;
@@ -229,17 +289,16 @@ __device__ __forceinline__ void build_table(const TreeParams &p, int b, int base
     bool any = false;
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-      const int i = w * 32 + lane;
-      to[w] = jump[i];
-      next[w] = -1;
+      to[w] = next[w] = -1;
 #pragma unroll
       for (int x = 0; x < 4; ++x) add[w][x] = 0;
+      if (w < words) to[w] = jump[w * 32 + lane];
       if (to[w] >= 0) {
         any = true;
         next[w] = jump[to[w]];
         const uint32_t *r = bits + bit_row(to[w]);
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
+        for (int x = 0; x <= w; ++x)
           if (x <= (to[w] >> 5)) add[w][x] = r[x];
       }
     }
@@ -247,11 +306,12 @@ __device__ __forceinline__ void build_table(const TreeParams &p, int b, int base
     __syncwarp();
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
+      if (w >= words) break;
       const int i = w * 32 + lane;
       if (to[w] >= 0) {
         uint32_t *r = bits + bit_row(i);
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
+        for (int x = 0; x <= w; ++x)
           if (x <= (to[w] >> 5)) r[x] |= add[w][x];
       }
       jump[i] = static_cast<int8_t>(next[w]);
@@ -259,18 +319,21 @@ __device__ __forceinline__ void build_table(const TreeParams &p, int b, int base
     __syncwarp();
   }
   // padding spreads to every node that has a padding node among its ancestors
-  for (int w = 0; w < 4; ++w) {
-    const int i = w * 32 + lane;
-    bool d = true;
-    if (i < n) {
-      const uint32_t *r = bits + bit_row(i);
-      uint32_t hit = 0;
 #pragma unroll
-      for (int x = 0; x < 4; ++x)
-        if (x <= w) hit |= r[x] & bad[x];
-      d = hit != 0;
+  for (int w = 0; w < 4; ++w) {
+    uint32_t m = 0xffffffffu;
+    if (w < words) {
+      const int i = w * 32 + lane;
+      bool d = true;
+      if (i < n) {
+        const uint32_t *r = bits + bit_row(i);
+        uint32_t hit = 0;
+#pragma unroll
+        for (int x = 0; x <= w; ++x) hit |= r[x] & bad[x];
+        d = hit != 0;
+      }
+      m = __ballot_sync(0xffffffffu, d);
     }
-    const uint32_t m = __ballot_sync(0xffffffffu, d);
     if (lane == 0) dead[w] = m;
   }
   __syncwarp();
@@ -290,17 +353,67 @@ struct SoftmaxArgs {
   int warps;        // warps of the warpgroup that hold rows
 };
 
+// Keys 32 q .. 32 q + 31 of a tile whose first key is node n0 of the tree (or
+// before it) that node i sees: rows before the tree, and its bit row.
+__device__ __forceinline__ uint32_t visible(const uint32_t *bits, int i, bool live, int f) {
+  if (!live || f >= 128) return 0u;
+  if (f <= -32) return ~0u;  // rows before the tree
+  const uint32_t *r = bits + bit_row(i);
+  const int top = i >> 5;    // words 0..top; nodes past it are not seen
+  if (f < 0) return (r[0] << -f) | ((1u << -f) - 1u);
+  const int x = f >> 5;
+  const uint32_t lo = x <= top ? r[x] : 0u, hi = x + 1 <= top ? r[x + 1] : 0u;
+  return __funnelshift_r(lo, hi, f & 31);
+}
+
+// The running maximum moves to `cand` if that exceeds it by enough; returns
+// whether it did, and the factor of what was summed before.
+__device__ __forceinline__ bool move_max(RowState &st, float cand, float *alpha) {
+  *alpha = 1.0f;
+  if (!(cand > st.m + kRescaleThreshold)) return false;
+  *alpha = ex2(st.m - cand);
+  st.m = cand;
+  return true;
+}
+
+// O rescaled where a row's maximum moved (after the P V product before it).
+template <int D>
+__device__ __forceinline__ bool rescale_o(const SoftmaxArgs &a, const WaitCtl &ctl, uint32_t cnt, float alpha) {
+  if (!__all_sync(0xffffffffu, mbar_wait(a.pv_done, (cnt - 1) & 1, ctl, kSitePvDone))) return false;
+  tc_fence_after();
+#pragma unroll 1
+  for (int ch = 0; ch < D / 16; ++ch) {
+    uint32_t o[16];
+    tmem_ld16(a.tO + ch * 16, o);
+    tmem_ld_wait16(o);
+#pragma unroll
+    for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
+    tmem_st16(a.tO + ch * 16, o);
+  }
+  tmem_st_wait();
+  return true;
+}
+
+__device__ __forceinline__ float max32(const uint32_t (&s)[32]) {
+  float m = fmax3(__uint_as_float(s[0]), __uint_as_float(s[1]), __uint_as_float(s[2]));
+#pragma unroll
+  for (int x = 3; x < 31; x += 2) m = fmax3(m, __uint_as_float(s[x]), __uint_as_float(s[x + 1]));
+  return fmaxf(m, __uint_as_float(s[31]));
+}
+__device__ __forceinline__ float min32(const uint32_t (&s)[32]) {
+  float m = fmin3(__uint_as_float(s[0]), __uint_as_float(s[1]), __uint_as_float(s[2]));
+#pragma unroll
+  for (int x = 3; x < 31; x += 2) m = fmin3(m, __uint_as_float(s[x]), __uint_as_float(s[x + 1]));
+  return fminf(m, __uint_as_float(s[31]));
+}
+
 // One 128-key tile: scores from TMEM, running maximum and sum, P as bf16 over
 // S, O rescaled when the maximum moves.  `cnt`: tiles this warpgroup has
-// taken so far (barrier phases); first: its first tile of the segment;
-// e_v: the V tile's place in the ring's sequence; key0: first key of the
-// tile.  MASK: the tile holds nodes or rows behind the end.
-template <int D, int SLOTS, bool MASK>
+// taken so far (barrier phases); first: its first tile of the segment.
+template <int D>
 __device__ __forceinline__ bool softmax_tile(const SoftmaxArgs &a, const TreeParams &p, const WaitCtl &ctl,
-                                             const Walk &wk, RowState &st, uint32_t cnt, bool first, uint32_t e_v,
-                                             int key0) {
+                                             RowState &st, uint32_t cnt, bool first) {
   const float c = p.scale_log2;
-  const bool neg = p.neg != 0;
   if (!__all_sync(0xffffffffu, mbar_wait(a.s_full, cnt & 1, ctl, kSiteSFull))) return false;
   tc_fence_after();
   uint32_t s[4][32];
@@ -308,73 +421,13 @@ __device__ __forceinline__ bool softmax_tile(const SoftmaxArgs &a, const TreePar
   for (int q = 0; q < 4; ++q) tmem_ld32(a.tS + q * 32, s[q]);
 #pragma unroll
   for (int q = 0; q < 4; ++q) tmem_ld_wait(s[q]);
-
-  uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};  // visible keys of the tile
-  if (MASK) {
-    const int n0 = key0 - wk.base();  // node of the tile's first key
-    const int i = a.node;
-    const bool live = i >= 0 && !((a.dead[i >> 5] >> (i & 31)) & 1u);
-    uint32_t w[6];                    // bits of nodes -32.. 0 and 0..127, then nothing
-    w[4] = w[5] = 0;
-#pragma unroll
-    for (int x = 0; x < 4; ++x) w[x] = live && x <= (i >> 5) ? a.bits[bit_row(i) + x] : 0u;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int f = n0 + 32 * q;      // first node of this quarter
-      uint32_t v;
-      if (f <= -32) {
-        v = ~0u;                      // rows before the tree
-      } else if (f < 0) {
-        v = (w[0] << -f) | ((1u << -f) - 1u);
-      } else {
-        uint32_t lo = 0, hi = 0;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          if (x == (f >> 5)) lo = w[x], hi = w[x + 1];
-        }
-        v = __funnelshift_r(lo, hi, f & 31);
-      }
-      see[q] = live ? v : 0u;
-    }
-    const uint32_t hide = __float_as_uint(neg ? INFINITY : -INFINITY);
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-#pragma unroll
-      for (int x = 0; x < 32; ++x)
-        if (!((see[q] >> x) & 1u)) s[q][x] = hide;
-  }
-
   float mx;
-  {
-    float mq[4];
-    if (!neg) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float m0 = fmax3(__uint_as_float(s[q][0]), __uint_as_float(s[q][1]), __uint_as_float(s[q][2]));
-#pragma unroll
-        for (int x = 3; x < 31; x += 2) m0 = fmax3(m0, __uint_as_float(s[q][x]), __uint_as_float(s[q][x + 1]));
-        mq[q] = fmaxf(m0, __uint_as_float(s[q][31]));
-      }
-      mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
-    } else {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float m0 = fmin3(__uint_as_float(s[q][0]), __uint_as_float(s[q][1]), __uint_as_float(s[q][2]));
-#pragma unroll
-        for (int x = 3; x < 31; x += 2) m0 = fmin3(m0, __uint_as_float(s[q][x]), __uint_as_float(s[q][x + 1]));
-        mq[q] = fminf(m0, __uint_as_float(s[q][31]));
-      }
-      mx = fminf(fminf(mq[0], mq[1]), fminf(mq[2], mq[3]));
-    }
-  }
-  const bool hidden = MASK && (see[0] | see[1] | see[2] | see[3]) == 0u;  // (0 * -inf is NaN)
-  const float cand = hidden ? -INFINITY : mx * c;
-  const bool grow = cand > st.m + kRescaleThreshold;
-  float alpha = 1.0f;
-  if (grow) {
-    alpha = ex2(st.m - cand);
-    st.m = cand;
-  }
+  if (!p.neg)
+    mx = fmaxf(fmaxf(max32(s[0]), max32(s[1])), fmaxf(max32(s[2]), max32(s[3])));
+  else
+    mx = fminf(fminf(min32(s[0]), min32(s[1])), fminf(min32(s[2]), min32(s[3])));
+  float alpha;
+  const bool grow = move_max(st, mx * c, &alpha);
   const float2 cc = make_float2(c, c), nm = make_float2(-st.m, -st.m);
   uint32_t pk[4][16];
   float2 sf = make_float2(0.f, 0.f);
@@ -384,11 +437,7 @@ __device__ __forceinline__ bool softmax_tile(const SoftmaxArgs &a, const TreePar
 #pragma unroll
     for (int x = 0; x < 32; x += 2) {
       const float2 y = ffma2(make_float2(__uint_as_float(s[q][x]), __uint_as_float(s[q][x + 1])), cc, nm);
-      float p0 = ex2(y.x), p1 = ex2(y.y);
-      if (MASK) {
-        p0 = (see[q] >> x) & 1u ? p0 : 0.0f;
-        p1 = (see[q] >> (x + 1)) & 1u ? p1 : 0.0f;
-      }
+      const float p0 = ex2(y.x), p1 = ex2(y.y);
       pk[q][x / 2] = pack_bf16x2(p0, p1);
       sq = fadd2(sq, make_float2(p0, p1));
     }
@@ -396,35 +445,7 @@ __device__ __forceinline__ bool softmax_tile(const SoftmaxArgs &a, const TreePar
     sf = fadd2(sf, sq);
   }
   tmem_st_wait();
-
-  if (!first && __any_sync(0xffffffffu, grow)) {
-    if (!__all_sync(0xffffffffu, mbar_wait(a.pv_done, (cnt - 1) & 1, ctl, kSitePvDone))) return false;
-    tc_fence_after();
-#pragma unroll 1
-    for (int ch = 0; ch < D / 16; ++ch) {
-      uint32_t o[16];
-      tmem_ld16(a.tO + ch * 16, o);
-      tmem_ld_wait16(o);
-#pragma unroll
-      for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
-      tmem_st16(a.tO + ch * 16, o);
-    }
-    tmem_st_wait();
-  }
-  if (MASK) {  // V rows that no query row sees
-    if (!__all_sync(0xffffffffu, mbar_wait(&a.full[e_v % SLOTS], (e_v / SLOTS) & 1, ctl, kSiteVFull))) return false;
-    uint8_t *v = a.ring + (e_v % SLOTS) * (kKeys * D * 2);
-    for (int r = threadIdx.x & 127; r < kKeys; r += a.warps * 32) {
-      const int node = key0 + r - wk.base();
-      if (node < 0 || (node < p.Nt && !((a.dead[node >> 5] >> (node & 31)) & 1u))) continue;
-#pragma unroll
-      for (int sl = 0; sl < D / 64; ++sl)
-#pragma unroll
-        for (int x = 0; x < 8; ++x)
-          *reinterpret_cast<uint4 *>(v + sl * (kKeys * 128) + r * 128 + x * 16) = make_uint4(0u, 0u, 0u, 0u);
-    }
-    fence_proxy_async_smem();
-  }
+  if (!first && __any_sync(0xffffffffu, grow) && !rescale_o<D>(a, ctl, cnt, alpha)) return false;
   tc_fence_before();
   warp_arrive(a.p_ready);
 
@@ -437,6 +458,80 @@ __device__ __forceinline__ bool softmax_tile(const SoftmaxArgs &a, const TreePar
     for (int x = 0; x < 16; ++x) sq = add_bf16x2_f32(sq, pk[q][x]);
     sb = fadd2(sb, sq);
   }
+  st.lb = st.lb * alpha + (sb.x + sb.y);
+  return true;
+}
+
+// The same for a tile that holds nodes or rows behind the end (its first key
+// is node n0), at most two or three of a unit's tiles: a loop over the
+// quarters, twice over S, because code that runs once per unit comes cold
+// from memory (the unrolled form took 7000 cycles, most of them waiting for
+// its instructions).  e_v: the V tile's place in the ring's sequence.
+template <int D, int SLOTS>
+__device__ __forceinline__ bool masked_tile(const SoftmaxArgs &a, const TreeParams &p, const WaitCtl &ctl,
+                                            RowState &st, uint32_t cnt, bool first, uint32_t e_v, int n0) {
+  const float c = p.scale_log2;
+  if (!__all_sync(0xffffffffu, mbar_wait(a.s_full, cnt & 1, ctl, kSiteSFull))) return false;
+  tc_fence_after();
+  const int i = a.node;
+  const bool live = i >= 0 && !((a.dead[i >> 5] >> (i & 31)) & 1u);
+  const uint32_t hide = __float_as_uint(p.neg ? INFINITY : -INFINITY);
+  float mx = __uint_as_float(hide);
+  uint32_t any = 0;
+#pragma unroll 1
+  for (int q = 0; q < 4; ++q) {
+    const uint32_t see = visible(a.bits, i, live, n0 + 32 * q);
+    any |= see;
+    uint32_t s[32];
+    tmem_ld32(a.tS + q * 32, s);
+    tmem_ld_wait(s);
+#pragma unroll
+    for (int x = 0; x < 32; ++x)
+      if (!((see >> x) & 1u)) s[x] = hide;
+    mx = p.neg ? fminf(mx, min32(s)) : fmaxf(mx, max32(s));
+  }
+  float alpha;
+  const bool grow = move_max(st, any ? mx * c : -INFINITY, &alpha);  // (0 * -inf is NaN)
+  float2 sf = make_float2(0.f, 0.f), sb = sf;
+#pragma unroll 1
+  for (int q = 0; q < 4; ++q) {  // P's quarter q lies over S's columns 16 q .. 16 q + 15, read by then
+    const uint32_t see = visible(a.bits, i, live, n0 + 32 * q);
+    uint32_t s[32], pk[16];
+    tmem_ld32(a.tS + q * 32, s);
+    tmem_ld_wait(s);
+#pragma unroll
+    for (int x = 0; x < 32; x += 2) {
+      const float p0 = (see >> x) & 1u ? ex2(fmaf(__uint_as_float(s[x]), c, -st.m)) : 0.0f;
+      const float p1 = (see >> (x + 1)) & 1u ? ex2(fmaf(__uint_as_float(s[x + 1]), c, -st.m)) : 0.0f;
+      pk[x / 2] = pack_bf16x2(p0, p1);
+      sf = fadd2(sf, make_float2(p0, p1));
+      sb = add_bf16x2_f32(sb, pk[x / 2]);
+    }
+    tmem_st16(a.tS + q * 16, pk);
+  }
+  tmem_st_wait();
+  if (!first && __any_sync(0xffffffffu, grow) && !rescale_o<D>(a, ctl, cnt, alpha)) return false;
+  // V rows that no query row sees become zeros (0 * NaN is NaN)
+  if (!__all_sync(0xffffffffu, mbar_wait(&a.full[e_v % SLOTS], (e_v / SLOTS) & 1, ctl, kSiteVFull))) return false;
+  uint8_t *v = a.ring + (e_v % SLOTS) * (kKeys * D * 2);
+#pragma unroll 1
+  for (int q = 0; q < 4; ++q) {
+    const int lane = threadIdx.x & 31, node = n0 + 32 * q + lane;
+    const bool gone = node >= p.Nt || (node >= 0 && ((a.dead[node >> 5] >> (node & 31)) & 1u));
+    const uint32_t rows = __ballot_sync(0xffffffffu, gone);
+    if (rows == 0) continue;
+    // 16-byte pieces, a row's eight side by side
+    for (int e = threadIdx.x & 127; e < 32 * 8; e += a.warps * 32) {
+      if (!((rows >> (e >> 3)) & 1u)) continue;
+#pragma unroll
+      for (int sl = 0; sl < D / 64; ++sl)
+        *reinterpret_cast<uint4 *>(v + sl * (kKeys * 128) + q * 32 * 128 + e * 16) = make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+  fence_proxy_async_smem();
+  tc_fence_before();
+  warp_arrive(a.p_ready);
+  st.l = st.l * alpha + (sf.x + sf.y);
   st.lb = st.lb * alpha + (sb.x + sb.y);
   return true;
 }
@@ -492,34 +587,43 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (!find_run(p, c, run, reinterpret_cast<long long *>(small + L::kOffScan))) return;
   if (warp == kWarpMma) {
     tmem_alloc(tmem_slot, kTmemCols);
     tmem_relinquish();
   }
+  if (warp == kWarpProducer && lane == 0) {
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
   tc_fence_before();
-  __syncthreads();
+  const bool has_run = find_run(p, c, run, reinterpret_cast<long long *>(small + L::kOffScan));
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if (!has_run) {
+    if (warp == kWarpMma) tmem_dealloc(tmem, kTmemCols);
+    return;
+  }
   Walk wk(p, *run);
 
   if (warp >= kWarpProducer) {
     regs_decrease<kRegsControl>();
     if (warp == kWarpProducer && lane == 0) {
       // ---------------------------------------------------------- producer
-      tma_prefetch_desc(&tm_q);
-      tma_prefetch_desc(&tm_k);
-      tma_prefetch_desc(&tm_v);
-      uint32_t e = 0, nq = 0;  // ring loads and Q loads so far
+      uint32_t e = 0, nq = 0;   // ring loads and Q loads so far
+      uint32_t sl = 0, ph = 0;  // the ring's next slot and its phase
       bool ok = true;
       auto load = [&](const CUtensorMap *map, int row) -> bool {
-        const uint32_t sl = e % S;
-        if (!mbar_wait(&empty[sl], ((e / S) & 1) ^ 1, ctl, kSiteKvEmpty)) return false;
+        if (!mbar_wait(&empty[sl], ph ^ 1, ctl, kSiteKvEmpty)) return false;
         mbar_arrive_expect_tx(&full[sl], L::kTile);
 #pragma unroll
         for (int x = 0; x < L::kSlabs; ++x)
           tma_load_4d(ring + sl * L::kTile + x * kKeys * 128, map, &full[sl], x * 64, row, wk.hk, wk.b);
         ++e;
+        if (++sl == S) {
+          sl = 0;
+          ph ^= 1;
+        }
         return true;
       };
       while (ok && wk.next()) {
@@ -541,30 +645,44 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------------------- MMA issuer
       constexpr uint32_t kIdS = idesc_bf16(kRows, kKeys, false, false);
       constexpr uint32_t kIdO = idesc_bf16(kRows, D, false, true);
-      const uint32_t aQ = smem_addr(sQ), aR = smem_addr(ring);
-      uint32_t g = 0, nq = 0;         // tiles and Q loads so far
-      uint32_t cnt[2] = {0, 0};       // P V products per warpgroup so far
+      const uint64_t dQ = sdesc_sw128(smem_addr(sQ), 16, 1024);
+      const uint64_t dK = sdesc_sw128(smem_addr(ring), 16, 1024);             // slot 0 as a K tile
+      const uint64_t dV = sdesc_sw128(smem_addr(ring), kKeys * 128, 1024);    // and as a V tile
+      // A place in the ring's sequence of loads K_0 V_0 K_1 V_1 ...: its slot
+      // and phase, stepped from tile to tile without a division.
+      struct Place {
+        uint32_t slot, phase;
+        __device__ void next_tile() {
+          slot += 2;
+          if (slot >= S) {
+            slot -= S;
+            phase ^= 1;
+          }
+        }
+      };
+      Place kp{0, 0}, vp{1, 0};
+      uint32_t nq = 0;            // Q loads so far
+      uint32_t cnt[2] = {0, 0};   // P V products per warpgroup so far
       bool ok = true;
-      auto full_wait = [&](uint32_t e, int site) {
-        const bool r = mbar_wait(&full[e % S], (e / S) & 1, ctl, site);
+      auto full_wait = [&](const Place &x, int site) {
+        const bool r = mbar_wait(&full[x.slot], x.phase, ctl, site);
         tc_fence_after();
         return r;
       };
-      // S of warpgroup t = its Q tile times K of tile x (counted over the run)
-      auto issue_s = [&](int t, uint32_t x) {
-        const uint64_t dq = sdesc_sw128(aQ + (SPLIT ? 0 : t) * L::kTile, 16, 1024);
-        const uint64_t dk = sdesc_sw128(aR + ((2 * x) % S) * L::kTile, 16, 1024);
+      // S of warpgroup t = its Q tile times the K tile at x
+      auto issue_s = [&](int t, const Place &x) {
+        const uint64_t dq = desc_add(dQ, (SPLIT ? 0 : t) * L::kTile), dk = desc_add(dK, x.slot * L::kTile);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
           mma_ss(tmem + t * 128, desc_add(dq, kmajor_step(kk, kRows)), desc_add(dk, kmajor_step(kk, kKeys)), kIdS,
                  kk > 0 ? 1u : 0u);
         tc_commit(&s_full[t]);
       };
-      auto issue_pv = [&](int t, uint32_t x, bool first) -> bool {
+      auto issue_pv = [&](int t, const Place &x, bool first) -> bool {
         if (!mbar_wait(&p_ready[t], cnt[t] & 1, ctl, kSitePReady)) return false;
         ++cnt[t];
         tc_fence_after();
-        const uint64_t dv = sdesc_sw128(aR + ((2 * x + 1) % S) * L::kTile, kKeys * 128, 1024);
+        const uint64_t dv = desc_add(dV, x.slot * L::kTile);
 #pragma unroll
         for (int kk = 0; kk < kKeys / 16; ++kk)
           mma_ts(tmem + 256 + t * D, tmem + t * 128 + kk * 8, desc_add(dv, mnmajor_step(kk)), kIdO,
@@ -581,37 +699,39 @@ __global__ void __launch_bounds__(kThreads, 1)
           // right after the P V product two tiles before it
           for (int x = 0; ok && x < n + 2; ++x) {
             if (x >= 2) {
-              const int y = x - 2;
-              ok = full_wait(2 * (g + y) + 1, kSiteVFull) && issue_pv(y & 1, g + y, y < 2);
-              if (ok) tc_commit(&empty[(2 * (g + y) + 1) % S]);
+              ok = full_wait(vp, kSiteVFull) && issue_pv(x & 1, vp, x < 4);
+              if (ok) tc_commit(&empty[vp.slot]);
+              vp.next_tile();
             }
             if (ok && x < n) {
-              if (!(ok = full_wait(2 * (g + x), kSiteKFull))) break;
-              issue_s(x & 1, g + x);
-              tc_commit(&empty[(2 * (g + x)) % S]);
+              if (!(ok = full_wait(kp, kSiteKFull))) break;
+              issue_s(x & 1, kp);
+              tc_commit(&empty[kp.slot]);
+              kp.next_tile();
               if (x == n - 1) tc_commit(q_empty);
             }
           }
         } else {
           for (int x = 0; ok && x <= n; ++x) {
-            if (x > 0 && !(ok = full_wait(2 * (g + x - 1) + 1, kSiteVFull))) break;
-            if (x > 0 && !(ok = issue_pv(0, g + x - 1, x == 1))) break;
+            if (x > 0 && !(ok = full_wait(vp, kSiteVFull))) break;
+            if (x > 0 && !(ok = issue_pv(0, vp, x == 1))) break;
             if (x < n) {
-              if (!(ok = full_wait(2 * (g + x), kSiteKFull))) break;
-              issue_s(0, g + x);
+              if (!(ok = full_wait(kp, kSiteKFull))) break;
+              issue_s(0, kp);
             }
             if (x > 0) {
-              if (two && !(ok = issue_pv(1, g + x - 1, x == 1))) break;
-              tc_commit(&empty[(2 * (g + x - 1) + 1) % S]);
+              if (two && !(ok = issue_pv(1, vp, x == 1))) break;
+              tc_commit(&empty[vp.slot]);
+              vp.next_tile();
             }
             if (x < n) {
-              if (two) issue_s(1, g + x);
-              tc_commit(&empty[(2 * (g + x)) % S]);
+              if (two) issue_s(1, kp);
+              tc_commit(&empty[kp.slot]);
+              kp.next_tile();
               if (x == n - 1) tc_commit(q_empty);
             }
           }
         }
-        g += n;
         ++nq;
       }
       tc_commit(drain);
@@ -671,9 +791,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 have_mask = true;
                 if (!ok) break;
               }
-              ok = softmax_tile<D, S, true>(a, p, ctl, wk, st, cnt, first, 2 * (g + x) + 1, kt * kKeys);
+              ok = masked_tile<D, S>(a, p, ctl, st, cnt, first, 2 * (g + x) + 1, kt * kKeys - wk.base());
             } else {
-              ok = softmax_tile<D, S, false>(a, p, ctl, wk, st, cnt, first, 2 * (g + x) + 1, kt * kKeys);
+              ok = softmax_tile<D>(a, p, ctl, st, cnt, first);
             }
             ++cnt;
           }
@@ -690,8 +810,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool whole = wk.whole();
         // partial results: slot 2 x + 1 for a unit that starts here and goes
         // on, 2 x for one that started before
-        const long long prow = (static_cast<long long>(blockIdx.x) * 2 + (wk.k0 == 0 ? 1 : 0)) * (SPLIT ? kRows : 2 * kRows) +
-                               (SPLIT ? 0 : t * kRows) + row;
+        constexpr int kSlotRows = SPLIT ? kRows : 2 * kRows;
+        const long long slot = static_cast<long long>(blockIdx.x) * 2 + (wk.k0 == 0 ? 1 : 0);
+        const int srow = (SPLIT ? 0 : t * kRows) + row;
+        float *part_o = p.part_o + slot * (kSlotRows * D) + srow;  // [column][row]: a warp's rows side by side
+        const long long prow = slot * kSlotRows + srow;
         if constexpr (SPLIT) {
           if (works) {
             xm[t * kRows + row] = st.m;
@@ -735,9 +858,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                   dst[x] = make_uint4(pack_bf16x2(r[8 * x], r[8 * x + 1]), pack_bf16x2(r[8 * x + 2], r[8 * x + 3]),
                                       pack_bf16x2(r[8 * x + 4], r[8 * x + 5]), pack_bf16x2(r[8 * x + 6], r[8 * x + 7]));
               } else {
-                float4 *dst = reinterpret_cast<float4 *>(p.part_o + prow * D + ch);
 #pragma unroll
-                for (int x = 0; x < 4; ++x) dst[x] = make_float4(r[4 * x], r[4 * x + 1], r[4 * x + 2], r[4 * x + 3]);
+                for (int x = 0; x < 16; ++x) part_o[(ch + x) * kSlotRows] = r[x];
               }
             }
             if (store && t == 0) {
@@ -769,9 +891,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 dst[x] = make_uint4(pack_bf16x2(r[8 * x], r[8 * x + 1]), pack_bf16x2(r[8 * x + 2], r[8 * x + 3]),
                                     pack_bf16x2(r[8 * x + 4], r[8 * x + 5]), pack_bf16x2(r[8 * x + 6], r[8 * x + 7]));
             } else {
-              float4 *dst = reinterpret_cast<float4 *>(p.part_o + prow * D + ch);
 #pragma unroll
-              for (int x = 0; x < 4; ++x) dst[x] = make_float4(r[4 * x], r[4 * x + 1], r[4 * x + 2], r[4 * x + 3]);
+              for (int x = 0; x < 16; ++x) part_o[(ch + x) * kSlotRows] = r[x];
             }
           }
           if (store) {
@@ -800,100 +921,126 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Merge the partial results of units cut by a run's end: one block per row,
-// the runs dealt to its warps, a lane owns D / 32 columns.
-//   O = sum 2^(lse_s - M) O_s / sum 2^(lse_s - M)
-template <int D, int WARPS>
+// Merge the partial results of units cut by a run's end:
+//   O = sum 2^(lse_s - M) O_s / sum 2^(lse_s - M).
+// A lane takes a row and 16 columns, a warp ROWS rows and 16 * 32 / ROWS
+// columns of one unit's row tile; the block's WARPS warps deal the runs out
+// among themselves and add up through shared memory, so that a unit cut into
+// a hundred runs is merged in a few round trips.
+constexpr int kMergeCols = 16;
+
+template <int D, int ROWS, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32) fa_tree_merge_kernel(const TreeParams p) {
-  constexpr int CPL = D / 32;
-  __shared__ long long sums[WARPS][2];
-  __shared__ float sh_m[WARPS], sh_l[WARPS], sh_o[WARPS][D];
+  constexpr int kCols = kMergeCols * 32 / ROWS;  // of a block
+  __shared__ float sh_m[WARPS][32], sh_l[WARPS][32], sh_o[WARPS][32][kMergeCols + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int heads_rows = p.G * p.Nt;
-  const int unit = blockIdx.x / heads_rows, r = blockIdx.x % heads_rows;
-  const int b = unit / p.Hkv, hk = unit % p.Hkv, gh = r / p.Nt, node = r % p.Nt;
+  const int used = p.gpt * p.Nt, row_groups = (used + ROWS - 1) / ROWS;
+  int x = blockIdx.x;
+  const int c0 = x % (D / kCols) * kCols + lane / ROWS * kMergeCols;
+  x /= D / kCols;
+  const int row = x % row_groups * ROWS + lane % ROWS;
+  x /= row_groups;
+  const int mtile = x % p.row_tiles, unit = x / p.row_tiles;
+  const int b = unit / p.Hkv, hk = unit - b * p.Hkv;
+  const int gh = mtile * p.gpt + row / p.Nt, node = row % p.Nt;
+  const bool on = row < used && gh < p.G;
   // first tile of the unit and the number of all tiles
   long long before = 0, total = 0;
+  int tiles = tiles_of(p.Nk);
   if (!p.cache_len) {
-    const long long per_b = static_cast<long long>(p.Hkv) * tiles_of(p.Nk);
-    before = per_b * b;
-    total = per_b * p.B;
+    before = static_cast<long long>(tiles) * b;
+    total = static_cast<long long>(tiles) * p.B;
   } else {
-    for (int x = threadIdx.x; x < p.B; x += WARPS * 32) {
-      const int n = tiles_of(cache_rows(p.cache_len, x, p.Nk));
+    for (int y = lane; y < p.B; y += 32) {
+      const int n = tiles_of(cache_rows(p.cache_len, y, p.Nk));
       total += n;
-      if (x < b) before += n;
+      if (y < b) before += n;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       total += __shfl_xor_sync(0xffffffffu, total, o);
       before += __shfl_xor_sync(0xffffffffu, before, o);
     }
-    if (WARPS > 1) {
-      if (lane == 0) sums[warp][0] = total, sums[warp][1] = before;
-      __syncthreads();
-      total = before = 0;
-      for (int w = 0; w < WARPS; ++w) total += sums[w][0], before += sums[w][1];
-    }
-    total *= p.Hkv;
-    before *= p.Hkv;
+    tiles = tiles_of(cache_rows(p.cache_len, b, p.Nk));
   }
-  const int tiles = tiles_of(cache_rows(p.cache_len, b, p.Nk));
-  const long long u0 = before + static_cast<long long>(hk) * tiles, u1 = u0 + tiles - 1;
+  total *= p.Hkv;
+  const long long u0 = before * p.Hkv + static_cast<long long>(hk) * tiles, u1 = u0 + tiles - 1;
   const long long runs = runs_of(p, total);
-  const int c0 = static_cast<int>(((u0 + 1) * runs - 1) / total);  // the run that holds tile u0
-  const int c1 = static_cast<int>(((u1 + 1) * runs - 1) / total);
-  if (c0 == c1) return;  // written by its CTA
-  const int mtile = gh / p.gpt, row = (gh % p.gpt) * p.Nt + node;
-  const int group = p.split ? 0 : mtile / 2;
-  const int slot_rows = p.split ? kRows : 2 * kRows;
+  const int r0 = static_cast<int>(divide((u0 + 1) * runs - 1, total));  // the run that holds tile u0
+  const int r1 = static_cast<int>(divide((u1 + 1) * runs - 1, total));
+  cudaGridDependencySynchronize();  // (launched while the main kernel still runs)
+  if (r0 == r1) return;             // written by its CTA
+
+  const int group = p.split ? 0 : mtile / 2, slot_rows = p.split ? kRows : 2 * kRows;
   const int in_slot = (p.split ? 0 : (mtile & 1) * kRows) + row;
-  float m = -INFINITY, l = 0.0f, o[CPL];
+  float m = -INFINITY, l = 0.0f, o[kMergeCols];
 #pragma unroll
-  for (int x = 0; x < CPL; ++x) o[x] = 0.0f;
-#pragma unroll 4
-  for (int c = c0 + warp; c <= c1; c += WARPS) {
-    const long long pr =
-        (static_cast<long long>(c * p.groups + group) * 2 + (c == c0 ? 1 : 0)) * slot_rows + in_slot;
-    const float s = p.part_lse[pr];
-    float v[CPL];
+  for (int y = 0; y < kMergeCols; ++y) o[y] = 0.0f;
+#pragma unroll 2
+  for (int r = r0 + warp; r <= r1; r += WARPS) {
+    const long long slot = static_cast<long long>(r * p.groups + group) * 2 + (r == r0 ? 1 : 0);
+    const float s = on ? p.part_lse[slot * slot_rows + in_slot] : -INFINITY;
+    const float *part = p.part_o + (slot * D + c0) * slot_rows + in_slot;
+    float v[kMergeCols];
 #pragma unroll
-    for (int x = 0; x < CPL; ++x) v[x] = p.part_o[pr * D + lane * CPL + x];
+    for (int y = 0; y < kMergeCols; ++y) v[y] = on ? part[y * slot_rows] : 0.0f;
     const float mn = fmaxf(m, s);
-    if (mn == -INFINITY) continue;
-    const float fa = m == -INFINITY ? 0.0f : ex2(m - mn), fb = s == mn ? 1.0f : (s == -INFINITY ? 0.0f : ex2(s - mn));
+    const float fa = m == mn ? 1.0f : (m == -INFINITY ? 0.0f : ex2(m - mn));
+    const float fb = s == -INFINITY ? 0.0f : (s == mn ? 1.0f : ex2(s - mn));
     l = l * fa + fb;
 #pragma unroll
-    for (int x = 0; x < CPL; ++x) o[x] = o[x] * fa + v[x] * fb;
+    for (int y = 0; y < kMergeCols; ++y) o[y] = o[y] * fa + v[y] * fb;
     m = mn;
   }
-  if (WARPS > 1) {
-    if (lane == 0) sh_m[warp] = m, sh_l[warp] = l;
+  sh_m[warp][lane] = m;
+  sh_l[warp][lane] = l;
 #pragma unroll
-    for (int x = 0; x < CPL; ++x) sh_o[warp][lane * CPL + x] = o[x];
-    __syncthreads();
-    if (warp > 0) return;
-    float M = -INFINITY;
-    for (int w = 0; w < WARPS; ++w) M = fmaxf(M, sh_m[w]);
-    l = 0.0f;
+  for (int y = 0; y < kMergeCols; ++y) sh_o[warp][lane][y] = o[y];
+  __syncthreads();
+  if (warp > 0) return;
+  float M = -INFINITY;
 #pragma unroll
-    for (int x = 0; x < CPL; ++x) o[x] = 0.0f;
-    for (int w = 0; w < WARPS; ++w) {
-      const float f = sh_m[w] == M ? 1.0f : (sh_m[w] == -INFINITY ? 0.0f : ex2(sh_m[w] - M));
-      l += sh_l[w] * f;
+  for (int w = 0; w < WARPS; ++w) M = fmaxf(M, sh_m[w][lane]);
+  l = 0.0f;
 #pragma unroll
-      for (int x = 0; x < CPL; ++x) o[x] += sh_o[w][lane * CPL + x] * f;
-    }
-    m = M;
+  for (int y = 0; y < kMergeCols; ++y) o[y] = 0.0f;
+  for (int w = 0; w < WARPS; ++w) {
+    const float mw = sh_m[w][lane], f = mw == -INFINITY ? 0.0f : (mw == M ? 1.0f : ex2(mw - M));
+    l += sh_l[w][lane] * f;
+#pragma unroll
+    for (int y = 0; y < kMergeCols; ++y) o[y] += sh_o[w][lane][y] * f;
   }
-  const bool any = m != -INFINITY && m != INFINITY;  // +inf: padding
+  if (!on) return;
+  const bool any = M != -INFINITY && M != INFINITY;  // +inf: padding
+  const float inv = any ? 1.0f / l : 0.0f;
   const int h = hk * p.G + gh;
-  __nv_bfloat16 *dst = p.o + b * p.so.b + h * p.so.h + node * p.so.n + lane * CPL;
+  uint4 *dst = reinterpret_cast<uint4 *>(p.o + b * p.so.b + h * p.so.h + node * p.so.n + c0);
 #pragma unroll
-  for (int x = 0; x < CPL; x += 2)
-    *reinterpret_cast<uint32_t *>(dst + x) = any ? pack_bf16x2(o[x] / l, o[x + 1] / l) : 0u;
-  if (lane == 0)
-    p.lse[(static_cast<long long>(b) * p.H + h) * p.Nt + node] = any ? (m + log2f(l)) * kLn2 : -INFINITY;
+  for (int y = 0; y < kMergeCols; y += 8)
+    dst[y / 8] = any ? make_uint4(pack_bf16x2(o[y] * inv, o[y + 1] * inv), pack_bf16x2(o[y + 2] * inv, o[y + 3] * inv),
+                                  pack_bf16x2(o[y + 4] * inv, o[y + 5] * inv), pack_bf16x2(o[y + 6] * inv, o[y + 7] * inv))
+                     : make_uint4(0u, 0u, 0u, 0u);
+  if (c0 == 0)
+    p.lse[(static_cast<long long>(b) * p.H + h) * p.Nt + node] = any ? (M + log2f(l)) * kLn2 : -INFINITY;
+}
+
+// The merge is launched as a dependent of the main kernel: its blocks find
+// their unit while that still runs.
+template <int D, int ROWS, int WARPS>
+cudaError_t launch_merge(const TreeParams &p, cudaStream_t stream) {
+  const long long blocks = static_cast<long long>(p.B) * p.Hkv * p.row_tiles * ((p.gpt * p.Nt + ROWS - 1) / ROWS) *
+                           (D / (kMergeCols * 32 / ROWS));
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(WARPS * 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fa_tree_merge_kernel<D, ROWS, WARPS>, p);
 }
 
 template <int D, bool SPLIT>
@@ -906,16 +1053,20 @@ cudaError_t launch_tree_t(const CUtensorMap &tq, const CUtensorMap &tk, const CU
   kern<<<static_cast<unsigned>(p.ranges) * p.groups, kThreads, L::kRequest, stream>>>(tq, tk, tv, p);
   e = cudaGetLastError();
   if (e != cudaSuccess || !merge) return e;
-  const unsigned rows = static_cast<unsigned>(p.B) * p.Hkv * p.G * p.Nt;
-  // runs a unit may be cut into
-  if (p.ranges / (p.B * p.Hkv) >= 4)
-    fa_tree_merge_kernel<D, 8><<<rows, 256, 0, stream>>>(p);
-  else
-    fa_tree_merge_kernel<D, 1><<<rows, 32, 0, stream>>>(p);
-  return cudaGetLastError();
+  // a unit is cut into about ranges / units + 1 runs
+  const bool many = p.ranges >= 2ll * p.B * p.Hkv;
+  if (SPLIT && p.gpt * p.Nt <= 8)
+    return many ? launch_merge<D, 8, 8>(p, stream) : launch_merge<D, 8, 2>(p, stream);
+  return many ? launch_merge<D, 32, 8>(p, stream) : launch_merge<D, 32, 2>(p, stream);
 }
 
 }  // namespace
+
+// Short caches are not cut inside a unit: up to 8 tiles take about as long as
+// the merge that their cutting would need (B1 H8 Hkv2 Nt7 on the device: Nk1000
+// 13.7 us cut into 16 runs, 15.4 whole; Nk500 13.5 and 12.0), and without a
+// workspace and a second launch the whole call goes from 29 to 24 us.
+constexpr int kWholeTiles = 8;
 
 TreePlan plan_tree(int B, int H, int Hkv, int Nt, int Nk) {
   TreePlan pl{};
@@ -924,12 +1075,15 @@ TreePlan plan_tree(int B, int H, int Hkv, int Nt, int Nk) {
   pl.row_tiles = (G + pl.gpt - 1) / pl.gpt;
   pl.split = pl.row_tiles == 1 ? 1 : 0;
   pl.groups = (pl.row_tiles + 1) / 2;
-  const long long tiles = static_cast<long long>(B) * Hkv * ((Nk + kKeys - 1) / kKeys);
+  const int per_unit = (Nk + kKeys - 1) / kKeys;
+  const long long units = static_cast<long long>(B) * Hkv;
+  pl.whole = per_unit <= kWholeTiles ? 1 : 0;
+  const long long pieces = pl.whole ? units : units * per_unit;
   long long ranges = kModelCtas / pl.groups;
   if (ranges < 1) ranges = 1;
-  if (ranges > tiles) ranges = tiles;
+  if (ranges > pieces) ranges = pieces;
   pl.ranges = static_cast<int>(ranges);
-  pl.merge = ranges > 1 && Nk > kKeys;
+  pl.merge = ranges > 1 && !pl.whole;
   pl.part_rows = pl.merge ? static_cast<size_t>(ranges) * pl.groups * 2 * (pl.split ? kRows : 2 * kRows) : 0;
   return pl;
 }

@@ -58,6 +58,9 @@ def check(q, k, v, par, lens, o, lse, scale, what):
     (1, 20, 1, 100, 901, 64, "bhnd"),
     (1, 2, 2, 65, 20001, 128, "bhnd"),
     (3, 6, 2, 12, 5003, 64, "bnhd"),
+    (40, 2, 1, 3, 300, 64, "bhnd"),
+    (37, 4, 2, 4, 1700, 64, "bhnd"),
+    (400, 1, 1, 2, 140, 64, "bhnd"),
 ])
 def test_tree(B, H, Hkv, Nt, Nk, d, layout):
     g = ref.gen(Nt + Nk)
