@@ -18,8 +18,8 @@
 // TMEM owner, warp 10 the tree's visibility table, warp 11 idle.  With one
 // row tile the two softmax warpgroups take alternate key tiles of it (each
 // with its own maximum, sum and O, merged at the end of the unit); with two
-// row tiles each takes its own.  TMEM columns: S_t at 128 t, O_t at 256 + d t,
-// P (bf16) over S.
+// row tiles each takes its own.  TMEM columns: the S buffers (two of 128, three
+// at d = 64 with one row tile), P (bf16) over S, and O_0, O_1 in the last 2 d.
 //
 // The tree.  Only a unit's last tiles hold nodes.  Warp 10 turns parents into
 // one bit row per node (its ancestors and itself) by pointer doubling, at
@@ -43,10 +43,11 @@ constexpr int kModelCtas = 152;  // GB300's SMs: the grid the runs are cut for
 constexpr float kRescaleThreshold = 8.0f;  // a row's maximum moves only when exceeded by more (log2 units)
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr uint32_t kTmemCols = 512;
-// 104 registers for the control warps and 200 for the softmax: the split of
-// the forward kernel, whose roles these are (128 * 104 + 256 * 200 is what
-// 384 threads were launched with, 168 each).
-constexpr uint32_t kRegsControl = 104, kRegsSoftmax = 200;
+// Register split: 384 threads launched with 168 each; no role spills at 152 for
+// the control warps and 176 for the softmax.  (At 104 and 200, the forward
+// kernel's split, the issuer and the producer spill: B2 H32 Hkv8 Nt64 Nk65536
+// d128 139 us against 127.)
+constexpr uint32_t kRegsControl = 152, kRegsSoftmax = 176;
 static_assert(128 * kRegsControl + 256 * kRegsSoftmax <= kThreads * 168, "register split");
 
 template <int D, bool SPLIT>
@@ -55,6 +56,14 @@ struct TreeLayout {
   static constexpr uint32_t kTile = kKeys * D * 2;                // a Q, K or V tile
   static constexpr int kQTiles = SPLIT ? 1 : 2;
   static constexpr int kSlots = D == 128 ? 5 : 10;                // ring of K and V tiles
+  // S buffers.  With one row tile the key tiles take them in turn; a third one,
+  // where TMEM has room for it, lets a warpgroup's next scores be formed while
+  // it still works on the last ones: with few rows and 32 KB tiles that chain
+  // and not HBM would set the pace (B2 H8 Hkv8 Nt1 Nk65536 d64: 68 us with
+  // two, 65 with three).
+  static constexpr int kSBufs = SPLIT && D == 64 ? 3 : 2;
+  static constexpr uint32_t kO = kTmemCols - 2 * D;               // first O column
+  static_assert(kSBufs * 128 <= kTmemCols - 2 * D, "TMEM columns");
   // first the small things, then (1 KB aligned) the tiles
   static constexpr uint32_t kOffBits = 0;                         // node bit rows, see bit_row()
   static constexpr uint32_t kOffDead = kOffBits + 32 * (1 + 2 + 3 + 4) * 4;
@@ -63,8 +72,8 @@ struct TreeLayout {
   static constexpr uint32_t kOffScan = kOffRange + 32;            // 12 warps' sums
   static constexpr uint32_t kOffStats = kOffScan + 12 * 8;        // SPLIT: m, l, lb of both warpgroups
   static constexpr uint32_t kOffBar = kOffStats + (SPLIT ? 2 * 3 * kRows * 4 : 0);
-  // full[S], empty[S], s_full[2], p_ready[2], pv_done[2], q_full, q_empty, mask_full, mask_empty, drain
-  static constexpr int kNumBars = 2 * kSlots + 6 + 5;
+  // full[S], empty[S], s_full[kSBufs], p_ready[2], pv_done[2], q_full, q_empty, mask_full, mask_empty, drain
+  static constexpr int kNumBars = 2 * kSlots + kSBufs + 4 + 5;
   static constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;    // TMEM address, abort flag
   static constexpr uint32_t kSmall = (kOffMisc + 16 + 15) / 16 * 16;
   static constexpr uint32_t kTiles = (kQTiles + kSlots) * kTile;
@@ -346,7 +355,8 @@ struct RowState {
 
 struct SoftmaxArgs {
   uint64_t *s_full, *p_ready, *pv_done, *full, *mask_full;
-  uint32_t tS, tO;  // this warpgroup's columns, lane base added
+  uint32_t s_phase;  // of the tile's S buffer
+  uint32_t tS, tO;   // its columns and this warpgroup's O, lane base added
   uint8_t *ring;    // K and V slots
   const uint32_t *bits, *dead;
   int node;         // tree node of this thread's row, -1 if the row is unused
@@ -414,7 +424,7 @@ template <int D>
 __device__ __forceinline__ bool softmax_tile(const SoftmaxArgs &a, const TreeParams &p, const WaitCtl &ctl,
                                              RowState &st, uint32_t cnt, bool first) {
   const float c = p.scale_log2;
-  if (!__all_sync(0xffffffffu, mbar_wait(a.s_full, cnt & 1, ctl, kSiteSFull))) return false;
+  if (!__all_sync(0xffffffffu, mbar_wait(a.s_full, a.s_phase, ctl, kSiteSFull))) return false;
   tc_fence_after();
   uint32_t s[4][32];
 #pragma unroll
@@ -471,7 +481,7 @@ template <int D, int SLOTS>
 __device__ __forceinline__ bool masked_tile(const SoftmaxArgs &a, const TreeParams &p, const WaitCtl &ctl,
                                             RowState &st, uint32_t cnt, bool first, uint32_t e_v, int n0) {
   const float c = p.scale_log2;
-  if (!__all_sync(0xffffffffu, mbar_wait(a.s_full, cnt & 1, ctl, kSiteSFull))) return false;
+  if (!__all_sync(0xffffffffu, mbar_wait(a.s_full, a.s_phase, ctl, kSiteSFull))) return false;
   tc_fence_after();
   const int i = a.node;
   const bool live = i >= 0 && !((a.dead[i >> 5] >> (i & 31)) & 1u);
@@ -541,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fa_tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const TreeParams p) {
   using L = TreeLayout<D, SPLIT>;
-  constexpr int S = L::kSlots;
+  constexpr int S = L::kSlots, NS = L::kSBufs;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *small = smem_raw;
   uint8_t *tiles = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + L::kSmall + 1023) &
@@ -552,8 +562,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   RunStart *run = reinterpret_cast<RunStart *>(small + L::kOffRange);
   uint64_t *full = reinterpret_cast<uint64_t *>(small + L::kOffBar);
   uint64_t *empty = full + S;
-  uint64_t *s_full = empty + S;    // [2 warpgroups]
-  uint64_t *p_ready = s_full + 2;  // [2]
+  uint64_t *s_full = empty + S;          // [buffer]
+  uint64_t *p_ready = s_full + NS;       // [warpgroup]
   uint64_t *pv_done = p_ready + 2;  // [2]
   uint64_t *q_full = pv_done + 2, *q_empty = q_full + 1;
   uint64_t *mask_full = q_empty + 1, *mask_empty = mask_full + 1, *drain = mask_empty + 1;
@@ -574,8 +584,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
+    for (int i = 0; i < NS; ++i) mbar_init(&s_full[i], 1);
     for (int t = 0; t < 2; ++t) {
-      mbar_init(&s_full[t], 1);
       mbar_init(&p_ready[t], warps);
       mbar_init(&pv_done[t], 1);
     }
@@ -663,29 +673,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       Place kp{0, 0}, vp{1, 0};
       uint32_t nq = 0;            // Q loads so far
       uint32_t cnt[2] = {0, 0};   // P V products per warpgroup so far
+      uint32_t ss = 0, ps = 0;    // buffers of the next S and of the next P V product (one row tile)
       bool ok = true;
       auto full_wait = [&](const Place &x, int site) {
         const bool r = mbar_wait(&full[x.slot], x.phase, ctl, site);
         tc_fence_after();
         return r;
       };
-      // S of warpgroup t = its Q tile times the K tile at x
-      auto issue_s = [&](int t, const Place &x) {
-        const uint64_t dq = desc_add(dQ, (SPLIT ? 0 : t) * L::kTile), dk = desc_add(dK, x.slot * L::kTile);
+      // S in buffer s = the warpgroup's Q tile times the K tile at x
+      auto issue_s = [&](uint32_t s, const Place &x) {
+        const uint64_t dq = desc_add(dQ, (SPLIT ? 0 : s) * L::kTile), dk = desc_add(dK, x.slot * L::kTile);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          mma_ss(tmem + t * 128, desc_add(dq, kmajor_step(kk, kRows)), desc_add(dk, kmajor_step(kk, kKeys)), kIdS,
+          mma_ss(tmem + s * 128, desc_add(dq, kmajor_step(kk, kRows)), desc_add(dk, kmajor_step(kk, kKeys)), kIdS,
                  kk > 0 ? 1u : 0u);
-        tc_commit(&s_full[t]);
+        tc_commit(&s_full[s]);
       };
-      auto issue_pv = [&](int t, const Place &x, bool first) -> bool {
+      // O_t += P (over S in buffer s) times the V tile at x
+      auto issue_pv = [&](int t, uint32_t s, const Place &x, bool first) -> bool {
         if (!mbar_wait(&p_ready[t], cnt[t] & 1, ctl, kSitePReady)) return false;
         ++cnt[t];
         tc_fence_after();
         const uint64_t dv = desc_add(dV, x.slot * L::kTile);
 #pragma unroll
         for (int kk = 0; kk < kKeys / 16; ++kk)
-          mma_ts(tmem + 256 + t * D, tmem + t * 128 + kk * 8, desc_add(dv, mnmajor_step(kk)), kIdO,
+          mma_ts(tmem + L::kO + t * D, tmem + s * 128 + kk * 8, desc_add(dv, mnmajor_step(kk)), kIdO,
                  (!first || kk > 0) ? 1u : 0u);
         tc_commit(&pv_done[t]);
         return true;
@@ -696,31 +708,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         if constexpr (SPLIT) {
           // tile x of the segment belongs to warpgroup x & 1; its S is issued
-          // right after the P V product two tiles before it
-          for (int x = 0; ok && x < n + 2; ++x) {
-            if (x >= 2) {
-              ok = full_wait(vp, kSiteVFull) && issue_pv(x & 1, vp, x < 4);
+          // right after the P V product that frees its buffer
+          for (int x = 0; ok && x < n + NS; ++x) {
+            const int y = x - NS;
+            if (y >= 0 && y < n) {
+              ok = full_wait(vp, kSiteVFull) && issue_pv(y & 1, ps, vp, y < 2);
               if (ok) tc_commit(&empty[vp.slot]);
               vp.next_tile();
+              if (++ps == NS) ps = 0;
             }
             if (ok && x < n) {
               if (!(ok = full_wait(kp, kSiteKFull))) break;
-              issue_s(x & 1, kp);
+              issue_s(ss, kp);
               tc_commit(&empty[kp.slot]);
               kp.next_tile();
+              if (++ss == NS) ss = 0;
               if (x == n - 1) tc_commit(q_empty);
             }
           }
         } else {
           for (int x = 0; ok && x <= n; ++x) {
             if (x > 0 && !(ok = full_wait(vp, kSiteVFull))) break;
-            if (x > 0 && !(ok = issue_pv(0, vp, x == 1))) break;
+            if (x > 0 && !(ok = issue_pv(0, 0, vp, x == 1))) break;
             if (x < n) {
               if (!(ok = full_wait(kp, kSiteKFull))) break;
               issue_s(0, kp);
             }
             if (x > 0) {
-              if (two && !(ok = issue_pv(1, vp, x == 1))) break;
+              if (two && !(ok = issue_pv(1, 1, vp, x == 1))) break;
               tc_commit(&empty[vp.slot]);
               vp.next_tile();
             }
@@ -766,7 +781,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       a.full = full;
       a.mask_full = mask_full;
       a.tS = tmem + t * 128 + lane_base;
-      a.tO = tmem + 256 + t * D + lane_base;
+      a.tO = tmem + L::kO + t * D + lane_base;
       a.ring = ring;
       a.bits = bits;
       a.dead = dead;
@@ -784,6 +799,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int step = SPLIT ? 2 : 1;
           for (int x = SPLIT ? t : 0; ok && x < n; x += step) {
             const int kt = wk.k0 + x;
+            if (SPLIT) {
+              const uint32_t q = g + x, s = q % NS;
+              a.s_full = &s_full[s];
+              a.s_phase = (q / NS) & 1;
+              a.tS = tmem + s * 128 + lane_base;
+            } else {
+              a.s_phase = cnt & 1;
+            }
             const bool first = x < step;
             if (kt >= mfrom) {
               if (!have_mask) {
@@ -832,7 +855,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool any = l > 0.0f && !padding;
             const float inv = any ? 1.0f / lb : 0.0f;
             const float g0 = f0 * inv, g1 = f1 * inv;
-            const uint32_t t0 = tmem + 256 + lane_base, t1 = t0 + D;
+            const uint32_t t0 = tmem + L::kO + lane_base, t1 = t0 + D;
             // each warpgroup writes half of the columns
 #pragma unroll 1
             for (int ch = t * (D / 2); ch < (t + 1) * (D / 2); ch += 16) {

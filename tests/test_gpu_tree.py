@@ -247,3 +247,47 @@ def test_refusals():
         fa_fwd_tree(q.repeat(1, 1, 17, 1), k, v, ref.ints([-1] * 136))    # more than 128 nodes
     with pytest.raises(TypeError):
         fa_fwd_tree(q.half(), k, v, par)
+
+
+def test_workspace_taken_by_the_library():
+    """The C call with a null workspace takes it on the stream; two captured graphs of it do not share it."""
+    import ctypes
+
+    from exact_attention_48_gb300 import fa_key_weights
+    from exact_attention_48_gb300.binding import library
+    g = ref.gen(57)
+    B, H, Hkv, Nt, Nk, d = 2, 4, 2, 9, 2000, 128
+    lib = library()
+    st = lambda t: (ctypes.c_int64 * 3)(*t.stride()[:3])  # noqa: E731
+    sets = []
+    for _ in range(2):
+        q, k, v = ref.draw(g, B, H, Nt, d), ref.draw(g, B, Hkv, Nk, d), ref.draw(g, B, Hkv, Nk, d)
+        par = trees(g, B, Nt)
+        o, lse = torch.empty_like(q), torch.empty(B, H, Nt, device="cuda")
+
+        def call():
+            return lib.fa_fwd_tree(q.data_ptr(), st(q), k.data_ptr(), st(k), v.data_ptr(), st(v), o.data_ptr(), st(o),
+                                   lse.data_ptr(), par.data_ptr(), Nt, None, B, H, Hkv, Nt, Nk, d, 1 / math.sqrt(d),
+                                   None, 0, torch.cuda.current_stream().cuda_stream)
+        assert call() == 0
+        want = fa_fwd_tree(q, k, v, par)
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            assert call() == 0
+        sets.append((o, lse, want, graph, (q, k, v, par)))  # a graph does not keep its inputs alive
+    for o, lse, *_ in sets:
+        o.zero_(), lse.zero_()
+    for i in (0, 1, 1, 0):
+        sets[i][3].replay()
+    torch.cuda.synchronize()
+    for o, lse, want, *_ in sets:
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    # the key weights' partial sums likewise
+    q, k = ref.draw(g, 1, 2, 700, d), ref.draw(g, 1, 1, 600, d)
+    lse = torch.full((1, 2, 700), 6.0, device="cuda")
+    assert lib.fa_key_weights_workspace_bytes(1, 2, 1, 700, 600, d) > 0
+    w = torch.empty(1, 1, 600, device="cuda")
+    rc = lib.fa_key_weights(q.data_ptr(), st(q), k.data_ptr(), st(k), lse.data_ptr(), None, w.data_ptr(), None, 1, 2, 1,
+                            700, 600, d, 1, 0.1, None, 0, torch.cuda.current_stream().cuda_stream)
+    assert rc == 0 and torch.equal(w, fa_key_weights(q, k, lse, None, True, 0.1))
