@@ -45,6 +45,8 @@ struct TreeParams {
   int *status;
   float *part_o;              // [2 * ctas][d][slot_rows], normalised
   float *part_lse;            // [2 * ctas][slot_rows], log2 units; +inf marks padding
+  int4 *cuts;                 // units cut by a run's end: (b, hk, first run, last run), b = -1: none.  An entry
+  int cuts_by_unit;           // per unit, or, where those are more, per run that a cut unit starts in
   int B, H, Hkv, G, Nt, Nk, d;
   int gpt, row_tiles, groups, ranges, split;
   int whole;                  // runs end at units' ends: no partial results

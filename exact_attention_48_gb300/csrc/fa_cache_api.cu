@@ -318,7 +318,7 @@ fa_status_t fa_rope_append(const void *q, const int64_t *q_strides, const void *
 size_t fa_tree_workspace_bytes(int B, int H, int Hkv, int Nt, int Nk, int d) {
   if (check_tree(B, H, Hkv, Nt, Nk, d, 1.0f) != FA_OK) return 0;
   const TreePlan pl = plan_tree(B, H, Hkv, Nt, Nk);
-  return pl.merge ? round256(pl.part_rows * d * 4) + round256(pl.part_rows * 4) : 0;
+  return pl.merge ? round256(pl.part_rows * d * 4) + round256(pl.part_rows * 4) + round256(pl.ranges * sizeof(int4)) : 0;
 }
 
 fa_status_t fa_fwd_tree(const void *q, const int64_t *q_strides, const void *k, const int64_t *k_strides,
@@ -362,8 +362,11 @@ fa_status_t fa_fwd_tree(const void *q, const int64_t *q_strides, const void *k, 
   p.par_b = parents_stride;
   p.cache_len = cache_seqlens;
   p.part_o = static_cast<float *>(ws.ptr);
-  p.part_lse = need ? reinterpret_cast<float *>(static_cast<uint8_t *>(ws.ptr) + round256(pl.part_rows * d * 4))
-                    : nullptr;
+  if (need) {
+    uint8_t *at = static_cast<uint8_t *>(ws.ptr) + round256(pl.part_rows * d * 4);
+    p.part_lse = reinterpret_cast<float *>(at);
+    p.cuts = reinterpret_cast<int4 *>(at + round256(pl.part_rows * 4));
+  }
   p.B = B;
   p.H = H;
   p.Hkv = Hkv;
@@ -377,6 +380,7 @@ fa_status_t fa_fwd_tree(const void *q, const int64_t *q_strides, const void *k, 
   p.ranges = pl.ranges;
   p.split = pl.split;
   p.whole = pl.whole;
+  p.cuts_by_unit = static_cast<long long>(B) * Hkv <= pl.ranges ? 1 : 0;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.neg = scale < 0.0f ? 1 : 0;
   const bool launched = launch_tree(tq, tk, tv, p, pl.merge, stream) == cudaSuccess;

@@ -235,6 +235,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (n.empty()) continue;
         const uint32_t kb = nk % KB, qb = nk % QB;
         if (!mbar_wait(&k_empty[kb], ((nk / KB) & 1) ^ 1, ctl, kSiteKEmpty)) break;
+#ifdef FA_TEST_SKIP_FIRST_V_LOAD
+        if (nk == 0) {  // test builds only: the first block is never loaded
+          ++nk;
+          continue;
+        }
+#endif
         mbar_arrive_expect_tx(&k_full[kb], L::kKBlock);
 #pragma unroll
         for (int t = 0; t < 2; ++t)
@@ -539,6 +545,13 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
           const int group = x / n.per_group, tile = n.first + x - group * n.per_group;
           const uint32_t qb = nq % QB;
           if (!(ok = mbar_wait(&q_empty[qb], ((nq / QB) & 1) ^ 1, ctl, kSiteQEmpty))) break;
+#ifdef FA_TEST_SKIP_FIRST_V_LOAD
+          // Test builds only: the first query tile is never loaded (see build.py).
+          if (nq == 0) {
+            ++nq;
+            continue;
+          }
+#endif
           mbar_arrive_expect_tx(&q_full[qb], q_bytes);
 #pragma unroll
           for (int s = 0; s < L::kSlabs; ++s)

@@ -59,8 +59,8 @@ struct TreeLayout {
   // S buffers.  With one row tile the key tiles take them in turn; a third one,
   // where TMEM has room for it, lets a warpgroup's next scores be formed while
   // it still works on the last ones: with few rows and 32 KB tiles that chain
-  // and not HBM would set the pace (B2 H8 Hkv8 Nt1 Nk65536 d64: 68 us with
-  // two, 65 with three).
+  // and not HBM would set the pace (B2 H8 Hkv8 Nt1 Nk65536 d64: 66 us with
+  // two, 61.5 with three and the cheaper merge).
   static constexpr int kSBufs = SPLIT && D == 64 ? 3 : 2;
   static constexpr uint32_t kO = kTmemCols - 2 * D;               // first O column
   static_assert(kSBufs * 128 <= kTmemCols - 2 * D, "TMEM columns");
@@ -69,11 +69,11 @@ struct TreeLayout {
   static constexpr uint32_t kOffDead = kOffBits + 32 * (1 + 2 + 3 + 4) * 4;
   static constexpr uint32_t kOffJump = kOffDead + 16;             // int8[128]: pointer doubling
   static constexpr uint32_t kOffRange = kOffJump + 128;           // the run's start (see RunStart)
-  static constexpr uint32_t kOffScan = kOffRange + 32;            // 12 warps' sums
+  static constexpr uint32_t kOffScan = kOffRange + 48;            // 12 warps' sums
   static constexpr uint32_t kOffStats = kOffScan + 12 * 8;        // SPLIT: m, l, lb of both warpgroups
   static constexpr uint32_t kOffBar = kOffStats + (SPLIT ? 2 * 3 * kRows * 4 : 0);
-  // full[S], empty[S], s_full[kSBufs], p_ready[2], pv_done[2], q_full, q_empty, mask_full, mask_empty, drain
-  static constexpr int kNumBars = 2 * kSlots + kSBufs + 4 + 5;
+  // full[S], empty[S], s_full[kSBufs], p_ready[2][2], pv_done[2][2], q_full, q_empty, mask_full, mask_empty, drain
+  static constexpr int kNumBars = 2 * kSlots + kSBufs + 8 + 5;
   static constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;    // TMEM address, abort flag
   static constexpr uint32_t kSmall = (kOffMisc + 16 + 15) / 16 * 16;
   static constexpr uint32_t kTiles = (kQTiles + kSlots) * kTile;
@@ -108,8 +108,9 @@ __device__ __forceinline__ long long divide(long long a, long long b) {
 struct RunStart {
   long long t, end;    // [t, end)
   long long b_start;   // first tile of batch entry b
+  long long total;     // tiles of all units
   int b;
-  int pad;
+  int runs;            // runs they are cut into
 };
 
 // The segments of a run: one per unit that it touches.
@@ -187,6 +188,8 @@ __device__ __forceinline__ bool find_run(const TreeParams &p, int c, RunStart *o
       out->end = end;
       out->b = static_cast<int>(divide(t, per_b));
       out->b_start = out->b * per_b;
+      out->total = total;
+      out->runs = static_cast<int>(runs);
     }
     __syncthreads();
     return c < runs && out->t < out->end;
@@ -205,7 +208,10 @@ __device__ __forceinline__ bool find_run(const TreeParams &p, int c, RunStart *o
       const long long t = run_start(total, c, runs), end = run_start(total, c + 1, runs);
       const int first = __ffs(__ballot_sync(0xffffffffu, t < incl)) - 1;  // (none past the last run)
       const int last = __ffs(__ballot_sync(0xffffffffu, end < incl)) - 1;
-      if (lane == 0) out->t = out->end = total;
+      if (lane == 0) {
+        out->t = out->end = out->total = total;
+        out->runs = static_cast<int>(runs);
+      }
       __syncwarp();
       if (lane == first) {
         out->t = p.whole ? unit_start(t, incl - n, tiles) : t;
@@ -260,7 +266,11 @@ __device__ __forceinline__ bool find_run(const TreeParams &p, int c, RunStart *o
     }
   }
   __syncthreads();
-  if (tid == 0 && out->end > total) out->end = total;
+  if (tid == 0) {
+    if (out->end > total) out->end = total;
+    out->total = total;
+    out->runs = static_cast<int>(runs);
+  }
   __syncthreads();
   return out->t < out->end;
 }
@@ -386,10 +396,15 @@ __device__ __forceinline__ bool move_max(RowState &st, float cand, float *alpha)
   return true;
 }
 
+// The P V product of this warpgroup's tile number k.
+__device__ __forceinline__ bool pv_wait(const SoftmaxArgs &a, const WaitCtl &ctl, uint32_t k) {
+  return mbar_wait(a.pv_done + (k & 1), (k >> 1) & 1, ctl, kSitePvDone);
+}
+
 // O rescaled where a row's maximum moved (after the P V product before it).
 template <int D>
 __device__ __forceinline__ bool rescale_o(const SoftmaxArgs &a, const WaitCtl &ctl, uint32_t cnt, float alpha) {
-  if (!__all_sync(0xffffffffu, mbar_wait(a.pv_done, (cnt - 1) & 1, ctl, kSitePvDone))) return false;
+  if (!__all_sync(0xffffffffu, pv_wait(a, ctl, cnt - 1))) return false;
   tc_fence_after();
 #pragma unroll 1
   for (int ch = 0; ch < D / 16; ++ch) {
@@ -457,7 +472,7 @@ __device__ __forceinline__ bool softmax_tile(const SoftmaxArgs &a, const TreePar
   tmem_st_wait();
   if (!first && __any_sync(0xffffffffu, grow) && !rescale_o<D>(a, ctl, cnt, alpha)) return false;
   tc_fence_before();
-  warp_arrive(a.p_ready);
+  warp_arrive(a.p_ready + (cnt & 1));
 
   st.l = st.l * alpha + (sf.x + sf.y);
   float2 sb = make_float2(0.f, 0.f);  // sum of the bf16 weights: what O is divided by
@@ -540,7 +555,7 @@ __device__ __forceinline__ bool masked_tile(const SoftmaxArgs &a, const TreePara
   }
   fence_proxy_async_smem();
   tc_fence_before();
-  warp_arrive(a.p_ready);
+  warp_arrive(a.p_ready + (cnt & 1));
   st.l = st.l * alpha + (sf.x + sf.y);
   st.lb = st.lb * alpha + (sb.x + sb.y);
   return true;
@@ -563,9 +578,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *full = reinterpret_cast<uint64_t *>(small + L::kOffBar);
   uint64_t *empty = full + S;
   uint64_t *s_full = empty + S;          // [buffer]
-  uint64_t *p_ready = s_full + NS;       // [warpgroup]
-  uint64_t *pv_done = p_ready + 2;  // [2]
-  uint64_t *q_full = pv_done + 2, *q_empty = q_full + 1;
+  // Each warpgroup's tiles take two barriers of each kind in turn.  With a third
+  // S buffer a warpgroup may be through with a tile while the product of its
+  // last one is still to come (S of tile x is issued after the product of tile
+  // x - 3): the issuer would find p_ready two phases on, and the warpgroup
+  // pv_done a phase short, and a parity wait can tell neither from the phase it
+  // wants.  On a barrier that serves every other tile the phase before is done.
+  uint64_t *p_ready = s_full + NS;       // [warpgroup][2]
+  uint64_t *pv_done = p_ready + 4;       // [warpgroup][2]
+  uint64_t *q_full = pv_done + 4, *q_empty = q_full + 1;
   uint64_t *mask_full = q_empty + 1, *mask_empty = mask_full + 1, *drain = mask_empty + 1;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(small + L::kOffMisc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(small + L::kOffMisc + 4);
@@ -586,8 +607,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < NS; ++i) mbar_init(&s_full[i], 1);
     for (int t = 0; t < 2; ++t) {
-      mbar_init(&p_ready[t], warps);
-      mbar_init(&pv_done[t], 1);
+      mbar_init(&p_ready[2 * t], warps);
+      mbar_init(&p_ready[2 * t + 1], warps);
+      mbar_init(&pv_done[2 * t], 1);
+      mbar_init(&pv_done[2 * t + 1], 1);
     }
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
@@ -610,6 +633,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool has_run = find_run(p, c, run, reinterpret_cast<long long *>(small + L::kOffScan));
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // (thread 0 writes the cuts below, when its softmax comes to them)
+  if (p.cuts && !p.cuts_by_unit && group == 0 && threadIdx.x == 0) p.cuts[c] = make_int4(-1, 0, 0, 0);
   if (!has_run) {
     if (warp == kWarpMma) tmem_dealloc(tmem, kTmemCols);
     return;
@@ -625,6 +650,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       auto load = [&](const CUtensorMap *map, int row) -> bool {
         if (!mbar_wait(&empty[sl], ph ^ 1, ctl, kSiteKvEmpty)) return false;
+#ifdef FA_TEST_SKIP_FIRST_V_LOAD
+        // Test builds only: the run's first V tile is never loaded, so the wait
+        // for it runs out and the bounded-wait path is taken.
+        if (e == 1) {
+          ++e;
+          ++sl;
+          return true;
+        }
+#endif
         mbar_arrive_expect_tx(&full[sl], L::kTile);
 #pragma unroll
         for (int x = 0; x < L::kSlabs; ++x)
@@ -691,7 +725,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       // O_t += P (over S in buffer s) times the V tile at x
       auto issue_pv = [&](int t, uint32_t s, const Place &x, bool first) -> bool {
-        if (!mbar_wait(&p_ready[t], cnt[t] & 1, ctl, kSitePReady)) return false;
+        const uint32_t bar = 2 * t + (cnt[t] & 1);
+        if (!mbar_wait(&p_ready[bar], (cnt[t] >> 1) & 1, ctl, kSitePReady)) return false;
         ++cnt[t];
         tc_fence_after();
         const uint64_t dv = desc_add(dV, x.slot * L::kTile);
@@ -699,7 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int kk = 0; kk < kKeys / 16; ++kk)
           mma_ts(tmem + L::kO + t * D, tmem + s * 128 + kk * 8, desc_add(dv, mnmajor_step(kk)), kIdO,
                  (!first || kk > 0) ? 1u : 0u);
-        tc_commit(&pv_done[t]);
+        tc_commit(&pv_done[bar]);
         return true;
       };
       while (ok && wk.next()) {
@@ -776,8 +811,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool used = row < rows_used && gh < p.G;
       SoftmaxArgs a;
       a.s_full = &s_full[t];
-      a.p_ready = &p_ready[t];
-      a.pv_done = &pv_done[t];
+      a.p_ready = &p_ready[2 * t];
+      a.pv_done = &pv_done[2 * t];
       a.full = full;
       a.mask_full = mask_full;
       a.tS = tmem + t * 128 + lane_base;
@@ -793,6 +828,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       while ((ok || SPLIT) && wk.next()) {
         const int n = wk.k1 - wk.k0, mfrom = wk.masked_from();
+        // what the merge has to do for a unit that starts here: nothing, or its
+        // runs if it goes on in the next ones
+        if (threadIdx.x == 0 && group == 0 && p.cuts && wk.k0 == 0 && (!wk.tail || p.cuts_by_unit))
+          p.cuts[p.cuts_by_unit ? wk.b * p.Hkv + wk.hk : c] =
+              wk.tail ? make_int4(-1, 0, 0, 0)
+                      : make_int4(wk.b, wk.hk, c,
+                                  static_cast<int>(divide((wk.u0 + wk.tiles) * run->runs - 1, run->total)));
         RowState st{-INFINITY, 0.0f, 0.0f};
         if (works && ok) {
           bool have_mask = false;
@@ -823,7 +865,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (ok && wk.masked() && !have_mask)
             ok = __all_sync(0xffffffffu, mbar_wait(mask_full, nmask & 1, ctl, kSiteMaskFull));
           if (ok && cnt > 0 && n > (SPLIT ? t : 0))
-            ok = __all_sync(0xffffffffu, mbar_wait(a.pv_done, (cnt - 1) & 1, ctl, kSitePvDone));
+            ok = __all_sync(0xffffffffu, pv_wait(a, ctl, cnt - 1));
         }
         tc_fence_after();
         // ---- the segment's result
@@ -944,7 +986,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Merge the partial results of units cut by a run's end:
+// Merge the partial results of units cut by a run's end (the unit that starts
+// in a run and goes on in the next ones; at most one a run):
 //   O = sum 2^(lse_s - M) O_s / sum 2^(lse_s - M).
 // A lane takes a row and 16 columns, a warp ROWS rows and 16 * 32 / ROWS
 // columns of one unit's row tile; the block's WARPS warps deal the runs out
@@ -963,36 +1006,14 @@ __global__ void __launch_bounds__(WARPS * 32) fa_tree_merge_kernel(const TreePar
   x /= D / kCols;
   const int row = x % row_groups * ROWS + lane % ROWS;
   x /= row_groups;
-  const int mtile = x % p.row_tiles, unit = x / p.row_tiles;
-  const int b = unit / p.Hkv, hk = unit - b * p.Hkv;
+  const int mtile = x % p.row_tiles;
   const int gh = mtile * p.gpt + row / p.Nt, node = row % p.Nt;
   const bool on = row < used && gh < p.G;
-  // first tile of the unit and the number of all tiles
-  long long before = 0, total = 0;
-  int tiles = tiles_of(p.Nk);
-  if (!p.cache_len) {
-    before = static_cast<long long>(tiles) * b;
-    total = static_cast<long long>(tiles) * p.B;
-  } else {
-    for (int y = lane; y < p.B; y += 32) {
-      const int n = tiles_of(cache_rows(p.cache_len, y, p.Nk));
-      total += n;
-      if (y < b) before += n;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      total += __shfl_xor_sync(0xffffffffu, total, o);
-      before += __shfl_xor_sync(0xffffffffu, before, o);
-    }
-    tiles = tiles_of(cache_rows(p.cache_len, b, p.Nk));
-  }
-  total *= p.Hkv;
-  const long long u0 = before * p.Hkv + static_cast<long long>(hk) * tiles, u1 = u0 + tiles - 1;
-  const long long runs = runs_of(p, total);
-  const int r0 = static_cast<int>(divide((u0 + 1) * runs - 1, total));  // the run that holds tile u0
-  const int r1 = static_cast<int>(divide((u1 + 1) * runs - 1, total));
   cudaGridDependencySynchronize();  // (launched while the main kernel still runs)
-  if (r0 == r1) return;             // written by its CTA
+  const int4 cut = p.cuts[x / p.row_tiles];
+  const int b = cut.x, hk = cut.y, r0 = cut.z, r1 = cut.w;
+  // nothing was cut here (b = -1); after a timeout the entry may hold anything
+  if (b < 0 || b >= p.B || hk < 0 || hk >= p.Hkv || r0 < 0 || r0 >= r1 || r1 >= p.ranges) return;
 
   const int group = p.split ? 0 : mtile / 2, slot_rows = p.split ? kRows : 2 * kRows;
   const int in_slot = (p.split ? 0 : (mtile & 1) * kRows) + row;
@@ -1047,11 +1068,11 @@ __global__ void __launch_bounds__(WARPS * 32) fa_tree_merge_kernel(const TreePar
     p.lse[(static_cast<long long>(b) * p.H + h) * p.Nt + node] = any ? (M + log2f(l)) * kLn2 : -INFINITY;
 }
 
-// The merge is launched as a dependent of the main kernel: its blocks find
-// their unit while that still runs.
+// The merge is launched as a dependent of the main kernel.
 template <int D, int ROWS, int WARPS>
 cudaError_t launch_merge(const TreeParams &p, cudaStream_t stream) {
-  const long long blocks = static_cast<long long>(p.B) * p.Hkv * p.row_tiles * ((p.gpt * p.Nt + ROWS - 1) / ROWS) *
+  const long long cuts = p.cuts_by_unit ? static_cast<long long>(p.B) * p.Hkv : p.ranges;
+  const long long blocks = cuts * p.row_tiles * ((p.gpt * p.Nt + ROWS - 1) / ROWS) *
                            (D / (kMergeCols * 32 / ROWS));
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg{};

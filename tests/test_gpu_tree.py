@@ -173,6 +173,29 @@ def test_long_cache_offsets_past_2_31():
             assert float((o[0, h, i].double() - want).abs().max()) <= 1e-2
 
 
+@pytest.mark.parametrize("H,Hkv,Nt,Nk,d", [(16, 8, 64, 9000, 64), (8, 8, 1, 9000, 64), (16, 8, 64, 9000, 128),
+                                           (32, 8, 64, 5000, 64), (32, 8, 64, 5000, 128)])
+def test_many_launches_under_load(H, Hkv, Nt, Nk, d):
+    """Hundreds of launches back to back, other copies running beside them: every one finishes in time and gives
+    the same bits (the softmax, product and load roles may overtake each other as far as their barriers let them)."""
+    g = ref.gen(58)
+    B = 4
+    q, k, v = ref.draw(g, B, H, Nt, d), ref.draw(g, B, Hkv, Nk, d), ref.draw(g, B, Hkv, Nk, d)
+    par, cl = trees(g, B, Nt), ref.ints([Nk, Nk - 5, Nk // 2, 3 * Nk // 4])
+    want, wl = fa_fwd_tree(q, k, v, par, cl)
+    a, b = torch.empty(1 << 27, device="cuda", dtype=torch.uint8), torch.empty(1 << 27, device="cuda", dtype=torch.uint8)
+    side = torch.cuda.Stream()
+    for _ in range(8):
+        with torch.cuda.stream(side):
+            for _ in range(8):
+                a.copy_(b)
+        outs = [fa_fwd_tree(q, k, v, par, cl) for _ in range(32)]
+        torch.cuda.synchronize()
+        assert fa_device_status() == 0
+        for o, lse in outs:
+            assert torch.equal(o, want) and torch.equal(lse, wl)
+
+
 def test_outputs_only_and_workspace():
     """o in a wider buffer, lse between guards, a caller's workspace: nothing else is written; runs repeat bitwise."""
     g = ref.gen(55)
