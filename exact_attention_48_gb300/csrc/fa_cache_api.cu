@@ -29,6 +29,10 @@ Range range_of(const void *p, int B, int H, int N, int d, const Strides &s) {
 }
 bool meet(const Range &a, const Range &b) { return spans_overlap(a.lo, a.hi, b.lo, b.hi); }
 
+// A stride of an int32 argument: up to a terabyte's elements, as other strides
+// (products with it stay within 64 bits).
+bool row_stride(int64_t s) { return s >= 0 && s < (1LL << 39); }
+
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // A bf16 [B, H, N, d] argument with its strides.
@@ -121,7 +125,7 @@ fa_status_t rope_impl(const void *q, const int64_t *q_strides, const void *k, co
                       int interleaved, float factor, float sign, cudaStream_t stream) {
   const fa_status_t st = check_rope(B, H, Hkv, N, d, rot, interleaved, factor);
   if (st != FA_OK) return st;
-  if (!inv_freq || !aligned4(inv_freq) || !aligned4(positions) || positions_stride < 0) return FA_ERR_INVALID_ARGUMENT;
+  if (!inv_freq || !aligned4(inv_freq) || !aligned4(positions) || !row_stride(positions_stride)) return FA_ERR_INVALID_ARGUMENT;
   const bool has_k = Hkv > 0;
   View vq, vk{}, vqo, vko{};
   if (!make_view(q, q_strides, B, H, N, d, &vq) || !make_view(q_out, q_out_strides, B, H, N, d, &vqo))
@@ -261,7 +265,7 @@ fa_status_t fa_rope_append(const void *q, const int64_t *q_strides, const void *
   if (st != FA_OK) return st;
   if (Hkv < 1 || Nk < 1 || Nk > kMaxRows) return FA_ERR_INVALID_ARGUMENT;
   if (!inv_freq || !cache_seqlens || !aligned4(inv_freq) || !aligned4(cache_seqlens) || !aligned4(positions) ||
-      positions_stride < 0)
+      !row_stride(positions_stride))
     return FA_ERR_INVALID_ARGUMENT;
   View vq, vk, vv, vqo, vkc, vvc;
   if (!make_view(q, q_strides, B, H, N, d, &vq) || !make_view(k, k_strides, B, Hkv, N, d, &vk) ||
@@ -328,7 +332,7 @@ fa_status_t fa_fwd_tree(const void *q, const int64_t *q_strides, const void *k, 
                         cudaStream_t stream) {
   const fa_status_t st = check_tree(B, H, Hkv, Nt, Nk, d, scale);
   if (st != FA_OK) return st;
-  if (!lse || !aligned16(lse) || !parents || !aligned4(parents) || parents_stride < 0 || !aligned4(cache_seqlens))
+  if (!lse || !aligned16(lse) || !parents || !aligned4(parents) || !row_stride(parents_stride) || !aligned4(cache_seqlens))
     return FA_ERR_INVALID_ARGUMENT;
   View vq, vk, vv, vo;
   if (!make_view(q, q_strides, B, H, Nt, d, &vq) || !make_view(k, k_strides, B, Hkv, Nk, d, &vk) ||
@@ -480,7 +484,8 @@ fa_status_t fa_cache_compact(const void *k, const int64_t *k_strides, const void
   fa_status_t st = check_cache(B, Hkv, Hkv, Nk, d);
   if (st != FA_OK) return st;
   if (Nk_out < 1 || Nk_out > kMaxRows || M < 1 || M > kMaxRows) return FA_ERR_INVALID_ARGUMENT;
-  if (!kept || !aligned4(kept) || kept_b_stride < 0 || kept_h_stride < 0 || !aligned4(base))
+  if (static_cast<long long>(B) * Hkv * ((M + 63) / 64) >= (1LL << 31)) return FA_ERR_INVALID_ARGUMENT;  // the grid
+  if (!kept || !aligned4(kept) || !row_stride(kept_b_stride) || !row_stride(kept_h_stride) || !aligned4(base))
     return FA_ERR_INVALID_ARGUMENT;
   if ((weights == nullptr) != (weights_out == nullptr) || !aligned4(weights) || !aligned4(weights_out))
     return FA_ERR_INVALID_ARGUMENT;

@@ -149,8 +149,7 @@ cudaError_t launch_cache_compact(const CompactParams &p, cudaStream_t stream) {
     return cudaGetLastError();
   }
   const int block_rows = kMoveThreads / (p.d / 8) * kMoveRows;
-  const long long grid = heads * ((p.M + block_rows - 1) / block_rows);
-  if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const long long grid = heads * ((p.M + block_rows - 1) / block_rows);  // below 2^31: checked on entry
   if (p.d == 64)
     fa_cache_gather_kernel<64><<<static_cast<unsigned>(grid), kMoveThreads, 0, stream>>>(p);
   else

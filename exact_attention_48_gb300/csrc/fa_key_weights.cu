@@ -696,8 +696,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
           const float sum =
               (red[row] + red[kWgKeys + row]) + (red[2 * kWgKeys + row] + red[3 * kWgKeys + row]);
           store_weight(p, n, key0 + row, sum);
-          fence_proxy_async_smem();
         }
+        fence_proxy_async_smem();
         warp_arrive(&k_empty[nk % KB]);
       }
       ++nk;

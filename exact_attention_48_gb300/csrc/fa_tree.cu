@@ -1073,8 +1073,7 @@ template <int D, int ROWS, int WARPS>
 cudaError_t launch_merge(const TreeParams &p, cudaStream_t stream) {
   const long long cuts = p.cuts_by_unit ? static_cast<long long>(p.B) * p.Hkv : p.ranges;
   const long long blocks = cuts * p.row_tiles * ((p.gpt * p.Nt + ROWS - 1) / ROWS) *
-                           (D / (kMergeCols * 32 / ROWS));
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+                           (D / (kMergeCols * 32 / ROWS));  // (at most 152 runs per pair of row tiles)
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks));
   cfg.blockDim = dim3(WARPS * 32);

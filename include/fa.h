@@ -433,13 +433,15 @@ FA_API fa_status_t fa_cache_select(const float *weights, const int *cache_seqlen
  *   k_out, v_out : [B, Hkv, Nk_out, d]; weights_out : fp32 [B, Hkv, Nk_out],
  *                  NULL exactly if weights is
  *   kept         : int32, list of (b, h) at kept[b * kept_b_stride + h *
- *                  kept_h_stride] (strides 0: shared), M entries each
+ *                  kept_h_stride] (strides 0: shared), M entries each;
+ *                  B * Hkv * ceil(M / 64) < 2^31
  *   base         : int32 [B] or NULL (zeros)
  * Either every output is its input (same pointers and strides, Nk_out = Nk:
  * in place), and then the non-negative entries of a list must ascend
  * strictly and none may be below its place, kept[i] >= i (otherwise rows
  * hold wrong values; no other memory is touched), or no output shares an
- * element with an argument, and then the lists may be in any order.
+ * element with an argument, and then the lists may be in any order and
+ * name a row more than once.
  * With fa_cache_select's lists this evicts; with base_b the row before which
  * a drafted tree starts and kept the nodes of the accepted branch, it makes
  * that branch the sequence's next rows.

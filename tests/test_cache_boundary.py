@@ -193,3 +193,17 @@ def test_rope_frequencies():
         fa_rope_frequencies(2, scaling="base", factor=2.0, device="cpu")
     with pytest.raises(ValueError):
         got(scaling="other")
+
+
+def test_int_strides_past_64_bits_are_refused(lib):
+    """Row strides whose products would not fit 64 bits."""
+    for far in (1 << 39, 2 ** 62, 2 ** 63 - 1):
+        assert rope(lib, pos_b=far) == INVALID and rope(lib, "fa_rope_bwd", pos_b=far) == INVALID
+        assert tree(lib, par_b=far) == INVALID
+        s = st(2, 2, 100, 64)
+        for kb, kh in ((far, 10), (20, far)):
+            assert lib.fa_cache_compact(at(0), s, at(1), s, None, at(4), s, at(5), s, None, at(3), kb, kh, None, 2, 2,
+                                        100, 100, 10, 64, None) == INVALID
+    s = st(1 << 10, 1 << 4, 100, 64)
+    assert lib.fa_cache_compact(at(0), s, at(10), s, None, at(20), s, at(30), s, None, at(40), 0, 0, None, 1 << 10,
+                                1 << 4, 100, 100, 1 << 30, 64, None) == INVALID
