@@ -403,27 +403,31 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------------
-// More than 64 query rows: S = Q K^T, M = 128 query rows, N = 256 keys, and
-// thread = query row.  A row's logsumexp is then one register, where S^T needs
-// a table of columns that every thread reads from shared memory (a broadcast
-// read costs a cycle per 4 bytes: 1024 cycles a tile, as much as the
-// products).  The sums over query rows stay in the threads too: each keeps an
-// accumulator per key for its rows of all tiles, and the lanes and warps are
-// added up once at the unit's end, through the unit's own K buffer, which the
-// producer gets back after that.
+// More than 64 query rows: S = Q K^T, M = 128 query rows, N = 256 keys.  S is
+// read back as matrix fragments: a thread then holds four query rows of 16 of
+// the keys, so that its rows' logsumexps are four registers (S^T would need a
+// table of columns that every thread reads from shared memory, 1024 cycles a
+// tile, as much as the products) and its running sums 16 (a thread that holds
+// one row of 64 keys needs 64, which leaves no registers for a long load of S
+// and made the kernel a sixth slower: 260 us where it takes 225).  The sums over
+// query rows stay in the threads over all tiles; lanes and warps are added up
+// once at the unit's end, through the unit's own K buffer, which the producer
+// gets back after that.
 //
-// CTA (640 threads): four weight warpgroups, each 64 of the 256 keys (64
-// accumulators a thread, and four warps per scheduler to hide the waits
-// between tiles; two warpgroups of 128 keys run as fast), producer, MMA
-// issuer.  TMEM: two S buffers of 256 columns.
+// CTA (576 threads): four weight warpgroups, each 64 of the 256 keys (four warps
+// per scheduler to hide the waits between tiles; eight warps of 128 keys and 208
+// registers took 255 us), producer, MMA issuer.  TMEM: two S buffers of 256
+// columns.
 //
 // What bounds it: a tile of 128 x 256 takes 1024 cycles of the tensor core and
-// 1024 of the exponentials; a one-CTA timeline shows 2000.  The product takes
-// most of them: its operands (12 KB of shared memory per instruction) and the
-// tiles coming in compete, and with two S buffers the chain buffer free -
-// product - buffer full - read leaves little slack.  Knocking out the
-// exponentials saves 19 %, the products 7 %, the query loads nothing.
-// Measured, B4 H32 N4096 d128 causal: 260 us, 1055 TFLOP/s (0.55 of burst).
+// 1024 of the exponentials, and 1790 in all: the exponential unit and the tensor
+// core are each busy 56 % of the time, the issue slots 58 %.  The rest is the
+// weight warps' own chain between tiles (wait, load, a row's logsumexp and mask):
+// knocking out the exponentials saves 15 %, the products 8 %, the fetch of the
+// logsumexps with the mask 18 %.  No better: that work moved to an idle warp and
+// a table in shared memory (more instructions than it saves), into the shadow of
+// the load, or the warpgroups on alternate tiles instead of all on one.
+// Measured, B4 H32 N4096 d128 causal: 225 us, 1220 TFLOP/s (0.63 of burst).
 
 template <int D>
 struct KwRowsLayout {
@@ -443,13 +447,9 @@ struct KwRowsLayout {
   static_assert(kKBlock >= 2 * 4 * 128 * 4, "the sums fit the K buffer");
 };
 
-constexpr int kRowsThreads = 640;   // 16 weight warps, producer, MMA issuer, 2 idle
+constexpr int kRowsThreads = 576;   // 16 weight warps, producer, MMA issuer
 constexpr int kRowsProducer = 16, kRowsMma = 17;
 constexpr int kWgKeys = 64;         // keys of a weight warpgroup
-// Registers: 64 accumulators and a chunk of S for the weight warps.
-constexpr uint32_t kRowsRegsControl = 64, kRowsRegsWeights = 104;
-static_assert(128 * kRowsRegsControl + 512 * kRowsRegsWeights <= kRowsThreads * 96, "register split");
-
 // x = *p if `on`.
 __device__ __forceinline__ void load_if(float &x, const float *p, bool on) {
   asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t@q ld.global.f32 %0, [%1];\n\t}"
@@ -457,19 +457,27 @@ __device__ __forceinline__ void load_if(float &x, const float *p, bool on) {
                : "l"(p), "r"(static_cast<uint32_t>(on)));
 }
 
-// acc[j] += exp2(s c + nl) for 32 keys; MASK: only keys j <= lim.
+// 16 rows x 64 keys of S as a fragment (see tmem_ld_frag64): the thread holds
+// rows lane / 4 and lane / 4 + 8, and of every 8 keys the two at j0 and j0 + 1.
+// acc[c] += the sum over its two rows of exp2(s cc + nl) for its keys 8 c + j0
+// and 8 c + j0 + 1; MASK: only keys j <= lim.
 template <bool MASK>
-__device__ __forceinline__ void add_keys(float2 (&acc)[kWgKeys / 2], int j0, const uint32_t (&s)[16], float2 cc, float2 nl,
-                                         int lim) {
+__device__ __forceinline__ void add_rows(float2 (&acc)[kWgKeys / 8], const uint32_t (&s)[32], float2 cc, float nl0,
+                                         float nl1, int lim0, int lim1, int j0) {
 #pragma unroll
-  for (int j = 0; j < 16; j += 2) {
-    const float2 y = ffma2(make_float2(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), cc, nl);
-    float p0 = ex2(y.x), p1 = ex2(y.y);
+  for (int c = 0; c < kWgKeys / 8; ++c) {
+    const float2 y0 = ffma2(make_float2(__uint_as_float(s[4 * c]), __uint_as_float(s[4 * c + 1])), cc,
+                            make_float2(nl0, nl0));
+    const float2 y1 = ffma2(make_float2(__uint_as_float(s[4 * c + 2]), __uint_as_float(s[4 * c + 3])), cc,
+                            make_float2(nl1, nl1));
+    float2 w0 = make_float2(ex2(y0.x), ex2(y0.y)), w1 = make_float2(ex2(y1.x), ex2(y1.y));
     if (MASK) {
-      p0 = j0 + j <= lim ? p0 : 0.0f;
-      p1 = j0 + j + 1 <= lim ? p1 : 0.0f;
+      if (8 * c + j0 > lim0) w0.x = 0.0f;
+      if (8 * c + j0 + 1 > lim0) w0.y = 0.0f;
+      if (8 * c + j0 > lim1) w1.x = 0.0f;
+      if (8 * c + j0 + 1 > lim1) w1.y = 0.0f;
     }
-    acc[(j0 + j) / 2] = fadd2(acc[(j0 + j) / 2], make_float2(p0, p1));
+    acc[c] = fadd2(acc[c], fadd2(w0, w1));
   }
 }
 
@@ -520,7 +528,6 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   const uint32_t tmem = *tmem_slot;
 
   if (warp >= kRowsProducer) {
-    regs_decrease<kRowsRegsControl>();
     if (warp == kRowsProducer && lane == 0) {
       // ---------------------------------------------------------- producer
       tma_prefetch_desc(&tm_q);
@@ -599,7 +606,6 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       mbar_drain(drain, 0);
     }
   } else {
-    regs_increase<kRowsRegsWeights>();
     // ------------------------------------------------------------ weights
     const int t = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -638,58 +644,61 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         lse = -INFINITY;
         load_if(lse, lse_u + static_cast<long long>(g) * p.Nq + i, row_in && g < p.G && i < p.Nq);
       };
-      float2 acc[kWgKeys / 2];
+      float2 acc[kWgKeys / 8];
 #pragma unroll
-      for (int j = 0; j < kWgKeys / 2; ++j) acc[j] = make_float2(0.f, 0.f);
+      for (int c = 0; c < kWgKeys / 8; ++c) acc[c] = make_float2(0.f, 0.f);
       int last;
       float lse;
       fetch(lse, last);
       for (int x = n.x0; ok && x < n.x1; ++x, ++cnt) {
         const bool on = lse != -INFINITY;
-        const float nl = on ? -(lse * kLog2e) : 0.0f;
+        const float row_nl = on ? -(lse * kLog2e) : 0.0f;
         // keys 0..lim of the tile are seen
-        const int lim = on ? (last >= key0 + kWgKeys - 1 ? kWgKeys - 1 : last - key0) : -1;
+        const int row_lim = on ? (last >= key0 + kWgKeys - 1 ? kWgKeys - 1 : last - key0) : -1;
         const uint32_t buf = cnt & 1;
         if (x + 1 < n.x1) fetch(lse, last);
+        const bool any = __any_sync(0xffffffffu, row_lim >= 0), all = __all_sync(0xffffffffu, row_lim >= kWgKeys - 1);
         if (!(ok = __all_sync(0xffffffffu, mbar_wait(&s_full[buf], (cnt >> 1) & 1, ctl, kSiteSFull)))) break;
         tc_fence_after();
         const uint32_t ts = tmem + buf * 2 * kKeys + t * kWgKeys + lane_base;
-        const bool any = __any_sync(0xffffffffu, lim >= 0), all = __all_sync(0xffffffffu, lim >= kWgKeys - 1);
-        const float2 n2 = make_float2(nl, nl);
         if (any) {
 #pragma unroll
-          for (int q = 0; q < kWgKeys / 16; ++q) {
-            uint32_t s[16];
-            tmem_ld16(ts + q * 16, s);
-            tmem_ld_wait16(s);
-            if (q == kWgKeys / 16 - 1) {
+          for (int half = 0; half < 2; ++half) {
+            uint32_t s[32];
+            tmem_ld_frag64(ts + half * (16u << 16), s);
+            const int from = (lane >> 2) + 16 * half;
+            const float nl0 = __shfl_sync(0xffffffffu, row_nl, from), nl1 = __shfl_sync(0xffffffffu, row_nl, from + 8);
+            tmem_ld_wait(s);
+            if (half == 1) {
               tc_fence_before();
               warp_arrive(&s_free[buf]);
             }
             if (all)
-              add_keys<false>(acc, q * 16, s, cc, n2, lim);
+              add_rows<false>(acc, s, cc, nl0, nl1, 0, 0, 0);
             else
-              add_keys<true>(acc, q * 16, s, cc, n2, lim);
+              add_rows<true>(acc, s, cc, nl0, nl1, __shfl_sync(0xffffffffu, row_lim, from),
+                             __shfl_sync(0xffffffffu, row_lim, from + 8), (lane & 3) * 2);
           }
         } else {
           tc_fence_before();
           warp_arrive(&s_free[buf]);
         }
       }
-      // ---- the unit's sums: over the lanes (each step halves the keys a lane
-      // keeps; lane l ends with keys 2 l and 2 l + 1), then over the warps
-      float *a = reinterpret_cast<float *>(acc);
+      // ---- the unit's sums: over the lanes with the same keys (each step halves
+      // the keys a lane keeps; lane l ends with keys 8 (l / 4) + 2 (l % 4) and the
+      // next), then over the warps
 #pragma unroll
-      for (int o = 16, w = kWgKeys / 2; o > 0; o >>= 1, w >>= 1) {
+      for (int o = 16, w = kWgKeys / 16; o > 2; o >>= 1, w >>= 1) {
         const bool up = lane & o;
 #pragma unroll
-        for (int j = 0; j < w; ++j) {
-          const float send = up ? a[j] : a[j + w], keep = up ? a[j + w] : a[j];
-          a[j] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+        for (int c = 0; c < w; ++c) {
+          const float2 send = up ? acc[c] : acc[c + w], keep = up ? acc[c + w] : acc[c];
+          acc[c] = make_float2(keep.x + __shfl_xor_sync(0xffffffffu, send.x, o),
+                               keep.y + __shfl_xor_sync(0xffffffffu, send.y, o));
         }
       }
       float *red = reinterpret_cast<float *>(smem + (nk % KB) * L::kKBlock) + t * 4 * kWgKeys;
-      if (ok) *reinterpret_cast<float2 *>(red + (warp & 3) * kWgKeys + lane * 2) = make_float2(a[0], a[1]);
+      if (ok) *reinterpret_cast<float2 *>(red + (warp & 3) * kWgKeys + lane * 2) = acc[0];
       named_barrier(1 + t, 128);
       if (ok) {
         if (row < kWgKeys) {
