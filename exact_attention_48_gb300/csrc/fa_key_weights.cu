@@ -802,10 +802,11 @@ KeyWeightPlan plan_key_weights(int B, int H, int Hkv, int Nq, int Nk, int d) {
   if (s > tiles) s = tiles;
   pl.splits = units >= 2 * 152 || s < 1 ? 1 : static_cast<int>(s);
   // Every unit of a cache head reads the group's query rows: only as many
-  // heads are worked on at a time as leave those rows in L2 (B4 H32 N4096:
-  // 294 us over all 128 heads, whose rows take 134 MB, 260 head by head; but
-  // with all 32 heads of a quarter of that, 33 MB, 69 us against 78, since the
-  // heavy units then go first over all of them).
+  // heads are worked on at a time as leave those rows in L2.  (B4 H32 N4096,
+  // causal: 230 us over all 128 heads, whose rows take 134 MB, 225 in windows of
+  // 48 heads, 222 head by head; but all 32 heads of a quarter of that, 33 MB, 57
+  // us together and 66 head by head, since the heavy units then go first over
+  // all of them.)
   const long long row_bytes = 2ll * G * Nq * d;
   const long long fit = kWindowBytes / row_bytes;
   const long long heads = static_cast<long long>(B) * Hkv;
