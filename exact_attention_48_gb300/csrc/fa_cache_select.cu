@@ -14,8 +14,8 @@
 //
 // A row list is a few KB to a few hundred, so latency bounds the call, not
 // bytes: a CTA keeps the keys of up to 16384 rows in shared memory through all
-// passes (two CTAs to an SM), and a longer list goes to a cluster of up to 8
-// CTAs, which read each other's histograms and counts through distributed
+// passes (two CTAs to an SM), and a longer list, or a list of more than 8192 rows
+// where there are few, goes to a cluster of up to 8 CTAs, which read each other's histograms and counts through distributed
 // shared memory.  Lists past 8 * 16384 rows are read again (from L2) in each
 // pass.  The loops over the keys are short ones: every instruction of this
 // kernel comes cold from memory (unrolled with the keys in registers the
@@ -26,7 +26,8 @@
 // one of them, so that little is read from other CTAs (all bins of all CTAs
 // took 4700 cycles a pass).
 // Measured on the device: B16 Hkv16 16384 rows to 8192 21 us (28 with all
-// weights alike), 8 lists of 131072 to 16384 18 us, 2 of 640 to 256 6.5 us.
+// weights alike), 8 lists of 131072 to 16384 18 us, of 32768 12 us, 2 of 640 to
+// 256 6 us.
 
 #include <cooperative_groups.h>
 #include <cstdint>
@@ -45,6 +46,7 @@ constexpr int kSelStep = kSelThreads * kSelStretch;  // rows of a CTA and step
 constexpr int kSelBins = 2048;
 constexpr int kSelCoarse = kSelBins / 32;
 constexpr int kSelCopies = 4;
+constexpr int kSelOneCta = 8192;                     // rows that one CTA does as fast as a cluster
 
 __device__ __forceinline__ uint32_t order_key(float w) {
   if (w != w) return 0u;
@@ -322,6 +324,12 @@ cudaError_t launch_cache_select(const SelectParams &p, cudaStream_t stream) {
   const int n = p.Nk - p.first - p.recent;
   int ranks = 1;
   while (ranks < 8 && n > ranks * kSelStep) ranks *= 2;
+  // and a larger one for long lists that would leave SMs idle (8 lists of 32768
+  // rows in clusters of 2 18.0 us, of 8 12.2; 16 and 32 of 16384 in one CTA each
+  // 13.6, in 8 and 4 11.8 and 12.0; 2 of 8192 the same in 1 and in 8, 9.9, and
+  // slower in 2, 11.7)
+  const long long lists = static_cast<long long>(p.B) * p.Hkv;
+  while (ranks < 8 && n > kSelOneCta && lists * ranks * 2 <= 152) ranks *= 2;
   if (ranks == 1) return launch_select<false, false>(p, ranks, stream);
   return n > ranks * kSelStep ? launch_select<true, true>(p, ranks, stream)
                               : launch_select<true, false>(p, ranks, stream);

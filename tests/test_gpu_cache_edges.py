@@ -146,3 +146,18 @@ def test_two_threads_on_two_streams():
     for a, b in zip(got, want):
         for x, y in zip(a, b):
             assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("B,Hkv,Nk", [(1, 2, 8193), (3, 5, 12000), (2, 20, 9000), (8, 10, 8500)])
+def test_select_clusters_of_every_size(B, Hkv, Nk):
+    """Lists that one CTA could hold, shared by clusters of 8, 8, 2 and 1 (few lists, many lists)."""
+    g = ref.gen(97 + Nk)
+    w = torch.randint(0, 50, (B, Hkv, Nk), generator=g, device="cuda").float()   # many ties, across the cluster's parts
+    lens = [max(1, Nk - 1000 * b) for b in range(B)]
+    keep, first, recent = 1500, 7, 100
+    kept, new = fa_cache_select(w, keep, ref.ints(lens), first, recent)
+    assert new.tolist() == [min(n, keep) for n in lens]
+    got, cpu = kept.tolist(), w.cpu()
+    for b in range(B):
+        for h in range(0, Hkv, max(1, Hkv // 3)):
+            assert got[b][h] == ref.select(cpu[b, h], lens[b], keep, first, recent), (b, h)
