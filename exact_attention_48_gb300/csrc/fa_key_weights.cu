@@ -628,35 +628,41 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         if (ok && row < kWgKeys) store_weight(p, n, key0 + row, 0.0f);
         continue;
       }
-      // the next column tile to fetch: its head group and tile of that group
-      int group = n.x0 / n.per_group, tile = n.first + n.x0 % n.per_group;
-      const float *lse_u = p.lse + (static_cast<long long>(n.b) * p.H + n.hk * p.G) * p.Nq;
-      // logsumexp of this thread's row of it (-inf: no such row), and the last
-      // key the row sees.  A predicated load into the register that the next
-      // turn reads: a copy of the value would wait for it here.
-      auto fetch = [&](float &lse, int &last) {
-        const int g = group * p.gpt + row_g, i = tile * kKeys + row_i;
-        last = p.causal ? n.len - p.Nq + i : 0x7fffffff;
+      // the tile to fetch next: this thread's row i of a head, its logsumexp at
+      // `at` (if i < Nq and heads > 0, the group's heads from the row's own on)
+      int tile = n.first + n.x0 % n.per_group, i = tile * kKeys + row_i;
+      int heads = p.G - n.x0 / n.per_group * p.gpt - row_g;
+      const float *at =
+          p.lse + (static_cast<long long>(n.b) * p.H + n.hk * p.G + p.G - heads) * static_cast<long long>(p.Nq) + i;
+      const int to_next = p.gpt * p.Nq - n.per_group * kKeys;  // of `at`, from behind a head's tiles to the next head's
+      const int see = p.causal ? n.len - p.Nq - key0 : 1 << 30;  // row i sees this warpgroup's keys 0..see + i
+      // A predicated load into the register that the next turn reads: a copy of
+      // the value would wait for it here.  (-inf: no such row)
+      auto fetch = [&](float &lse, int &lim) {
+        lim = see + i;
+        lse = -INFINITY;
+        load_if(lse, at, row_in && heads > 0 && i < p.Nq);
+        at += kKeys;
+        i += kKeys;
         if (++tile == p.tiles_per_head) {
           tile = n.first;
-          ++group;
+          i = tile * kKeys + row_i;
+          at += to_next;
+          heads -= p.gpt;
         }
-        lse = -INFINITY;
-        load_if(lse, lse_u + static_cast<long long>(g) * p.Nq + i, row_in && g < p.G && i < p.Nq);
       };
       float2 acc[kWgKeys / 8];
 #pragma unroll
       for (int c = 0; c < kWgKeys / 8; ++c) acc[c] = make_float2(0.f, 0.f);
-      int last;
+      int lim;
       float lse;
-      fetch(lse, last);
+      fetch(lse, lim);
       for (int x = n.x0; ok && x < n.x1; ++x, ++cnt) {
         const bool on = lse != -INFINITY;
         const float row_nl = on ? -(lse * kLog2e) : 0.0f;
-        // keys 0..lim of the tile are seen
-        const int row_lim = on ? (last >= key0 + kWgKeys - 1 ? kWgKeys - 1 : last - key0) : -1;
+        const int row_lim = on ? lim : -1;  // keys 0..row_lim are seen
         const uint32_t buf = cnt & 1;
-        if (x + 1 < n.x1) fetch(lse, last);
+        if (x + 1 < n.x1) fetch(lse, lim);
         const bool any = __any_sync(0xffffffffu, row_lim >= 0), all = __all_sync(0xffffffffu, row_lim >= kWgKeys - 1);
         if (!(ok = __all_sync(0xffffffffu, mbar_wait(&s_full[buf], (cnt >> 1) & 1, ctl, kSiteSFull)))) break;
         tc_fence_after();
