@@ -23,7 +23,7 @@ struct RopeParams {
   float factor;
   float sign;                 // +1 forward, -1 backward (the transposed rotation)
   int heads;                  // H + Hkv (+ Hkv)
-  int tokens;                 // tokens of a CTA, a power of two up to 256 / (d / 16)
+  int tokens;                 // tokens of a CTA, a power of two up to 8
   int head_groups;            // CTAs along the head axis
 };
 cudaError_t launch_rope(bool interleaved, const RopeParams &p, cudaStream_t stream);

@@ -104,13 +104,15 @@ fa_status_t check_rope(int B, int H, int Hkv, int N, int d, int rot, int interle
   return FA_OK;
 }
 
-// Tokens of a CTA and CTAs along the head axis: up to 8 (d = 128) or 16
-// tokens, fewer while that leaves SMs without two CTAs, then the heads cut.
+// Tokens of a CTA and CTAs along the head axis: up to 4 (d = 128) or 8 tokens
+// (B4 H32 N4096 d128 and B8 H16 Hkv4 N2047 d64 82 and 16.6 us, twice as many 86 and
+// 18.2; with CTAs of 256 threads 8 and 16 tokens 83 and 17.3), fewer while that
+// leaves SMs without two CTAs, then the heads cut.
 void plan_rope(RopeParams *p) {
   const long long all = static_cast<long long>(p->B) * p->N;
-  int tokens = p->d == 128 ? 8 : 16;
+  int tokens = p->d == 128 ? 4 : 8;
   while (tokens > 1 && all / tokens < 2 * 152) tokens /= 2;
-  const int at_once = 256 / (p->d / 16 * tokens);
+  const int at_once = 128 / (p->d / 16 * tokens);
   const long long blocks = (all + tokens - 1) / tokens;
   long long groups = (p->heads + at_once - 1) / at_once;
   const long long want = (4 * 152 + blocks - 1) / blocks;

@@ -13,7 +13,8 @@
 // token and pair and not per head, then each keeps the eight pairs of its
 // (token, piece) in registers over the heads it walks.  The first heads' rows
 // are on their way before the angles are computed.
-// Measured, B4 H32 Hkv32 N4096 d128: 84 us, 6380 GB/s (0.94 of the copy rate).
+// Measured on the device, B4 H32 Hkv32 N4096 d128: 82 us, 6570 GB/s (0.97 of the
+// copy rate); B8 H16 Hkv4 N2047 d64, 84 MB: 16.6 us.
 //
 // Angles.  The product p * f has to be exact to about 2^-20 of a turn for
 // positions in the millions, which fp32 cannot hold and fp64 (a sixty-fourth
@@ -30,11 +31,12 @@
 namespace fa {
 namespace {
 
-constexpr int kRopeThreads = 256;
-// Heads in flight per thread, and CTAs on an SM (B4 H32 N4096 d128: 84 us; 4 heads
-// and 2 CTAs 88.5, 6 and 2 84.8, 8 and 2 85.1, 3 and 3 87, 4 and 4 104).
+constexpr int kRopeThreads = 128;
+// Heads in flight per thread, and CTAs on an SM (with CTAs of twice the threads,
+// B4 H32 N4096 d128, 84 us: 4 heads and 2 CTAs 88.5, 6 and 2 84.8, 8 and 2 85.1, 3
+// and 3 87, 4 and 4 104).
 constexpr int kRopeUnroll = 4;
-constexpr int kRopeCtas = 3;  // (the append form, which has a tensor more to place, spills at 3: 2)
+constexpr int kRopeCtas = 6;  // (the append form, which has a tensor more to place, spills at 6: 4)
 
 // f / (2 pi) turns as a 0.64 fixed-point number, modulo one turn.
 __device__ __forceinline__ uint64_t turn_fraction(float f) {
@@ -98,7 +100,7 @@ __device__ __forceinline__ Pieces pieces_of(const RopeParams &p, int c) {
 // grid: x = blocks of `tokens` tokens, y = head groups.  Thread: piece c of
 // d / 16, token of the block, and first head.
 template <bool INTERLEAVED, bool APPEND>
-__global__ void __launch_bounds__(kRopeThreads, APPEND ? 2 : kRopeCtas) fa_rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, APPEND ? 4 : kRopeCtas) fa_rope_kernel(const RopeParams p) {
   extern __shared__ float table[];  // cos, then sin: [tokens][rot / 2]
   const int per_row = p.d >> 4, half = p.rot >> 1;
   const int t0 = blockIdx.x * p.tokens, all = p.B * p.N;
