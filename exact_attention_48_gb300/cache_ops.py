@@ -34,7 +34,9 @@ def _c_strides(strides):
 
 def _view(name, t, dev=None, shape=None):
     """A [B, H, N, d] bf16 view with contiguous d: its pointer and strides."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not isinstance(t, torch.Tensor) or (t.device != dev if dev is not None else not t.is_cuda):
+        if isinstance(t, torch.Tensor) and t.is_cuda:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be bfloat16, got {t.dtype}")
@@ -43,8 +45,6 @@ def _view(name, t, dev=None, shape=None):
         raise ValueError(f"{name} must be a [B, H, N, d] view with contiguous d")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if dev is not None and t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
     return t.data_ptr(), _c_strides(st)
 
 

@@ -161,3 +161,22 @@ def test_select_clusters_of_every_size(B, Hkv, Nk):
     for b in range(B):
         for h in range(0, Hkv, max(1, Hkv // 3)):
             assert got[b][h] == ref.select(cpu[b, h], lens[b], keep, first, recent), (b, h)
+
+
+def test_tensors_elsewhere_are_refused():
+    g = ref.gen(98)
+    q, k = ref.draw(g, 1, 2, 3, 64), ref.draw(g, 1, 2, 40, 64)
+    par, lse = ref.ints([-1, 0, 1]), torch.zeros(1, 2, 3, device="cuda")
+    for bad in (k.cpu(), None):
+        with pytest.raises(TypeError):
+            fa_fwd_tree(q, bad if bad is not None else par.tolist(), k, par)
+        with pytest.raises(TypeError):
+            fa_fwd_tree(q, k, bad, par)
+    with pytest.raises(TypeError):
+        fa_key_weights(q.cpu(), k, lse)
+    with pytest.raises(ValueError):
+        fa_fwd_tree(q, k, k, par.cpu())
+    with pytest.raises(ValueError):
+        fa_key_weights(q, k, lse.cpu())
+    with pytest.raises(ValueError):
+        fa_cache_compact(k, k.clone(), torch.zeros(1, 2, 4, dtype=torch.int32))
