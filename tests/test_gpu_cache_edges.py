@@ -180,3 +180,29 @@ def test_tensors_elsewhere_are_refused():
         fa_key_weights(q, k, lse.cpu())
     with pytest.raises(ValueError):
         fa_cache_compact(k, k.clone(), torch.zeros(1, 2, 4, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("Nq,d", [(1, 128), (33, 64), (700, 128), (700, 64)])
+def test_weights_and_eviction_under_load(Nq, d):
+    """Hundreds of launches back to back, copies running beside them: every one finishes in time with the same bits."""
+    g = ref.gen(99)
+    B, H, Hkv, Nk, keep = 3, 8, 4, 5000, 1000
+    q, k = ref.draw(g, B, H, Nq, d), ref.draw(g, B, Hkv, Nk, d)
+    lens = ref.ints([5000, 4097, 900])
+    lse = torch.rand(B, H, Nq, generator=g, device="cuda") + 8
+    want = fa_key_weights(q, k, lse, lens, True)
+    rows, new = fa_cache_select(want, keep, lens, 4, 64)
+    a, b = torch.empty(1 << 27, device="cuda", dtype=torch.uint8), torch.empty(1 << 27, device="cuda", dtype=torch.uint8)
+    side = torch.cuda.Stream()
+    for _ in range(6):
+        with torch.cuda.stream(side):
+            for _ in range(8):
+                a.copy_(b)
+        outs = []
+        for _ in range(32):
+            w = fa_key_weights(q, k, lse, lens, True)
+            outs.append((w, *fa_cache_select(w, keep, lens, 4, 64)))
+        torch.cuda.synchronize()
+        assert fa_device_status() == 0
+        for w, r, n in outs:
+            assert torch.equal(w, want) and torch.equal(r, rows) and torch.equal(n, new)
