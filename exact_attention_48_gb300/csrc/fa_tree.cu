@@ -26,6 +26,12 @@
 // most seven rounds, into shared memory while earlier tiles are worked on;
 // the softmax of those tiles tests bits.  Rows behind the sequence's end and
 // padding nodes' rows are set to zero in the V tile, for 0 * NaN is NaN.
+//
+// Scores that are not finite.  A score of -inf weighs nothing: while a row has
+// seen no other its maximum stays -inf and its exponents are taken relative to 0
+// (-inf less -inf would be NaN).  A NaN that a row sees makes its sum NaN, and
+// with it its O and logsumexp, through the merge of the runs as well.  A sum of
+// zero marks a row that nothing was added to.
 
 #include <cstdint>
 
@@ -401,6 +407,9 @@ __device__ __forceinline__ bool pv_wait(const SoftmaxArgs &a, const WaitCtl &ctl
   return mbar_wait(a.pv_done + (k & 1), (k >> 1) & 1, ctl, kSitePvDone);
 }
 
+// What a row's exponents are taken relative to.
+__device__ __forceinline__ float exponent_base(const RowState &st) { return st.m == -INFINITY ? 0.0f : st.m; }
+
 // O rescaled where a row's maximum moved (after the P V product before it).
 template <int D>
 __device__ __forceinline__ bool rescale_o(const SoftmaxArgs &a, const WaitCtl &ctl, uint32_t cnt, float alpha) {
@@ -453,7 +462,8 @@ __device__ __forceinline__ bool softmax_tile(const SoftmaxArgs &a, const TreePar
     mx = fminf(fminf(min32(s[0]), min32(s[1])), fminf(min32(s[2]), min32(s[3])));
   float alpha;
   const bool grow = move_max(st, mx * c, &alpha);
-  const float2 cc = make_float2(c, c), nm = make_float2(-st.m, -st.m);
+  const float base = exponent_base(st);
+  const float2 cc = make_float2(c, c), nm = make_float2(-base, -base);
   uint32_t pk[4][16];
   float2 sf = make_float2(0.f, 0.f);
 #pragma unroll
@@ -517,6 +527,7 @@ __device__ __forceinline__ bool masked_tile(const SoftmaxArgs &a, const TreePara
   }
   float alpha;
   const bool grow = move_max(st, any ? mx * c : -INFINITY, &alpha);  // (0 * -inf is NaN)
+  const float base = exponent_base(st);
   float2 sf = make_float2(0.f, 0.f), sb = sf;
 #pragma unroll 1
   for (int q = 0; q < 4; ++q) {  // P's quarter q lies over S's columns 16 q .. 16 q + 15, read by then
@@ -526,8 +537,8 @@ __device__ __forceinline__ bool masked_tile(const SoftmaxArgs &a, const TreePara
     tmem_ld_wait(s);
 #pragma unroll
     for (int x = 0; x < 32; x += 2) {
-      const float p0 = (see >> x) & 1u ? ex2(fmaf(__uint_as_float(s[x]), c, -st.m)) : 0.0f;
-      const float p1 = (see >> (x + 1)) & 1u ? ex2(fmaf(__uint_as_float(s[x + 1]), c, -st.m)) : 0.0f;
+      const float p0 = (see >> x) & 1u ? ex2(fmaf(__uint_as_float(s[x]), c, -base)) : 0.0f;
+      const float p1 = (see >> (x + 1)) & 1u ? ex2(fmaf(__uint_as_float(s[x + 1]), c, -base)) : 0.0f;
       pk[x / 2] = pack_bf16x2(p0, p1);
       sf = fadd2(sf, make_float2(p0, p1));
       sb = add_bf16x2_f32(sb, pk[x / 2]);
@@ -894,7 +905,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float M = fmaxf(m0, m1);
             const float f0 = m0 == -INFINITY ? 0.0f : ex2(m0 - M), f1 = m1 == -INFINITY ? 0.0f : ex2(m1 - M);
             const float l = xl[row] * f0 + xl[kRows + row] * f1, lb = xb[row] * f0 + xb[kRows + row] * f1;
-            const bool any = l > 0.0f && !padding;
+            const bool any = l != 0.0f && !padding;
             const float inv = any ? 1.0f / lb : 0.0f;
             const float g0 = f0 * inv, g1 = f1 * inv;
             const uint32_t t0 = tmem + L::kO + lane_base, t1 = t0 + D;
@@ -938,7 +949,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_before();
           named_barrier(2, 256);
         } else if (ok) {
-          const bool any = st.l > 0.0f && !padding;
+          const bool any = st.l != 0.0f && !padding;
           const float inv = any ? 1.0f / st.lb : 0.0f;
 #pragma unroll 1
           for (int ch = 0; ch < D; ch += 16) {
@@ -995,6 +1006,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 // a hundred runs is merged in a few round trips.
 constexpr int kMergeCols = 16;
 
+// The greater of two runs' logsumexps: +inf, the mark of padding, before NaN,
+// and NaN before every other value.
+__device__ __forceinline__ float merge_max(float a, float b) {
+  const float x = fmaxf(a, b);
+  return x != INFINITY && (a != a || b != b) ? NAN : x;
+}
+
 template <int D, int ROWS, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32) fa_tree_merge_kernel(const TreeParams p) {
   constexpr int kCols = kMergeCols * 32 / ROWS;  // of a block
@@ -1028,7 +1046,7 @@ __global__ void __launch_bounds__(WARPS * 32) fa_tree_merge_kernel(const TreePar
     float v[kMergeCols];
 #pragma unroll
     for (int y = 0; y < kMergeCols; ++y) v[y] = on ? part[y * slot_rows] : 0.0f;
-    const float mn = fmaxf(m, s);
+    const float mn = merge_max(m, s);
     const float fa = m == mn ? 1.0f : (m == -INFINITY ? 0.0f : ex2(m - mn));
     const float fb = s == -INFINITY ? 0.0f : (s == mn ? 1.0f : ex2(s - mn));
     l = l * fa + fb;
@@ -1044,7 +1062,7 @@ __global__ void __launch_bounds__(WARPS * 32) fa_tree_merge_kernel(const TreePar
   if (warp > 0) return;
   float M = -INFINITY;
 #pragma unroll
-  for (int w = 0; w < WARPS; ++w) M = fmaxf(M, sh_m[w][lane]);
+  for (int w = 0; w < WARPS; ++w) M = merge_max(M, sh_m[w][lane]);
   l = 0.0f;
 #pragma unroll
   for (int y = 0; y < kMergeCols; ++y) o[y] = 0.0f;

@@ -366,6 +366,8 @@ FA_API fa_status_t fa_rope_frequencies(float *inv_freq, float *factor_out, int r
  * result is o = 0, lse = -inf, and no row sees it, whatever its cache row
  * holds.  (A value row that some node sees must be finite: one that is not
  * may reach the results of the nodes that do not see it.)
+ * A score of -inf weighs nothing (a row with no other gets o = 0,
+ * lse = -inf); a NaN, or a score of +inf, makes its own row NaN.
  *   q, o   : [B, H, Nt, d]; k, v : [B, Hkv, Nk, d]; lse : fp32 [B, H, Nt]
  *   parents: int32, node (b, i) at parents[b * parents_stride + i] (stride
  *            0: one tree for the whole batch)
