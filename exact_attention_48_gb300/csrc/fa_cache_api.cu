@@ -12,7 +12,7 @@ namespace fa {
 namespace {
 
 constexpr int kMaxRows = 1 << 30;       // rows of a cache, tokens of a call
-constexpr int kMaxHeads = (1 << 24) - 1;  // B * H
+constexpr int kMaxHeads = (1 << 24) - 1;  // B * H, and B * Hkv
 
 // A memory range of an argument.
 struct Range {
@@ -100,7 +100,8 @@ fa_status_t check_rope(int B, int H, int Hkv, int N, int d, int rot, int interle
   if (rot < 1 || rot > d) return FA_ERR_INVALID_ARGUMENT;
   if (rot % 16) return FA_ERR_UNSUPPORTED;
   if (static_cast<long long>(B) * N > kMaxRows) return FA_ERR_INVALID_ARGUMENT;
-  if (static_cast<long long>(B) * (static_cast<long long>(H) + 2 * Hkv) > kMaxHeads) return FA_ERR_INVALID_ARGUMENT;
+  if (static_cast<long long>(B) * H > kMaxHeads || static_cast<long long>(B) * Hkv > kMaxHeads)
+    return FA_ERR_INVALID_ARGUMENT;
   return FA_OK;
 }
 

@@ -275,11 +275,12 @@ FA_API fa_status_t fa_fwd_decode(const void *q, const int64_t *q_strides, const 
  * [B, Hkv, Nk, d] with cache_seqlens as in fa_fwd_decode (int32 [B], 4-byte
  * aligned, NULL for all Nk rows; it counts the new rows; clamped into
  * [0, Nk]); queries may have H = G * Hkv heads, G of them sharing a cache
- * head (query head h uses cache head h / G).  B * H < 2^24; Nk, the query
- * rows and the tokens of a call (B * N) are at most 2^30.  Values behind a
- * sequence's last row are read as memory but never used, whatever they are
- * (infinities and NaN included), and rows that no argument names are left
- * as they were.  Every call may be captured into a graph.
+ * head (query head h uses cache head h / G).  B * H and B * Hkv are below
+ * 2^24; Nk, the query rows and the tokens of a call (B * N) are at most
+ * 2^30.  Values behind a sequence's last row are read as memory but never
+ * used, whatever they are (infinities and NaN included), and rows that no
+ * argument names are left as they were.  Every call may be captured into a
+ * graph.
  */
 
 /*
