@@ -264,7 +264,12 @@ def fa_key_weights(q, k, lse, cache_seqlens=None, causal: bool = False, scale: f
     fp32 = weights_in (or zeros) plus, for the rows j < cache_seqlens[b], the
     sum over the query rows q [B, H, Nq, d] that see j (the last Nq
     positions; causal: up to their own) and the heads that share the cache
-    head of exp(scale q.k_j - lse).  ``weights=weights_in`` adds in place."""
+    head of exp(scale q.k_j - lse).  ``weights=weights_in`` adds in place.
+
+    lse has to be over the rows that the query sees here: that of fa_fwd and
+    fa_fwd_decode with the same ``causal``; of fa_fwd_tree one node's, or a
+    chain's with ``causal``.  A tree with branches is weighed once its accepted
+    branch has been compacted: that branch's queries and lse, ``causal``."""
     qp, qs = _view("q", q)
     dev = q.device
     kp, ks = _view("k", k, dev)
@@ -320,7 +325,9 @@ def fa_cache_compact(k, v, kept, weights=None, base=None, k_out=None, v_out=None
     k, v (and weights) where that entry is not negative.  kept: int32
     [B, Hkv, M], or [B, M] for all heads.  Without outputs the cache is
     changed in place (the entries must then ascend, none below its place).
-    Returns (k_out, v_out, weights_out)."""
+    Rows behind the last place filled keep what they held: set their weights to
+    0 before new rows are appended there.  Returns (k_out, v_out,
+    weights_out)."""
     kp, ks = _view("k", k)
     B, Hkv, Nk, d = k.shape
     dev = k.device

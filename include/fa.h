@@ -392,10 +392,16 @@ FA_API fa_status_t fa_fwd_tree(const void *q, const int64_t *q_strides, const vo
  *     weights[b, hk, j] = weights_in[b, hk, j]
  *         + sum over the G heads h of hk and the query rows i that see j of
  *           exp(scale * q[b, h, i] . k[b, hk, j] - lse[b, h, i]),
- * the column sums of the attention matrix whose logsumexp fa_fwd,
- * fa_fwd_decode or fa_fwd_tree returned.  The Nq query rows are the LAST Nq
- * positions: with causal = 1 row i sees j <= len_b - Nq + i, with 0 every
- * j < len_b.  A query row whose lse is -inf adds nothing, whatever q holds.
+ * the column sums of an attention matrix, given its logsumexp.  The Nq query
+ * rows are the LAST Nq positions: with causal = 1 row i sees j <= len_b - Nq
+ * + i, with 0 every j < len_b.  These have to be the rows that lse was taken
+ * over: fa_fwd's and fa_fwd_decode's with the same causal; of fa_fwd_tree's,
+ * one node's (causal = 0) or a chain's (causal = 1).  The nodes of a tree with
+ * branches see neither all rows nor the rows up to their own; call this for
+ * the accepted branch, once fa_cache_compact has made it the sequence's next
+ * rows, with its nodes' queries and lse and causal = 1 (shorter branches
+ * padded in front, lse = -inf).  A query row whose lse is -inf adds nothing,
+ * whatever q holds.
  * Rows j >= len_b get weights_in's value.
  *   q : [B, H, Nq, d]; k : [B, Hkv, Nk, d]; lse : fp32 [B, H, Nq]
  *   weights_in : fp32 [B, Hkv, Nk] or NULL (zeros); may be weights itself
@@ -448,6 +454,8 @@ FA_API fa_status_t fa_cache_select(const float *weights, const int *cache_seqlen
  * With fa_cache_select's lists this evicts; with base_b the row before which
  * a drafted tree starts and kept the nodes of the accepted branch, it makes
  * that branch the sequence's next rows.
+ * In place, rows behind the last place filled keep what they held, the weights
+ * among them: set those to 0 before new rows are appended there and weighed.
  */
 FA_API fa_status_t fa_cache_compact(const void *k, const int64_t *k_strides, const void *v,
                                     const int64_t *v_strides, const float *weights, void *k_out,
