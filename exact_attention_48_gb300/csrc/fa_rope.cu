@@ -22,7 +22,9 @@
 // fixed-point fraction of a turn per position (a 24-bit mantissa times
 // 2^66 / 2 pi, shifted), and the product modulo 2^64 is the fraction of a
 // turn itself: whole turns fall off the top.  Its top 32 bits go to
-// sincospi.
+// sincospi as fp32.  Error, in turns: rounding to 24 bits 2^-26 near half a
+// turn, the cut 2^-32, the fraction's last bits (1 + f / 4) |p| 2^-64, since
+// 2^66 / 2 pi is cut too; together below 2^-25 up to f = 128.
 
 #include <cstdint>
 

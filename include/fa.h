@@ -288,8 +288,10 @@ FA_API fa_status_t fa_fwd_decode(const void *q, const int64_t *q_strides, const 
  * by the angle a = position * inv_freq[i] and is scaled by `factor`:
  *     y1 = factor * (x1 cos a - x2 sin a),  y2 = factor * (x2 cos a + x1 sin a)
  * with pairs (i, i + rot/2), or (2i, 2i + 1) if interleaved = 1; the columns
- * past rot are copied.  Computed in fp32 (the angle modulo a turn to 2^-32
- * of one, for any 32-bit position) and rounded once.
+ * past rot are copied.  Computed in fp32 and rounded once; the angle is taken
+ * modulo a turn in 64-bit fixed point before it is rounded to fp32, within
+ * 2^-25 of a turn for any 32-bit position and frequencies of up to 128 radians
+ * per position.
  *   q, k           : inputs  [B, H, N, d] and [B, Hkv, N, d]; k and k_out are
  *                    NULL and Hkv = 0 when there is only q
  *   q_out, k_out   : outputs of the same shapes; each is its own input
