@@ -34,6 +34,7 @@ enum WaitSite : int {
   kSiteMaskEmpty,
   kSiteLseFull,
   kSiteLseEmpty,
+  kSiteSFree,
 };
 
 // Element strides of a [B, H, N, d] bf16 tensor whose d elements are

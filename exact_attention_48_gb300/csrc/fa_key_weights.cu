@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t dq = sdesc_sw128(aQ + qb * L::kQTile, 16, 1024);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          if (!(ok = mbar_wait(&s_free[2 * t + buf], ((nk >> 1) & 1) ^ 1, ctl, kSiteSFull))) break;
+          if (!(ok = mbar_wait(&s_free[2 * t + buf], ((nk >> 1) & 1) ^ 1, ctl, kSiteSFree))) break;
           tc_fence_after();
           const uint64_t dk = sdesc_sw128(aK + kb * L::kKBlock + t * L::kKTile, 16, 1024);
 #pragma unroll
@@ -588,7 +588,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         for (int x = n.x0; x < n.x1; ++x) {
           const uint32_t qb = nq % QB, buf = nq & 1;
           if (!(ok = mbar_wait(&q_full[qb], (nq / QB) & 1, ctl, kSiteQFull))) break;
-          if (!(ok = mbar_wait(&s_free[buf], ((nq >> 1) & 1) ^ 1, ctl, kSiteSFull))) break;
+          if (!(ok = mbar_wait(&s_free[buf], ((nq >> 1) & 1) ^ 1, ctl, kSiteSFree))) break;
           tc_fence_after();
           const uint64_t dq = sdesc_sw128(aQ + qb * L::kQTile, 16, 1024);
 #pragma unroll
