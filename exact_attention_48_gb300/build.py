@@ -59,8 +59,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
 # Test builds: the same sources with extra preprocessor definitions, linked
 # into their own folder under _build/ (never into libfa.so).  The one used
 # by the tests shortens every pipeline wait to FA_WAIT_LIMIT_NS (1 ms) and
-# leaves out the forward's first V load, so that the bounded-wait path
-# (FA_ERR_DEVICE_TIMEOUT through fa_device_status) can be exercised
+# leaves out one load of a kernel: the first V tile of the forward and of each
+# run of the drafted-tree attention, the first key block of the key weights of
+# few query rows and the first query tile of those of many.  So the bounded-wait
+# path (FA_ERR_DEVICE_TIMEOUT through fa_device_status) can be exercised
 # without any kernel waiting for long.
 VARIANTS = {
     "stalltest": ["-DFA_WAIT_LIMIT_NS=1000000ULL", "-DFA_TEST_SKIP_FIRST_V_LOAD"],

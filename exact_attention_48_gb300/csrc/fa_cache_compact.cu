@@ -11,7 +11,9 @@
 // while this one is written.  Heads times two tensors alone may leave SMs
 // idle, so a row is cut across CTAs where there are few.
 // Measured, B16 Hkv16 16384 to 8192 rows d128 with weights: out of place 318 us
-// (6810 GB/s, the HBM copy rate), in place 356 (6080).
+// (6810 GB/s, the HBM copy rate), in place 356 (6080).  One head has at most 17
+// CTAs in place, each of which walks the whole list: 131072 to 65536 rows of 1,
+// 2 and 8 heads take 102, 106 and 119 us, out of place 12, 23 and 82.
 
 #include <cstdint>
 

@@ -420,14 +420,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 // columns.
 //
 // What bounds it: a tile of 128 x 256 takes 1024 cycles of the tensor core and
-// 1024 of the exponentials, and 1790 in all: the exponential unit and the tensor
-// core are each busy 56 % of the time, the issue slots 58 %.  The rest is the
+// 1024 of the exponentials, and 1790 in all: the exponential unit is busy 56 % of
+// the time, the tensor core 52 %, the issue slots 58 % (B1 H32 N4096 d128).  The rest is the
 // weight warps' own chain between tiles (wait, load, a row's logsumexp and mask):
 // knocking out the exponentials saves 15 %, the products 8 %, the fetch of the
 // logsumexps with the mask 18 %.  No better: that work moved to an idle warp and
 // a table in shared memory (more instructions than it saves), into the shadow of
 // the load, or the warpgroups on alternate tiles instead of all on one.
-// Measured, B4 H32 N4096 d128 causal: 223.5 us, 1230 TFLOP/s (0.64 of burst).
+// Measured, B4 H32 N4096 d128 causal: 206 us in a short run of calls, 1335
+// TFLOP/s (0.69 of burst), 218 to 224 in a long one, with the SM clock that the
+// power limit leaves; d64 198 us, with half the products and as many exponentials.
 
 template <int D>
 struct KwRowsLayout {

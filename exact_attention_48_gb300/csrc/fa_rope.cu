@@ -38,7 +38,7 @@ constexpr int kRopeThreads = 128;
 // B4 H32 N4096 d128, 84 us: 4 heads and 2 CTAs 88.5, 6 and 2 84.8, 8 and 2 85.1, 3
 // and 3 87, 4 and 4 104).
 constexpr int kRopeUnroll = 4;
-constexpr int kRopeCtas = 6;  // (the append form, which has a tensor more to place, spills at 6: 4)
+constexpr int kRopeCtas = 6;  // (80 registers: the half-split form spills one; of the append form see the kernel)
 
 // f / (2 pi) turns as a 0.64 fixed-point number, modulo one turn.
 __device__ __forceinline__ uint64_t turn_fraction(float f) {
@@ -100,7 +100,10 @@ __device__ __forceinline__ Pieces pieces_of(const RopeParams &p, int c) {
 }
 
 // grid: x = blocks of `tokens` tokens, y = head groups.  Thread: piece c of
-// d / 16, token of the block, and first head.
+// d / 16, token of the block, and first head.  The append form, with a tensor
+// more to place, needs about 100 registers (at 80 it spills 15 to 30 of them) and
+// has four CTAs on an SM (B4 H32
+// N4096 d128, 805 MB: 149 us, 0.80 of the copy rate; the others 0.97).
 template <bool INTERLEAVED, bool APPEND>
 __global__ void __launch_bounds__(kRopeThreads, APPEND ? 4 : kRopeCtas) fa_rope_kernel(const RopeParams p) {
   extern __shared__ float table[];  // cos, then sin: [tokens][rot / 2]

@@ -6,12 +6,21 @@
 // time, as in the forward pass.
 //
 // What bounds it.  Every key costs 4 d bytes of cache and 4 d flops a row, so
-// up to about 280 rows (the tensor rate over the HBM rate) the cache traffic
-// sets the pace: each K and V tile is read once and used for all rows of the
-// unit, as A = Q (128 rows) against 128 keys on tcgen05.  The 128-key tiles
-// of all units form one list that is cut into equal runs, one per CTA (one
-// CTA per SM), whatever the sequences' lengths; a unit cut by a run's end
-// leaves partial results that a second kernel merges.
+// up to about 280 rows (the tensor rate over the HBM rate) the floor is the
+// cache traffic: each K and V tile is read once for up to two row tiles of a
+// unit, as A = Q (128 rows) against 128 keys on tcgen05 (a unit of more row
+// tiles is walked once by each pair of them).  The 128-key tiles of all units
+// form one list that is cut into equal runs, one per CTA (one CTA per SM),
+// whatever the sequences' lengths; a unit cut by a run's end leaves partial
+// results that a second kernel merges.
+//   One row tile at d = 128 keeps to the floor but for the runs' ends and the
+// merge (device times, B2 Hkv8 Nk65536, 79 us of traffic: 1 to 128 rows 89 to 93
+// us; B16 H16 Nt32, ragged up to 16384 keys: 242 to 248 against 243).  With two
+// row tiles the chain of each, S, softmax and P V, sets the pace (256 rows 128
+// us), and at d = 64, where a tile has half the bytes and as many exponentials,
+// with one as well (60 to 68 us and 104 against 40).  Three and four row tiles
+// take as long, 230 and 236 us at d = 128: a lone tile's CTAs have half the work
+// and as many SMs as a pair's.
 //
 // CTA (384 threads): warps 0..3 and 4..7 softmax (a row per thread), warp 8
 // TMA producer (Q, and K and V tiles through one ring), warp 9 MMA issuer and
@@ -26,6 +35,11 @@
 // most seven rounds, into shared memory while earlier tiles are worked on;
 // the softmax of those tiles tests bits.  Rows behind the sequence's end and
 // padding nodes' rows are set to zero in the V tile, for 0 * NaN is NaN.
+//
+// Rounding.  Scores, maxima, sums, O and the partial results are fp32.  The
+// weights of P V are rounded to bf16, since the product with bf16 V takes bf16 on
+// its other side: off by at most 2^-8 of each, and O is divided by the sum of the
+// rounded ones.
 //
 // Scores that are not finite.  A score of -inf weighs nothing: while a row has
 // seen no other its maximum stays -inf and its exponents are taken relative to 0
@@ -370,7 +384,7 @@ struct RowState {
 };
 
 struct SoftmaxArgs {
-  uint64_t *s_full, *p_ready, *pv_done, *full, *mask_full;
+  uint64_t *s_full, *p_ready, *pv_done, *full;
   uint32_t s_phase;  // of the tile's S buffer
   uint32_t tS, tO;   // its columns and this warpgroup's O, lane base added
   uint8_t *ring;    // K and V slots
@@ -825,7 +839,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       a.p_ready = &p_ready[2 * t];
       a.pv_done = &pv_done[2 * t];
       a.full = full;
-      a.mask_full = mask_full;
       a.tS = tmem + t * 128 + lane_base;
       a.tO = tmem + L::kO + t * D + lane_base;
       a.ring = ring;
@@ -1086,7 +1099,9 @@ __global__ void __launch_bounds__(WARPS * 32) fa_tree_merge_kernel(const TreePar
     p.lse[(static_cast<long long>(b) * p.H + h) * p.Nt + node] = any ? (M + log2f(l)) * kLn2 : -INFINITY;
 }
 
-// The merge is launched as a dependent of the main kernel.
+// The merge is launched as a dependent of the main kernel: its launch is set up
+// while that one runs.  The main kernel triggers nothing early, so the blocks of
+// the merge are placed when its last CTA has left.
 template <int D, int ROWS, int WARPS>
 cudaError_t launch_merge(const TreeParams &p, cudaStream_t stream) {
   const long long cuts = p.cuts_by_unit ? static_cast<long long>(p.B) * p.Hkv : p.ranges;
