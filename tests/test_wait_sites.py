@@ -1,7 +1,6 @@
 """The sites that bounded waits of the cache operators report
-(fa_debug_last_wait_site): a wait for a
-buffer to be free never reports the site of a wait for one to be filled, or a
-timeout would name the wrong side."""
+(fa_debug_last_wait_site): a wait for a buffer to be free never reports the
+site of a wait for one to be filled, or a timeout would name the wrong side."""
 import collections
 import os
 import re
