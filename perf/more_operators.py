@@ -303,6 +303,7 @@ def _verify(c, s):
         node = torch.where(yes, torch.full_like(node, i), node)
         accepted[seq, count.clamp(max=Nt - 1)] = torch.where(yes, node.int(), accepted[seq, count.clamp(max=Nt - 1)])
         count = count + yes.long()
+    rest = torch.where(rest.sum(-1, keepdim=True) > 0.0, rest, s["p"][seq, node].double())
     below = rest.cumsum(-1)
     token = (below <= s["u"][:, :1].double() * below[:, -1:]).sum(-1)
     return [accepted, count.int(), token.int()]
@@ -495,6 +496,8 @@ def _exact_verify(c, s):
             if hit is None:
                 break
             path.append(hit)
+        if not rest.sum().item() > 0.0:  # (nothing is left but by rounding: p itself)
+            rest = p
         sums = list(itertools.accumulate(rest.tolist()))
         follows.append(next(x for x, below in enumerate(sums) if below > u[b][0] * sums[-1]))
         accepted.append(path + [-1] * (c["Nt"] - len(path)))
