@@ -10,24 +10,15 @@
 // bounds it.  A CTA takes a few tokens and all their heads (or, with few
 // tokens, a part of the heads): its threads first share the cosines and sines
 // of those tokens out among themselves through shared memory, one angle per
-// token and pair and not per head, then each keeps the eight pairs of its
+// token and pair and not per head (see fa_angles.cuh), then each keeps the eight pairs of its
 // (token, piece) in registers over the heads it walks.  The first heads' rows
 // are on their way before the angles are computed.
 // Measured on the device, B4 H32 Hkv32 N4096 d128: 82 us, 6570 GB/s (0.97 of the
 // copy rate); B8 H16 Hkv4 N2047 d64, 84 MB: 16.6 us.
-//
-// Angles.  The product p * f has to be exact to about 2^-20 of a turn for
-// positions in the millions, which fp32 cannot hold and fp64 (a sixty-fourth
-// of the fp32 rate here) is too slow for.  Each frequency becomes a 64-bit
-// fixed-point fraction of a turn per position (a 24-bit mantissa times
-// 2^66 / 2 pi, shifted), and the product modulo 2^64 is the fraction of a
-// turn itself: whole turns fall off the top.  Its top 32 bits go to
-// sincospi as fp32.  Error, in turns: rounding to 24 bits 2^-26 near half a
-// turn, the cut 2^-32, the fraction's last bits (1 + f / 4) |p| 2^-64, since
-// 2^66 / 2 pi is cut too; together below 2^-25 up to f = 128.
 
 #include <cstdint>
 
+#include "fa_angles.cuh"
 #include "fa_cache.h"
 
 namespace fa {
@@ -39,65 +30,6 @@ constexpr int kRopeThreads = 128;
 // and 3 87, 4 and 4 104).
 constexpr int kRopeUnroll = 4;
 constexpr int kRopeCtas = 6;  // (80 registers: the half-split form spills one; of the append form see the kernel)
-
-// f / (2 pi) turns as a 0.64 fixed-point number, modulo one turn.
-__device__ __forceinline__ uint64_t turn_fraction(float f) {
-  const uint32_t bits = __float_as_uint(f);
-  const int e = (bits >> 23) & 255;
-  const uint64_t m = (bits & 0x7fffffu) | (e ? 0x800000u : 0u);
-  constexpr uint64_t kInv2Pi = 0xa2f9836e4e441529ull;  // floor(2^66 / (2 pi))
-  const uint64_t lo = m * kInv2Pi, hi = __umul64hi(m, kInv2Pi);
-  const int s = 152 - (e ? e : 1);  // f / (2 pi) * 2^64 = (m * kInv2Pi) >> s
-  uint64_t r;
-  if (s <= 0)
-    r = s > -64 ? lo << -s : 0;
-  else if (s < 64)
-    r = (lo >> s) | (hi << (64 - s));
-  else
-    r = s < 128 ? hi >> (s - 64) : 0;
-  return (bits >> 31) ? 0 - r : r;
-}
-
-__device__ __forceinline__ float2 unpack2(uint32_t u) {
-  return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
-}
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t *>(&v);
-}
-
-// A thread's two 16-byte pieces of a row.  Neighbouring threads take
-// neighbouring pieces, so that a warp's accesses fill whole sectors.
-struct Pieces {
-  int c0, c1;      // first columns
-  int p0, p1;      // pairs p0 .. p0 + 3 and p1 .. p1 + 3 (of the two pieces, or of both together)
-  bool t0, t1;     // the pieces turn
-};
-
-template <bool INTERLEAVED>
-__device__ __forceinline__ Pieces pieces_of(const RopeParams &p, int c) {
-  Pieces x;
-  if (INTERLEAVED) {  // a piece holds four whole pairs
-    x.c0 = c * 8;
-    x.c1 = p.d / 2 + c * 8;
-    x.p0 = x.c0 / 2;
-    x.p1 = x.c1 / 2;
-    x.t0 = x.c0 < p.rot;
-    x.t1 = x.c1 < p.rot;
-  } else if (c * 16 < p.rot) {  // the two halves of eight pairs
-    x.c0 = c * 8;
-    x.c1 = p.rot / 2 + c * 8;
-    x.p0 = c * 8;
-    x.p1 = c * 8 + 4;
-    x.t0 = x.t1 = true;
-  } else {  // two pieces past rot
-    x.c0 = p.rot + (c * 16 - p.rot) / 2;
-    x.c1 = x.c0 + (p.d - p.rot) / 2;
-    x.p0 = x.p1 = 0;
-    x.t0 = x.t1 = false;
-  }
-  return x;
-}
 
 // grid: x = blocks of `tokens` tokens, y = head groups.  Thread: piece c of
 // d / 16, token of the block, and first head.  The append form, with a tensor
@@ -115,7 +47,7 @@ __global__ void __launch_bounds__(kRopeThreads, APPEND ? 4 : kRopeCtas) fa_rope_
   const int heads_at_once = kRopeThreads / lanes;
   const int t = t0 + tl;
   const int b = t / p.N, n = t - b * p.N;
-  const Pieces x = pieces_of<INTERLEAVED>(p, c);
+  const Pieces x = pieces_of<INTERLEAVED>(p.d, p.rot, c);
   // rows of the three tensors' first heads
   const __nv_bfloat16 *src[3] = {p.q + b * p.sq.b + n * p.sq.n, p.k + b * p.sk.b + n * p.sk.n, nullptr};
   __nv_bfloat16 *dst[3] = {p.qo + b * p.sqo.b + n * p.sqo.n, nullptr, nullptr};
@@ -174,10 +106,8 @@ __global__ void __launch_bounds__(kRopeThreads, APPEND ? 4 : kRopeCtas) fa_rope_
     const int be = te / p.N, ne = te - be * p.N;
     const long long pos = p.positions ? p.positions[be * p.pos_b + ne]
                                       : (APPEND ? static_cast<long long>(p.cache_len[be]) - p.N + ne : ne);
-    const uint64_t a = static_cast<uint64_t>(pos) * turn_fraction(p.inv_freq[i]);
-    const float half_turns = static_cast<float>(static_cast<int32_t>(a >> 32)) * 4.656612873077393e-10f;  // 2^-31
     float sn, cs;
-    sincospif(half_turns, &sn, &cs);
+    angle_of(pos, p.inv_freq[i], &cs, &sn);
     cos_t[e] = cs * p.factor;
     sin_t[e] = sn * (p.factor * p.sign);
   }
