@@ -32,3 +32,10 @@ from .cache_ops import (  # noqa: F401
     fa_rope_frequencies,
     fa_tree_workspace_bytes,
 )
+from .cache8_ops import (  # noqa: F401
+    fa_cache_compact_fp8,
+    fa_fwd_tree_fp8,
+    fa_rope_append_fp8,
+    fa_tree_fp8_workspace_bytes,
+    fa_tree_verify,
+)

@@ -107,6 +107,20 @@ def library(path: str | None = None):
             lib.fa_cache_compact.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, vp,
                                              i, i, i, i, i, i, vp]
             lib.fa_cache_compact.restype = i
+            lib.fa_rope_append_fp8.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i64,
+                                               vp, i, i, i, i, i, i, i, i, f, i, vp]
+            lib.fa_rope_append_fp8.restype = i
+            lib.fa_tree_fp8_workspace_bytes.argtypes = [i, i, i, i, i, i]
+            lib.fa_tree_fp8_workspace_bytes.restype = sz
+            lib.fa_fwd_tree_fp8.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, vp,
+                                            i, i, i, i, i, i, i, f, vp, sz, vp]
+            lib.fa_fwd_tree_fp8.restype = i
+            lib.fa_cache_compact_fp8.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, vp,
+                                                 i, i, i, i, i, i, i, vp]
+            lib.fa_cache_compact_fp8.restype = i
+            lib.fa_tree_verify.argtypes = [vp, i64, vp, i64, vp, i64, i64, vp, i64, i64, vp, i64, vp, vp, vp,
+                                           i, i, i, vp]
+            lib.fa_tree_verify.restype = i
             lib.fa_status_string.argtypes = [i]
             lib.fa_status_string.restype = ctypes.c_char_p
             _lib = lib

@@ -1,0 +1,216 @@
+// fa_append_fp8.cu -- rotary positions and the append to a cache held in 8 bits.
+//
+// A block of rows of a head has one scale, the least power of two by which its
+// rows fit e4m3 (448): k turned by its positions in fp32 (fa_angles.cuh), or v,
+// divided by it and rounded to codes once.  Where new rows go on in a block that
+// holds rows already, the scale is the greater of the two; if it grew, the old
+// rows' codes are rounded to it again (a shift of exponents, exact but for codes
+// that fall below e4m3's normal range).
+//
+// What bounds it.  HBM: a token's q is read and written in bf16, its k and v are
+// read in bf16 and written in 8 bits.  A CTA takes the tokens of one block of
+// rows and walks heads: the tokens' angles are computed once, into shared memory,
+// and a head's rows stay in registers between the search for their greatest value
+// and the rounding, so nothing is read twice.  With few tokens several heads share
+// the CTA and the heads are cut across CTAs.
+
+#include <cfloat>
+#include <cstdint>
+
+#include "fa_angles.cuh"
+#include "fa_cache8.h"
+#include "ptx.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ long long floor_shift(long long x, int s) { return x >> s; }  // (arithmetic: floors)
+
+// A value as e4m3 stores it: infinities become NaN (the conversion would
+// saturate them).
+__device__ __forceinline__ float storable(float x) { return fabsf(x) <= FLT_MAX ? x : NAN; }
+
+// grid: x = blocks of rows (per_b of a sequence), y = head groups.  A head's
+// slots * d / 16 pieces take ITEMS per thread, or a part of the threads.
+template <bool INTERLEAVED, int ITEMS>
+__global__ void __launch_bounds__(kThreads) fa_append_fp8_kernel(const Append8Params p) {
+  extern __shared__ float table[];  // cos, then sin: [slots][rot / 2]
+  __shared__ uint32_t most[3][kThreads / 4];  // greatest values of the heads at work, used in turn
+  const int per_row = p.d >> 4, half = p.rot >> 1, tid = threadIdx.x;
+  const int lanes = ITEMS > 1 ? kThreads : per_row * p.slots;
+  const int heads_at_once = kThreads / lanes;
+  const int b = blockIdx.x / p.per_b, j = blockIdx.x - b * p.per_b;
+  const int block = 1 << p.block_log2;
+  const long long len = p.cache_len[b], start = len - p.N;
+  // the block of rows [lo, lo + block) and the tokens n0 .. n0 + count - 1 in it
+  const long long lo = (floor_shift(start, p.block_log2) + j) << p.block_log2;
+  const long long from = lo > start ? lo : start, to = lo + block < len ? lo + block : len;
+  if (from >= to) return;
+  const int n0 = static_cast<int>(from - start), count = static_cast<int>(to - from);
+  // of those, the ones with a row of the cache
+  const bool any_row = from < p.Nk && to > 0;
+  const bool has_old = start > lo && start > 0 && any_row;
+  const int blk = any_row ? static_cast<int>(lo >> p.block_log2) : 0;
+
+  for (int i = tid; i < 3 * (kThreads / 4); i += kThreads) most[i / (kThreads / 4)][i % (kThreads / 4)] = 0u;
+  float *cos_t = table, *sin_t = table + p.slots * half;
+  for (int e = tid; e < count * half; e += kThreads) {
+    const int s = e / half, i = e - s * half;
+    const long long pos = p.positions ? p.positions[b * p.pos_b + n0 + s] : from + s;
+    float cs, sn;
+    angle_of(pos, p.inv_freq[i], &cs, &sn);
+    cos_t[e] = cs * p.factor;
+    sin_t[e] = sn * p.factor;
+  }
+  __syncthreads();
+
+  const int hl = tid / lanes, in_head = tid - hl * lanes;
+  const int c = in_head & (per_row - 1), slot0 = in_head / per_row, slot_step = kThreads / per_row;
+  const Pieces x = pieces_of<INTERLEAVED>(p.d, p.rot, c);
+  const int heads = p.H + 2 * p.Hkv, step = heads_at_once * gridDim.y;
+  int turn = 0;
+  for (int h0 = blockIdx.y * heads_at_once; h0 < heads; h0 += step, turn = turn == 2 ? 0 : turn + 1) {
+    const int hh = h0 + hl;
+    const bool is_q = hh < p.H, is_k = !is_q && hh < p.H + p.Hkv;
+    const bool head_on = hl < heads_at_once && hh < heads && (is_q || any_row);
+    const int h = is_q ? hh : (is_k ? hh - p.H : hh - p.H - p.Hkv);
+    const __nv_bfloat16 *src = is_q ? p.q + b * p.sq.b + h * p.sq.h
+                                    : (is_k ? p.k + b * p.sk.b + h * p.sk.h : p.v + b * p.sv.b + h * p.sv.h);
+    const long long sn_ = is_q ? p.sq.n : (is_k ? p.sk.n : p.sv.n);
+    float *scale = (is_k ? p.ks : p.vs) + (static_cast<long long>(b) * p.Hkv + h) * p.blocks + blk;
+    float old = 0.0f;
+    if (head_on && !is_q && has_old) old = *scale;
+    float y[ITEMS][16];
+    float top = 0.0f;
+    // whether a thread's item is at work (of K and V: has a row of the cache)
+    auto on = [&](int it) {
+      const int s = slot0 + it * slot_step;
+      return head_on && s < count && (is_q || (from + s >= 0 && from + s < p.Nk));
+    };
+#pragma unroll
+    for (int it = 0; it < ITEMS; ++it) {
+      if (!on(it)) continue;
+      const int s = slot0 + it * slot_step;
+      const __nv_bfloat16 *row = src + (n0 + s) * sn_;
+      const uint4 w0 = __ldcs(reinterpret_cast<const uint4 *>(row + x.c0));
+      const uint4 w1 = __ldcs(reinterpret_cast<const uint4 *>(row + x.c1));
+      const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 v = unpack2(w[i]);
+        y[it][2 * i] = v.x;
+        y[it][2 * i + 1] = v.y;
+      }
+      if (is_q || is_k) {
+        const float *cs = cos_t + s * half, *sn = sin_t + s * half;
+        if (INTERLEAVED) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (!(i < 4 ? x.t0 : x.t1)) continue;
+            const int pr = i < 4 ? x.p0 + i : x.p1 + i - 4;
+            const float a = y[it][2 * i], z = y[it][2 * i + 1];
+            y[it][2 * i] = a * cs[pr] - z * sn[pr];
+            y[it][2 * i + 1] = z * cs[pr] + a * sn[pr];
+          }
+        } else if (x.t0) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int pr = i < 4 ? x.p0 + i : x.p1 + i - 4;
+            const float a = y[it][i], z = y[it][8 + i];
+            y[it][i] = a * cs[pr] - z * sn[pr];
+            y[it][8 + i] = z * cs[pr] + a * sn[pr];
+          }
+        }
+      }
+      if (is_q) {
+        uint32_t o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = pack2(y[it][2 * i], y[it][2 * i + 1]);
+        __nv_bfloat16 *dst = p.qo + b * p.sqo.b + h * p.sqo.h + (n0 + s) * p.sqo.n;
+        __stcs(reinterpret_cast<uint4 *>(dst + x.c0), make_uint4(o[0], o[1], o[2], o[3]));
+        __stcs(reinterpret_cast<uint4 *>(dst + x.c1), make_uint4(o[4], o[5], o[6], o[7]));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          y[it][i] = storable(y[it][i]);
+          top = fmaxf(top, fabsf(y[it][i]));  // (fmaxf passes over NaN)
+        }
+      }
+    }
+    // the heads' greatest values (that of this turn's slot was last read two barriers ago)
+    const int next_turn = turn == 2 ? 0 : turn + 1;
+    if (tid < heads_at_once) most[next_turn][tid] = 0u;
+    if (top > 0.0f) atomicMax(&most[turn][hl], __float_as_uint(top));
+    __syncthreads();
+    if (!head_on || is_q) continue;
+    const float now = fmaxf(old, least_scale(__uint_as_float(most[turn][hl]))), inv = 1.0f / now;
+    uint8_t *dst = is_k ? p.kc + b * p.skc.b + h * p.skc.h : p.vc + b * p.svc.b + h * p.svc.h;
+    const long long dn = is_k ? p.skc.n : p.svc.n;
+    if (has_old && now > old) {  // the rows before the new ones, 16 bytes a thread
+      const int rows = static_cast<int>(start - lo) * per_row;
+      const float r = old / now;
+      for (int e = in_head; e < rows; e += lanes) {
+        uint4 *at = reinterpret_cast<uint4 *>(dst + (lo + e / per_row) * dn + (e & (per_row - 1)) * 16);
+        uint4 w = *at;
+        w.x = rescale_codes(w.x, r);
+        w.y = rescale_codes(w.y, r);
+        w.z = rescale_codes(w.z, r);
+        w.w = rescale_codes(w.w, r);
+        *at = w;
+      }
+    }
+#pragma unroll
+    for (int it = 0; it < ITEMS; ++it) {
+      if (!on(it)) continue;
+      uint8_t *row = dst + (from + slot0 + it * slot_step) * dn;
+      uint32_t o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        o[i] = pack_e4m3x4(y[it][4 * i] * inv, y[it][4 * i + 1] * inv, y[it][4 * i + 2] * inv, y[it][4 * i + 3] * inv);
+      *reinterpret_cast<uint2 *>(row + x.c0) = make_uint2(o[0], o[1]);
+      *reinterpret_cast<uint2 *>(row + x.c1) = make_uint2(o[2], o[3]);
+    }
+    if (in_head == 0) *scale = now;
+  }
+}
+
+template <bool INTERLEAVED, int ITEMS>
+cudaError_t launch_append8_t(const Append8Params &p, cudaStream_t stream) {
+  auto kern = fa_append_fp8_kernel<INTERLEAVED, ITEMS>;
+  const size_t smem = sizeof(float) * p.slots * p.rot;  // up to 64 KB
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 65536);
+  if (e != cudaSuccess) return e;
+  kern<<<dim3(static_cast<unsigned>(p.B) * p.per_b, p.head_groups), kThreads, smem, stream>>>(p);
+  return cudaGetLastError();
+}
+
+template <bool INTERLEAVED>
+cudaError_t launch_append8_i(const Append8Params &p, cudaStream_t stream) {
+  switch (p.slots * (p.d / 16) / kThreads) {
+    case 4: return launch_append8_t<INTERLEAVED, 4>(p, stream);
+    case 2: return launch_append8_t<INTERLEAVED, 2>(p, stream);
+    default: return launch_append8_t<INTERLEAVED, 1>(p, stream);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_append8(bool interleaved, const Append8Params &in, cudaStream_t stream) {
+  Append8Params p = in;
+  const int block = 1 << p.block_log2;
+  p.per_b = (p.N - 1 + block - 1) / block + 1;
+  p.slots = 1;
+  while (p.slots < p.N && p.slots < block) p.slots *= 2;
+  const int lanes = p.slots * (p.d / 16);
+  const int heads = p.H + 2 * p.Hkv, at_once = lanes < kThreads ? kThreads / lanes : 1;
+  const long long blocks = static_cast<long long>(p.B) * p.per_b;
+  long long groups = (heads + at_once - 1) / at_once;
+  const long long want = (4 * 152 + blocks - 1) / blocks;  // four CTAs an SM where there are heads for them
+  if (groups > want) groups = want;
+  p.head_groups = groups > 65535 ? 65535 : static_cast<int>(groups);
+  return interleaved ? launch_append8_i<true>(p, stream) : launch_append8_i<false>(p, stream);
+}
+
+}  // namespace fa

@@ -16,6 +16,12 @@ namespace fa {
 bool encode_map(CUtensorMap *map, const void *base, int B, int H, int N, int d, const Strides &s,
                 unsigned box_rows = 128, unsigned box_heads = 1);
 
+// An [B, H, N, d] tensor of one byte an element (strides s in bytes) as 4-D
+// (d, N, H, B); one box is a whole row x box_rows rows of one head, swizzled by
+// the row's 128 (d = 128) or 64 bytes.  Rows past N read as 0.
+bool encode_map_rows8(CUtensorMap *map, const void *base, int B, int H, int N, int d, const Strides &s,
+                      unsigned box_rows);
+
 // A caller's strides made usable: the stride of an extent-1 dimension is
 // never used, so it is replaced by a harmless valid value; then every
 // stride must be positive and a multiple of 8 elements (16 bytes: TMA and

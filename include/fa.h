@@ -467,6 +467,120 @@ FA_API fa_status_t fa_cache_compact(const void *k, const int64_t *k_strides, con
                                     int M, int d, cudaStream_t stream);
 
 /*
+ * A cache held in 8 bits.  k and v are e4m3 codes (OCP E4M3, a byte each; NaN
+ * but no infinities) [B, Hkv, Nk, d] with element strides that are multiples of
+ * 16, and each block of `block` rows of a head has one scale: element (b, h, n, c)
+ * stands for code * scale[b, h, n / block], scales fp32, contiguous
+ * [B, Hkv, ceil(Nk / block)], powers of two from 2^-100 to 2^120.  block is 16,
+ * 32, 64 or 128 (FA_ERR_UNSUPPORTED otherwise); k and v have scales of their own.
+ * (e4m3 is a floating type: a scale between two powers of two would gain
+ * nothing, and a block is given another one by a shift of its exponents.)  The
+ * conventions of the operators around the cache above hold for these calls too.
+ * A scale none of whose rows is in use may hold anything.
+ */
+
+/*
+ * fa_rope_append to a cache held in 8 bits: q is rotated into q_out (which may be
+ * q) in bf16; k, rotated in fp32, and v become cache rows, rounded once.  For each
+ * block of rows that gets new ones,
+ *     need  = the least power of two >= 2^-100 by which the greatest finite
+ *             magnitude among its new rows is at most 448,
+ *     scale = need, or the greater of need and the present scale if the block
+ *             holds rows before the new ones (rows below cache_seqlens[b] - N),
+ *     code  = e4m3(x / scale), to the nearest, ties to even; NaN and the
+ *             infinities become NaN,
+ * and where the scale grew the old rows' codes become e4m3(code * old / new):
+ * exact but for codes that fall below e4m3's normal range.  Rows behind the
+ * new ones keep their codes.  Other arguments as in fa_rope_append.
+ */
+FA_API fa_status_t fa_rope_append_fp8(const void *q, const int64_t *q_strides, const void *k,
+                                      const int64_t *k_strides, const void *v, const int64_t *v_strides, void *q_out,
+                                      const int64_t *q_out_strides, void *k_cache, const int64_t *k_cache_strides,
+                                      void *v_cache, const int64_t *v_cache_strides, float *k_scale, float *v_scale,
+                                      const int *cache_seqlens, const int *positions, int64_t positions_stride,
+                                      const float *inv_freq, int B, int H, int Hkv, int N, int Nk, int d, int rot,
+                                      int interleaved, float factor, int block, cudaStream_t stream);
+
+/*
+ * fa_fwd_tree over a cache held in 8 bits: q, o bf16, lse fp32, the tree, padding,
+ * scores that are not finite and the workspace as there.  parents may be NULL: the
+ * last Nt rows are a chain, each of which sees the rows up to its own (Nt = 1: one
+ * new token; several: the causal decode).  The products run in f16 on the codes'
+ * exact values, q scaled by a power of two a row; scores, sums and o are fp32,
+ * and a weight is off by at most 2^-11 of it or 2^-31 of its row's greatest.
+ */
+FA_API size_t fa_tree_fp8_workspace_bytes(int B, int H, int Hkv, int Nt, int Nk, int d);
+
+FA_API fa_status_t fa_fwd_tree_fp8(const void *q, const int64_t *q_strides, const void *k, const int64_t *k_strides,
+                                   const void *v, const int64_t *v_strides, const float *k_scale,
+                                   const float *v_scale, void *o, const int64_t *o_strides, float *lse,
+                                   const int *parents, int64_t parents_stride, const int *cache_seqlens, int B, int H,
+                                   int Hkv, int Nt, int Nk, int d, int block, float scale, void *workspace,
+                                   size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * fa_cache_compact of a cache held in 8 bits: for every head and every i in
+ * [0, M) with kept[i] >= 0, row base_b + i of k_out, v_out becomes row base_b +
+ * kept[i] of k, v.  A block of the output that rows move to gets the greatest
+ * scale of the blocks they come from; rows of it before base_b are kept as well,
+ * and its present scale counts with them (so out of place they, and that scale,
+ * have to be there).  A row whose own scale was smaller has its codes rounded
+ * to the new one, the others move bit by bit.  Rows of a written block that
+ * are neither lose their values; blocks that no row moves to stay as they are.
+ *   k_scale, v_scale         : [B, Hkv, ceil(Nk / block)]
+ *   k_scale_out, v_scale_out : [B, Hkv, ceil(Nk_out / block)]
+ *   B * Hkv * (ceil(M / 128) + 1) < 2^31
+ * Either every output is its input (same pointers and strides, Nk_out = Nk: in
+ * place; the lists must then ascend as for fa_cache_compact), or no output shares
+ * an element with an argument.
+ */
+FA_API fa_status_t fa_cache_compact_fp8(const void *k, const int64_t *k_strides, const void *v,
+                                        const int64_t *v_strides, const float *k_scale, const float *v_scale,
+                                        void *k_out, const int64_t *k_out_strides, void *v_out,
+                                        const int64_t *v_out_strides, float *k_scale_out, float *v_scale_out,
+                                        const int *kept, int64_t kept_b_stride, int64_t kept_h_stride,
+                                        const int *base, int B, int Hkv, int Nk, int Nk_out, int M, int d, int block,
+                                        cudaStream_t stream);
+
+/*
+ * Verification of drafted tokens against the target's probabilities, from given
+ * random numbers.  The tree is fa_fwd_tree's, and node 0 is its root (the last
+ * token that is decided; parent -1).  target[b, n] is the target's distribution
+ * at node n and draft[b, n] the one that n's children were drawn from, each one by
+ * itself.  From the root on, a node's children are tried in ascending order: with
+ *     R = target[b, n], S = 1
+ * before the first, child i with token x = tokens[b, i] is accepted, and the walk
+ * goes on from it, if
+ *     uniforms[b, i] * draft[b, n, x] * S < R[x];
+ * otherwise R becomes max(R - S * draft[b, n], 0) and S the sum of R.  Where no
+ * child is left, the next token is the least y with
+ *     R[0] + .. + R[y] > uniforms[b, 0] * (R[0] + .. + R[V - 1]).
+ * Should R be zero there (rounding, or a token that its draft's row gives no
+ * probability, can make it so), target[b, n] takes its place; -1 if that is zero
+ * too.  The accepted tokens and the next one are then distributed as the
+ * target's.  draft NULL: each child was chosen for certain (its token's draft
+ * probability is 1 and the others' 0), as by a draft of likeliest tokens.
+ *   parents, tokens, uniforms: node (b, i) at [b * stride + i]; a node whose
+ *               parent is not in [0, i) or whose token is not in [0, V) is never
+ *               tried; with parents[b, 0] != -1 the sequence is padding
+ *   uniforms  : fp32, in [0, 1)
+ *   target, draft : fp32, finite and not negative, row (b, n) at
+ *               b * b_stride + n * n_stride, V contiguous values (4-byte aligned)
+ *   accepted  : int32 [B, Nt]: the accepted nodes from the root on, -1 behind
+ *               them: fa_cache_compact's list (base_b = len_b - Nt)
+ *   counts    : int32 [B], how many; 0 for padding
+ *   next_token: int32 [B]; -1 for padding
+ *   1 <= Nt <= 128; V <= 2^30
+ * Sums are taken to about 48 bits, so that a number decides as in the formulas.
+ */
+FA_API fa_status_t fa_tree_verify(const int *parents, int64_t parents_stride, const int *tokens,
+                                  int64_t tokens_stride, const float *target, int64_t target_b_stride,
+                                  int64_t target_n_stride, const float *draft, int64_t draft_b_stride,
+                                  int64_t draft_n_stride, const float *uniforms, int64_t uniforms_stride,
+                                  int *accepted, int *counts, int *next_token, int B, int Nt, int V,
+                                  cudaStream_t stream);
+
+/*
  * Size in bytes of the fixed device array that fa_bwd_noalloc uses as its
  * scratch (8 MiB).  Every GPU that loads the library holds this array until
  * the process exits.  It covers B * H * Np <= 1,048,576 padded rows, where
