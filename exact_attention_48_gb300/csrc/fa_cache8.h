@@ -10,7 +10,7 @@ namespace fa {
 
 // Attention of the newest rows of each sequence, or of a drafted tree, over an
 // 8-bit cache.  The G * Nt query rows of a unit (b, hk), head after head, are
-// cut into groups of 16 * row_tiles rows, one CTA each; the 128-key tiles of all
+// cut into groups of `rows` rows, one CTA each; the 128-key tiles of all
 // units are cut into `ranges` equal runs (fa_runs.cuh).  CTA x takes run
 // x / groups for row group x % groups.
 struct Tree8Params {
@@ -23,27 +23,29 @@ struct Tree8Params {
   long long par_b;
   const int *cache_len;       // [B] or null
   int *status;
-  float *part_o;              // [2 * ctas][16 * row_tiles][d], normalised
-  float *part_lse;            // [2 * ctas][16 * row_tiles], log2 units; +inf marks padding
+  float *part_o;              // [2 * ctas][rows][d], normalised
+  float *part_lse;            // [2 * ctas][rows], log2 units; +inf marks padding
   int4 *cuts;                 // as in TreeParams
   int cuts_by_unit;
   int B, H, Hkv, G, Nt, Nk, d;
   int block_log2, blocks;     // rows of a scale, scales of a head
-  int row_tiles, groups, ranges;
+  int rows, groups, ranges;
   int whole;                  // runs end at units' ends: no partial results
   float scale_log2;
 };
 
 struct Tree8Plan {
-  int row_tiles, groups, ranges, whole;
+  int rows, groups, ranges, whole;
   bool merge;
   size_t part_rows;
 };
-Tree8Plan plan_tree8(int B, int H, int Hkv, int Nt, int Nk);
+Tree8Plan plan_tree8(int B, int H, int Hkv, int Nt, int Nk, int d);
 
 // tk, tv: maps of encode_map_rows8 with boxes of 128 rows.
 cudaError_t launch_tree8(const CUtensorMap &tk, const CUtensorMap &tv, const Tree8Params &p, bool merge,
                          cudaStream_t stream);
+// Its main kernel at d = 128.
+cudaError_t launch_tree8_tc(const CUtensorMap &tk, const CUtensorMap &tv, const Tree8Params &p, cudaStream_t stream);
 
 // Rotary positions and the append to an 8-bit cache: as RopeParams' append form,
 // with codes and scales instead of bf16 rows.

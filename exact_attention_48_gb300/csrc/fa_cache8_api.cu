@@ -41,7 +41,7 @@ extern "C" {
 
 size_t fa_tree_fp8_workspace_bytes(int B, int H, int Hkv, int Nt, int Nk, int d) {
   if (check_tree(B, H, Hkv, Nt, Nk, d, 1.0f) != FA_OK) return 0;
-  const Tree8Plan pl = plan_tree8(B, H, Hkv, Nt, Nk);
+  const Tree8Plan pl = plan_tree8(B, H, Hkv, Nt, Nk, d);
   return pl.merge ? round256(pl.part_rows * d * 4) + round256(pl.part_rows * 4) + round256(pl.ranges * sizeof(int4)) : 0;
 }
 
@@ -75,7 +75,7 @@ fa_status_t fa_fwd_tree_fp8(const void *q, const int64_t *q_strides, const void 
   if (overlap(vq, vo, B, d) || meet(ro, rl) || meet(used[2], rl)) return FA_ERR_INVALID_ARGUMENT;
   for (int i = 3; i < 9; ++i)
     if (meet(used[i], ro) || meet(used[i], rl)) return FA_ERR_INVALID_ARGUMENT;
-  const Tree8Plan pl = plan_tree8(B, H, Hkv, Nt, Nk);
+  const Tree8Plan pl = plan_tree8(B, H, Hkv, Nt, Nk, d);
   const size_t need = fa_tree_fp8_workspace_bytes(B, H, Hkv, Nt, Nk, d);
   Scratch ws(workspace, workspace_bytes, need);
   st = ws.check(used, 9);
@@ -111,7 +111,7 @@ fa_status_t fa_fwd_tree_fp8(const void *q, const int64_t *q_strides, const void 
   p.d = d;
   p.block_log2 = log2_of(block);
   p.blocks = blocks_of(Nk, block);
-  p.row_tiles = pl.row_tiles;
+  p.rows = pl.rows;
   p.groups = pl.groups;
   p.ranges = pl.ranges;
   p.whole = pl.whole;

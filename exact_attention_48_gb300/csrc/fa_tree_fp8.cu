@@ -187,8 +187,12 @@ struct Rows {
     const float by = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 #pragma unroll
     for (int s = 0; s < D / 16; ++s) {
-      q[s][x] = pack_f16x2(__uint_as_float(w[s].x << 16) * by, __uint_as_float(w[s].x & 0xffff0000u) * by);
-      q[s][x + 2] = pack_f16x2(__uint_as_float(w[s].y << 16) * by, __uint_as_float(w[s].y & 0xffff0000u) * by);
+      float v[4] = {__uint_as_float(w[s].x << 16), __uint_as_float(w[s].x & 0xffff0000u), __uint_as_float(w[s].y << 16),
+                    __uint_as_float(w[s].y & 0xffff0000u)};
+#pragma unroll
+      for (int y = 0; y < 4; ++y) v[y] = fabsf(v[y]) <= FLT_MAX ? v[y] * by : NAN;
+      q[s][x] = pack_f16x2(v[0], v[1]);
+      q[s][x + 2] = pack_f16x2(v[2], v[3]);
     }
     return __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * p.scale_log2;
   }
@@ -563,7 +567,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) fa_tree_fp8_merge_kernel(con
   constexpr int kCols = D / 32;
   __shared__ float sh_m[kMergeWarps], sh_l[kMergeWarps], sh_o[kMergeWarps][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int unit_rows = p.G * p.Nt, rows = 16 * p.row_tiles;
+  const int unit_rows = p.G * p.Nt, rows = p.rows;
   const int r = blockIdx.x % unit_rows, x = blockIdx.x / unit_rows;
   cudaGridDependencySynchronize();  // (launched while the main kernel still runs)
   const int4 cut = p.cuts[x];
@@ -613,16 +617,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) fa_tree_fp8_merge_kernel(con
     p.lse[(static_cast<long long>(b) * p.H + h) * p.Nt + node] = any ? (M + log2f(sum)) * kLn2 : -INFINITY;
 }
 
-template <int D, int RT>
-cudaError_t launch_tree8_t(const CUtensorMap &tk, const CUtensorMap &tv, const Tree8Params &p, bool merge,
-                           cudaStream_t stream) {
-  using L = Layout8<D>;
-  auto kern = fa_tree_fp8_kernel<D, RT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kRequest);
-  if (e != cudaSuccess) return e;
-  kern<<<static_cast<unsigned>(p.ranges) * p.groups, kThreads, L::kRequest, stream>>>(tk, tv, p);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || !merge) return e;
+template <int D>
+cudaError_t launch_merge8(const Tree8Params &p, cudaStream_t stream) {
   const long long cuts = p.cuts_by_unit ? static_cast<long long>(p.B) * p.Hkv : p.ranges;  // at most 152
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(cuts * p.G * p.Nt));
@@ -636,15 +632,14 @@ cudaError_t launch_tree8_t(const CUtensorMap &tk, const CUtensorMap &tv, const T
   return cudaLaunchKernelEx(&cfg, fa_tree_fp8_merge_kernel<D>, p);
 }
 
-template <int D>
-cudaError_t launch_tree8_d(const CUtensorMap &tk, const CUtensorMap &tv, const Tree8Params &p, bool merge,
-                           cudaStream_t stream) {
-  switch (p.row_tiles) {
-    case 1: return launch_tree8_t<D, 1>(tk, tv, p, merge, stream);
-    case 2: return launch_tree8_t<D, 2>(tk, tv, p, merge, stream);
-    case 4: return launch_tree8_t<D, 4>(tk, tv, p, merge, stream);
-    default: return launch_tree8_t<D, 8>(tk, tv, p, merge, stream);
-  }
+template <int D, int RT>
+cudaError_t launch_rows(const CUtensorMap &tk, const CUtensorMap &tv, const Tree8Params &p, cudaStream_t stream) {
+  using L = Layout8<D>;
+  auto kern = fa_tree_fp8_kernel<D, RT>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kRequest);
+  if (e != cudaSuccess) return e;
+  kern<<<static_cast<unsigned>(p.ranges) * p.groups, kThreads, L::kRequest, stream>>>(tk, tv, p);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -652,11 +647,12 @@ cudaError_t launch_tree8_d(const CUtensorMap &tk, const CUtensorMap &tv, const T
 // Short caches are not cut inside a unit: see plan_tree.
 constexpr int kWholeTiles = 8;
 
-Tree8Plan plan_tree8(int B, int H, int Hkv, int Nt, int Nk) {
+Tree8Plan plan_tree8(int B, int H, int Hkv, int Nt, int Nk, int d) {
   Tree8Plan pl{};
-  const int rows = H / Hkv * Nt;  // (below 2^31: H < 2^24, Nt <= 128)
-  pl.row_tiles = rows <= 16 ? 1 : (rows <= 32 ? 2 : (rows <= 64 ? 4 : 8));
-  pl.groups = (rows + 16 * pl.row_tiles - 1) / (16 * pl.row_tiles);
+  const int rows = H / Hkv * Nt, most = d == 128 ? 64 : 128;  // (rows below 2^31: H < 2^24, Nt <= 128)
+  pl.rows = 16;
+  while (pl.rows < rows && pl.rows < most) pl.rows *= 2;
+  pl.groups = (rows + pl.rows - 1) / pl.rows;
   const int per_unit = (Nk + kKeys - 1) / kKeys;
   const long long units = static_cast<long long>(B) * Hkv;
   pl.whole = per_unit <= kWholeTiles ? 1 : 0;
@@ -666,13 +662,25 @@ Tree8Plan plan_tree8(int B, int H, int Hkv, int Nt, int Nk) {
   if (ranges > pieces) ranges = pieces;
   pl.ranges = static_cast<int>(ranges);
   pl.merge = ranges > 1 && !pl.whole;
-  pl.part_rows = pl.merge ? static_cast<size_t>(ranges) * pl.groups * 2 * 16 * pl.row_tiles : 0;
+  pl.part_rows = pl.merge ? static_cast<size_t>(ranges) * pl.groups * 2 * pl.rows : 0;
   return pl;
 }
 
 cudaError_t launch_tree8(const CUtensorMap &tk, const CUtensorMap &tv, const Tree8Params &p, bool merge,
                          cudaStream_t stream) {
-  return p.d == 64 ? launch_tree8_d<64>(tk, tv, p, merge, stream) : launch_tree8_d<128>(tk, tv, p, merge, stream);
+  cudaError_t e;
+  if (p.d == 128) {
+    e = launch_tree8_tc(tk, tv, p, stream);
+  } else {
+    switch (p.rows) {
+      case 16: e = launch_rows<64, 1>(tk, tv, p, stream); break;
+      case 32: e = launch_rows<64, 2>(tk, tv, p, stream); break;
+      case 64: e = launch_rows<64, 4>(tk, tv, p, stream); break;
+      default: e = launch_rows<64, 8>(tk, tv, p, stream); break;
+    }
+  }
+  if (e != cudaSuccess || !merge) return e;
+  return p.d == 128 ? launch_merge8<128>(p, stream) : launch_merge8<64>(p, stream);
 }
 
 }  // namespace fa

@@ -1,16 +1,25 @@
 """Attention over a cache held in 8 bits (fa_fwd_tree_fp8) against the 64-bit
 attention of the values that its codes stand for.
 
-Bounds.  A score is a sum of d products, exact in fp32, added in fp32 in an order
-of the hardware's: off by at most d * 2^-23 of scale * sum |q k| (A below; each of
-the d additions by at most 2^-23 of the running sum of magnitudes, truncation
-included), then a few 2^-24 of itself, which A exceeds too: e = (d + 8) 2^-23 A.
-Every weight is off by e and by the exponential's 2^-22, and by its rounding to f16,
-2^-11, or 2^-31 of its row's greatest (V's scales relative to each other times that:
-at most 2^16 in these tests, on weights below 2^-20 of the greatest, so below 2^-15
-of the greatest product and covered by 2^-11 of sum P|v|).  O, a quotient of two
-such sums, is off by twice that of sum P|v|, and is rounded to bf16, 2^-8 of it.  The
-logsumexp takes unrounded weights: e and 2^-20 (of its sum and its logarithm).
+Bounds.  q enters as the sum of two e4m3 parts of a row scaled to at most 448 and more
+than 224, off by at most 2^-10 there (the second part's least half step; bf16's
+8 bits are otherwise 4 + 4), 2^-17.8 of the row's greatest value: a score is off by
+that times scale * sum |k|.  It is a sum of 2 d products, exact in fp32, added in fp32 in
+an order of the hardware's: off by at most 2 d * 2^-23 of scale * sum |q k| (A below;
+each addition by at most 2^-23 of the running sum of magnitudes, truncation
+included), then a few 2^-24 of itself, which A exceeds too: e is the sum of both.
+Every weight is off by e and by the exponential's 2^-22, then by its rounding.  d = 64: to
+f16, 2^-11, or 2^-31 of its row's greatest (V's scales relative to each other times that:
+at most 2^16 in these tests, on weights below 2^-20 of the greatest, so below 2^-15 of the
+greatest product and covered by a second 2^-11 of sum P|v|).  d = 128: to f16, 2^-11, and
+to two e4m3 parts: the first leaves at most half a step, 2^(a - 4) of a weight in
+[2^a, 2^(a + 1)), and the second at most a sixteenth of a power of two below that, 2^(a - 9),
+or 2^-10 where it falls below e4m3's normal range: 2^-9 of the weight, or 2^-10 with the
+tile's greatest product of a weight and its value's scale at 2^8, so 2^-18 of that times
+sum |codes| of the tile (F below).  O, a quotient of two sums with errors of e and 2^-22 of
+their terms, is off by twice those of sum P|v| and by the roundings; then it is rounded
+to bf16, 2^-8 of it.  The logsumexp takes unrounded weights: e and 2^-20 (of its sum and
+its logarithm).
 """
 import math
 
@@ -25,18 +34,38 @@ from exact_attention_48_gb300 import (FaError, fa_device_status, fa_fwd_tree, fa
 pytestmark = pytest.mark.gpu
 
 
-def check(o, lse, q, kv, vv, parents, n, Nt, scale, what):
-    """One (b, hk): q [G, Nt, d], values kv, vv [Nk, d]; parents a list or None."""
+def floor_of(q, kv, mask, lse, scale, vcodes, vs, block):
+    """F: 2^-18 of each 128-row tile's greatest P vs, times its sum of |codes|."""
+    Nk = kv.shape[0]
+    s = vs.double().repeat_interleave(block)[:Nk]
+    on = mask.to(q.device)
+    t = q.double() @ torch.where(on.any(0)[:, None], kv, torch.zeros_like(kv)).T * scale
+    p = torch.where(on, (t - lse[:, None].clamp(min=-1e30)).exp() * s.nan_to_num(), torch.zeros_like(t))
+    c = torch.where(on.any(0)[:, None], vcodes.double().abs().nan_to_num(), torch.zeros_like(kv))
+    pad = -Nk % 128
+    p = torch.nn.functional.pad(p, (0, pad)).view(p.shape[0], -1, 128).amax(-1)
+    c = torch.nn.functional.pad(c, (0, 0, 0, pad)).view(-1, 128, c.shape[1]).sum(1)
+    return 2.0 ** -18 * p @ c
+
+
+def check(o, lse, q, kv, vv, parents, n, Nt, scale, what, v8):
+    """One (b, hk): q [G, Nt, d], values kv, vv [Nk, d]; parents a list or None; v8: V's codes, scales and block."""
     Nk, d = kv.shape
     par = list(range(-1, Nt - 1)) if parents is None else parents
     mask = ref.tree_mask(par, n, Nt, Nk)
     on = mask.any(1).to(q.device)
     for h in range(q.shape[0]):
         wo, wl, pv, A = r8.attention(q[h], kv, vv, mask, scale)
-        e = (d + 8) * 2.0 ** -23 * A
+        e = (2 * d + 8) * 2.0 ** -23 * A
+        e += 2.0 ** -17.8 * float(q[h].abs().max()) * float(kv[mask.any(0).to(kv.device)].abs().sum(-1).max().nan_to_num()
+                                                            if bool(mask.any()) else 0.0) * abs(scale)
         assert bool((lse[h][~on] == -math.inf).all()) and bool((o[h][~on] == 0).all()), what
         err = (o[h].double() - wo).abs()[on]
-        tol = 2.0 ** -8 * wo.abs()[on] + 2 * (2 * e + 2.0 ** -11 + 2.0 ** -22) * pv[on] + 1e-30
+        if d == 64:
+            tol = 2 * (2 * e + 2.0 ** -11 + 2.0 ** -22) * pv[on]
+        else:
+            tol = (4 * e + 2.0 ** -21 + 2.0 ** -11 + 2.0 ** -9) * pv[on] + floor_of(q[h], kv, mask, wl, scale, *v8)[on]
+        tol += 2.0 ** -8 * wo.abs()[on] + 1e-30
         assert bool((err <= tol).all()), f"{what} head {h}: {float(err.max()):.3e}, {float((err / tol).max()):.2f} of the bound"
         err = (lse[h].double() - wl).abs()[on]
         assert bool((err <= e + 2.0 ** -20 * (1 + wl[on].abs())).all()), f"{what} head {h}: lse {float(err.max()):.3e}"
@@ -63,7 +92,7 @@ def run(g, B, H, Hkv, Nt, Nk, d, block, layout="bhnd", lens=None, parents=None, 
                 continue
             par = None if parents is None else parents[b].tolist() if parents.dim() == 2 else parents.tolist()
             check(o[b, hk * G:hk * G + G], lse[b, hk * G:hk * G + G], q[b, hk * G:hk * G + G], kv[b, hk], vv[b, hk], par,
-                  Nk if lens is None else lens[b], Nt, s, f"b{b} hk{hk}")
+                  Nk if lens is None else lens[b], Nt, s, f"b{b} hk{hk}", (v[b, hk], vs[b, hk], block))
     return o, lse
 
 
