@@ -29,11 +29,13 @@
 // a row and warp.  More rows come in groups of 64, a CTA each, whose tiles mostly
 // come from L2.
 //
-// CTA (512 threads): warps 0..3 and 4..7 softmax, a key per thread, alternate tiles;
-// warps 8..11 add up O^T, a column of V per thread; warp 12 TMA producer, warp 13
-// MMA issuer and TMEM owner, warp 14 the tree's table, warp 15 q's parts.  TMEM: two
-// S^T and two O^T of 2 C columns.  The tiles of all units form one list that is cut
-// into equal runs (fa_runs.cuh), and a CTA's products run on from unit to unit.
+// CTA: two to four warpgroups of softmax, a key per thread, which take the tiles in
+// turn; one that adds up O^T, a column of V per thread; then the TMA producer (and the
+// tiles' scales), a warp that issues S^T and owns TMEM, one that issues O^T (one thread
+// for both took 1950 cycles a tile, most of them in the instructions themselves), and
+// one for q's parts and the tree's table.  TMEM: four S^T and four O^T of 2 C columns (two
+// each for 64 rows).  The tiles of all units form one list that is cut into equal runs
+// (fa_runs.cuh), and a CTA's products run on from unit to unit.
 
 #include <cfloat>
 #include <cstdint>
@@ -47,48 +49,85 @@ namespace fa {
 namespace {
 
 constexpr int kD = 128;
-constexpr int kThreads = 512;
-constexpr int kWarpAdd = 8, kWarpProducer = 12, kWarpMma = 13, kWarpMask = 14, kWarpQ = 15;
 constexpr float kMoveBy = 8.0f;   // a running maximum moves only when exceeded by more (log2 units)
 constexpr float kLift = 8.0f;     // weights reach 2^kLift
 constexpr float kLn2 = 0.69314718055994530942f;
-// Register split: 512 threads launched with 128 each.
-constexpr uint32_t kRegsSoftmax = 160, kRegsControl = 64;  // (the sums' warps keep their 128)
-static_assert(256 * kRegsSoftmax + 128 * 128 + 128 * kRegsControl <= kThreads * 128, "register split");
+// The CTA's warps: kGroups warpgroups of softmax, then one that adds up O^T, then the
+// control warps.  A softmax warpgroup takes some 3000 cycles a tile, most of them
+// latency, so there are as many as the registers hold.  Registers: launched with
+// kLaunch a thread, split by setmaxnreg.
+template <int C>
+struct Roles;
+template <>
+struct Roles<16> {
+  static constexpr int kGroups = 4;
+  static constexpr uint32_t kLaunch = 80, kSoftmax = 88, kAdd = 72, kControl = 56;
+};
+template <>
+struct Roles<32> {
+  static constexpr int kGroups = 3;
+  static constexpr uint32_t kLaunch = 96, kSoftmax = 112, kAdd = 96, kControl = 48;
+};
+template <>
+struct Roles<64> {
+  static constexpr int kGroups = 2;
+  static constexpr uint32_t kLaunch = 128, kSoftmax = 160, kAdd = 128, kControl = 64;
+};
 
 template <int C>
 struct LayoutTc {
+  using R = Roles<C>;
+  static constexpr int kGroups = R::kGroups, kSoftmaxWarps = 4 * kGroups;
+  static constexpr int kThreads = 128 * (kGroups + 2);
+  static_assert(128 * (kGroups * R::kSoftmax + R::kAdd + R::kControl) <= kThreads * R::kLaunch, "register split");
+  static constexpr int kWarpAdd = kSoftmaxWarps, kWarpProducer = kWarpAdd + 4, kWarpS = kWarpProducer + 1;
+  static constexpr int kWarpO = kWarpProducer + 2, kWarpQ = kWarpProducer + 3;
   static constexpr uint32_t kTile = kKeys * kD;        // a K or V tile, 16 KB
-  static constexpr int kSlots = 10;
-  static constexpr uint32_t kTmem = 8 * C <= 512 ? 8 * C : 512;  // S^T, S^T, O^T, O^T
-  static constexpr uint32_t kQ = 2 * C * kD;           // q's parts
+  // Slots of K and of V.  V tiles are asked for kLag tiles after their K: S^T runs about so far ahead of O^T, and a V
+  // tile that came with its K would hold its slot meanwhile.
+  static constexpr int kSlotsK = 4, kSlotsV = 5, kLag = C == 64 ? 2 : 3;
+  static constexpr int kBufs = C == 64 ? 2 : 4;        // of S^T, and of O^T
+  static constexpr uint32_t kTmem = 2 * kBufs * 2 * C;
+  static_assert(kTmem <= 512, "TMEM columns");
+  // How many of what one role leaves to another are used in turn.
+  // A tile's maxima: tile x + 2 kGroups' are written by a warpgroup that saw tile x's sums done at its tile before.
+  static constexpr int kTiles = kGroups == 2 ? 4 : 8;
+  static_assert(kTiles >= 2 * kGroups, "tile x's maxima have been read by then");
+  // A segment's row factors: segment n + NB + 3's are written when S^T of segment n + NB + 1 is done, so that of a tile
+  // beyond x + NB, x any of segment n's, and that takes tile x's scores read.
+  static constexpr int kSegs = kBufs == 2 ? 5 : 8;
+  static_assert(kSegs >= kBufs + 3, "segment n's factors have been read by then");
+  static constexpr uint32_t kQ = 2 * C * kD;           // q's parts (two segments' in turn)
   // first the small things, then (1 KB aligned) ring, P, q
   static constexpr uint32_t kOffBits = 0;
   static constexpr uint32_t kOffDead = kOffBits + 32 * (1 + 2 + 3 + 4) * 4;
   static constexpr uint32_t kOffJump = kOffDead + 16;
   static constexpr uint32_t kOffRange = kOffJump + 128;
-  static constexpr uint32_t kOffScan = kOffRange + 48;                    // 16 warps' sums
-  static constexpr uint32_t kOffMost = kOffScan + 16 * 8;                 // [8 warps][C] greatest e
-  static constexpr uint32_t kOffBase = kOffMost + 8 * C * 4;              // [8 warps][2][C]: 8 - m, l's factor
-  static constexpr uint32_t kOffMove = kOffBase + 8 * 2 * C * 4;          // [8 warps][C]: l's rescale
-  static constexpr uint32_t kOffTileM = kOffMove + 8 * C * 4;             // [4 tiles][C] m, for the sums' warps
-  static constexpr uint32_t kOffTileV = kOffTileM + 4 * C * 4;            // [4 tiles] vs_max
-  static constexpr uint32_t kOffAdd = kOffTileV + 16;                     // [4 warps][2][C]: factors of O
-  static constexpr uint32_t kOffL = kOffAdd + 4 * 2 * C * 4;              // [8 warps][C] l, and [2][C] its base
-  static constexpr uint32_t kOffLm = kOffL + 8 * C * 4;
-  static constexpr uint32_t kOffRow = kOffLm + 2 * C * 4;                 // [4 segments][C] rows' factors
-  static constexpr uint32_t kOffBar = kOffRow + 4 * C * 4;
-  // full[S], empty[S], s_full[2], p_ready[2], pv_done[2], o_empty[2], q_full, q_empty, mask_full, mask_empty, l_full,
-  // l_empty, drain
-  static constexpr int kNumBars = 2 * kSlots + 8 + 7;
+  static constexpr uint32_t kOffScan = kOffRange + 48;                    // warps' sums
+  static constexpr uint32_t kOffMost = kOffScan + 24 * 8;                 // [softmax warps][C] greatest e
+  static constexpr uint32_t kOffBase = kOffMost + kSoftmaxWarps * C * 4;  // [softmax warps][2][C]: 8 - m, l's factor
+  static constexpr uint32_t kOffTileM = kOffBase + kSoftmaxWarps * 2 * C * 4;  // [kTiles][C] m and the greatest vs
+  static constexpr uint32_t kOffAdd = kOffTileM + kTiles * (C + 4) * 4;   // [4 warps][C]: factors of O
+  static constexpr uint32_t kOffL = kOffAdd + 4 * C * 4;                  // [softmax warps][C] l, and [groups][C] its base
+  static constexpr uint32_t kOffLm = kOffL + kSoftmaxWarps * C * 4;
+  static constexpr uint32_t kOffRow = kOffLm + kGroups * C * 4;           // [kSegs][C] rows' factors
+  static constexpr uint32_t kOffBar = kOffRow + kSegs * C * 4;
+  // k_full[], k_empty[], v_full[], v_empty[], s_full[bufs], s_free[bufs], pv_done[bufs], o_empty[bufs], p_ready[groups], q_full[2], q_empty[2],
+  // mask_full, mask_empty, l_full, l_empty, drain[2]
+  static constexpr int kNumBars = 2 * (kSlotsK + kSlotsV) + 4 * kBufs + kGroups + 10;
   static constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;            // TMEM address, abort flag
   static constexpr uint32_t kSmall = (kOffMisc + 16 + 15) / 16 * 16;
-  static constexpr uint32_t kRing = kSlots * kTile, kP = 2 * kTile;
-  static constexpr uint32_t kRequest = kSmall + 1008 + kRing + kP + kQ;
+  static constexpr uint32_t kRing = (kSlotsK + kSlotsV) * kTile, kP = kGroups * kTile;
+  static constexpr uint32_t kRequest = kSmall + 1008 + kRing + kP + 2 * kQ;
   static_assert(kOffBar % 8 == 0 && kOffRange % 8 == 0 && kOffScan % 8 == 0 && kOffMost % 16 == 0, "alignment");
   static_assert(kRequest <= 232448, "shared memory budget");
 };
 
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&v);
@@ -120,17 +159,18 @@ __device__ __forceinline__ void parts_of(uint32_t a, uint32_t b, uint32_t *hi, u
       : "r"(a), "r"(b));
 }
 
-// 32 lanes x N consecutive columns.
-template <int N>
-__device__ __forceinline__ void tmem_load(uint32_t addr, float (&r)[N]) {
-  static_assert(N % 16 == 0, "columns");
-#pragma unroll
-  for (int c = 0; c < N; c += 16) {
-    uint32_t w[16];
-    tmem_ld16(addr + c, w);
-#pragma unroll
-    for (int x = 0; x < 16; ++x) r[c + x] = __uint_as_float(w[x]);
-  }
+// 32 lanes x 16 or 32 columns from each of two places.
+__device__ __forceinline__ void tmem_pair(uint32_t a, uint32_t b, uint32_t (&x)[16], uint32_t (&y)[16]) {
+  tmem_ld16(a, x);
+  tmem_ld16(b, y);
+  tmem_ld_wait16(x);
+  tmem_ld_wait16(y);
+}
+__device__ __forceinline__ void tmem_pair(uint32_t a, uint32_t b, uint32_t (&x)[32], uint32_t (&y)[32]) {
+  tmem_ld32(a, x);
+  tmem_ld32(b, y);
+  tmem_ld_wait(x);
+  tmem_ld_wait(y);
 }
 
 // Sums over the warp's lanes of N values each (N = 16, 32): lane l gets the sum of
@@ -154,37 +194,33 @@ __device__ __forceinline__ float lane_sums(float (&v)[N]) {
   return v[0];
 }
 
-// Whether node i sees the key that is `node` rows from the tree's start.
-__device__ __forceinline__ bool sees(const uint32_t *bits, int i, bool live, int node, int Nt) {
-  if (!live || node >= Nt) return false;
-  if (node < 0) return true;
-  if ((node >> 5) > (i >> 5)) return false;
-  return (bits[bit_row(i) + (node >> 5)] >> (node & 31)) & 1u;
-}
-
 template <int C>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(LayoutTc<C>::kThreads, 1)
     fa_tree_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                           const Tree8Params p) {
   using L = LayoutTc<C>;
-  constexpr int S = L::kSlots;
+  using R = Roles<C>;
+  constexpr int SK = L::kSlotsK, SV = L::kSlotsV, NB = L::kBufs, W = L::kGroups, kLag = L::kLag;
+  constexpr int kWarpAdd = L::kWarpAdd, kWarpProducer = L::kWarpProducer, kWarpS = L::kWarpS, kWarpO = L::kWarpO;
   constexpr int kLanes = C < 32 ? C : 32, kPerLane = C / kLanes;  // columns that lanes look after
   extern __shared__ uint8_t smem_raw[];
   uint8_t *small = smem_raw;
   uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + L::kSmall + 1023) &
                                               ~uintptr_t(1023));
-  uint8_t *sP = ring + L::kRing, *sQ = sP + L::kP;
+  uint8_t *ring_v = ring + SK * L::kTile, *sP = ring + L::kRing, *sQ = sP + L::kP;
   uint32_t *bits = reinterpret_cast<uint32_t *>(small + L::kOffBits);
   uint32_t *dead = reinterpret_cast<uint32_t *>(small + L::kOffDead);
   RunStart *run = reinterpret_cast<RunStart *>(small + L::kOffRange);
   auto floats = [&](uint32_t off) { return reinterpret_cast<float *>(small + off); };
-  float *tile_m = floats(L::kOffTileM), *tile_v = floats(L::kOffTileV), *row_f = floats(L::kOffRow);
+  float *tile_m = floats(L::kOffTileM), *row_f = floats(L::kOffRow);
   float *sum_l = floats(L::kOffL), *sum_m = floats(L::kOffLm);
-  uint64_t *full = reinterpret_cast<uint64_t *>(small + L::kOffBar);
-  uint64_t *empty = full + S;
-  // Tile x of the run uses s_full, p_ready, pv_done and o_empty number x & 1.
-  uint64_t *s_full = empty + S, *p_ready = s_full + 2, *pv_done = p_ready + 2, *o_empty = pv_done + 2;
-  uint64_t *q_full = o_empty + 2, *q_empty = q_full + 1, *mask_full = q_empty + 1, *mask_empty = mask_full + 1;
+  uint64_t *k_full = reinterpret_cast<uint64_t *>(small + L::kOffBar), *k_empty = k_full + SK;
+  uint64_t *v_full = k_empty + SK, *v_empty = v_full + SV;
+  // Tile x of the run uses number x % NB of the buffers' barriers and p_ready number x % W.  No wait can find its
+  // barrier two phases on: tile x + NB's product waits for what tile x's readers arrive on.
+  uint64_t *s_full = v_empty + SV, *s_free = s_full + NB, *pv_done = s_free + NB, *o_empty = pv_done + NB;
+  uint64_t *p_ready = o_empty + NB;
+  uint64_t *q_full = p_ready + W, *q_empty = q_full + 2, *mask_full = q_empty + 2, *mask_empty = mask_full + 1;
   uint64_t *l_full = mask_empty + 1, *l_empty = l_full + 1, *drain = l_empty + 1;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(small + L::kOffMisc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(small + L::kOffMisc + 4);
@@ -195,27 +231,35 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int first_row = group * C, unit_rows = p.G * p.Nt;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < S; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+    for (int i = 0; i < SK; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < SV; ++i) {
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_empty[i], 1);
+    }
+    for (int i = 0; i < NB; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_ready[i], 4);
+      mbar_init(&s_free[i], 4);
       mbar_init(&pv_done[i], 1);
       mbar_init(&o_empty[i], 4);
     }
-    mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
+    for (int i = 0; i < W; ++i) mbar_init(&p_ready[i], 4);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 1);
+    }
     mbar_init(mask_full, 1);
-    mbar_init(mask_empty, 12);
-    mbar_init(l_full, 8);
+    mbar_init(mask_empty, L::kSoftmaxWarps + 4);
+    mbar_init(l_full, L::kSoftmaxWarps);
     mbar_init(l_empty, 4);
-    mbar_init(drain, 1);
+    mbar_init(&drain[0], 1);
+    mbar_init(&drain[1], 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == kWarpMma) {
+  if (warp == kWarpS) {
     tmem_alloc(tmem_slot, L::kTmem);
     tmem_relinquish();
   }
@@ -224,105 +268,140 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tm_v);
   }
   tc_fence_before();
-  const bool has_run = find_run<kThreads>(p, c, run, reinterpret_cast<long long *>(small + L::kOffScan));
+  const bool has_run = find_run<L::kThreads>(p, c, run, reinterpret_cast<long long *>(small + L::kOffScan));
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   if (p.cuts && !p.cuts_by_unit && group == 0 && threadIdx.x == 0) p.cuts[c] = make_int4(-1, 0, 0, 0);
   if (!has_run) {
-    if (warp == kWarpMma) tmem_dealloc(tmem, L::kTmem);
+    if (warp == kWarpS) tmem_dealloc(tmem, L::kTmem);
     return;
   }
   Walk<Tree8Params> wk(p, *run);
   const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
 
   if (warp >= kWarpProducer) {
-    regs_decrease<kRegsControl>();
+    regs_decrease<R::kControl>();
     if (warp == kWarpProducer && lane == 0) {
       // ---------------------------------------------------------- producer
-      uint32_t e = 0;
-      bool ok = true;
-      auto load = [&](const CUtensorMap *map, int row) -> bool {
-        const uint32_t sl = e % S;
-        if (!mbar_wait(&empty[sl], ((e / S) & 1) ^ 1, ctl, kSiteKvEmpty)) return false;
-#ifdef FA_TEST_SKIP_FIRST_V_LOAD
-        // Test builds only: the run's first V tile is never loaded, so the wait
-        // for it runs out and the bounded-wait path is taken.
-        if (e == 1) {
-          ++e;
-          return true;
-        }
-#endif
-        mbar_arrive_expect_tx(&full[sl], L::kTile);
-        tma_load_4d(ring + sl * L::kTile, map, &full[sl], 0, row, wk.hk, wk.b);
-        ++e;
-        return true;
-      };
-      while (ok && wk.next())
-        for (int j = wk.k0; ok && j < wk.k1; ++j) ok = load(&tm_k, j * kKeys) && load(&tm_v, j * kKeys);
-      // every copy issued lands before this thread leaves (bounded waits)
-      for (uint32_t i = e > S ? e - S : 0; i < e; ++i) mbar_drain(&full[i % S], (i / S) & 1);
-    } else if (warp == kWarpMma && lane == 0) {
-      // ---------------------------------------------------------- MMA issuer
-      constexpr uint32_t kIdS = idesc_e4m3(kKeys, 2 * C, false, false);
-      constexpr uint32_t kIdO = idesc_e4m3(kD, 2 * C, true, true);
-      const uint64_t dQ = sdesc_sw128(smem_addr(sQ), 16, 1024), dT = sdesc_sw128(smem_addr(ring), 16, 1024);
-      const uint64_t dP = sdesc_sw128(smem_addr(sP), 16, 1024);
       const uint32_t total = static_cast<uint32_t>(wk.end - wk.t);
-      uint32_t left = 0, seg = 0;  // tiles of the segment that S is to be formed of, segments begun
+      uint32_t ks = 0, kph = 1, vs = 0, vph = 1;  // the next slots and their phases
+      uint32_t nk = 0, nv = 0;                    // tiles asked for
+      int left = 0, row = 0;
+      int4 ahead[kLag];                           // where the K tiles whose V is still to come lie
       bool ok = true;
-      for (uint32_t i = 0; ok && i < total + 2; ++i) {
-        if (i >= 2) {
-          // O^T = V^T P^T of tile i - 2
-          const uint32_t y = i - 2, buf = y & 1, ph = (y >> 1) & 1, sl = (2 * y + 1) % S;
-          if (!(ok = mbar_wait(&p_ready[buf], ph, ctl, kSitePReady) &&
-                     mbar_wait(&full[sl], ((2 * y + 1) / S) & 1, ctl, kSiteVFull) &&
-                     mbar_wait(&o_empty[buf], ph ^ 1, ctl, kSiteSFree)))
-            break;
-          tc_fence_after();
-          const uint64_t dv = desc_add(dT, sl * L::kTile), dp = desc_add(dP, buf * L::kTile);
 #pragma unroll
-          for (int kk = 0; kk < kKeys / 32; ++kk)
-            mma_ss_f8(tmem + (2 + buf) * 2 * C, desc_add(dv, kk * 4096), desc_add(dp, kk * 4096), kIdO, kk > 0 ? 1u : 0u);
-          tc_commit(&pv_done[buf]);
-          tc_commit(&empty[sl]);
-        }
-        if (i < total) {
-          // S^T = K Q^T of tile i (its buffer was read before tile i - 2's weights were ready)
+      for (int i = 0; i < kLag; ++i) ahead[i] = make_int4(0, 0, 0, 0);
+      for (uint32_t y = 0; ok && y < total + kLag; ++y) {
+        const int4 v = ahead[0];
+#pragma unroll
+        for (int i = 0; i + 1 < kLag; ++i) ahead[i] = ahead[i + 1];
+        if (y < total) {
           if (left == 0) {
             wk.next();
             left = wk.k1 - wk.k0;
-            if (!(ok = mbar_wait(q_full, seg & 1, ctl, kSiteQFull))) break;
-            ++seg;
+            row = wk.k0 * kKeys;
           }
-          const uint32_t sl = (2 * i) % S;
-          if (!(ok = mbar_wait(&full[sl], ((2 * i) / S) & 1, ctl, kSiteKFull))) break;
+          if (!(ok = mbar_wait(&k_empty[ks], kph, ctl, kSiteKEmpty))) break;
+          mbar_arrive_expect_tx(&k_full[ks], L::kTile);
+          tma_load_4d(ring + ks * L::kTile, &tm_k, &k_full[ks], 0, row, wk.hk, wk.b);
+          ++nk;
+          if (++ks == SK) {
+            ks = 0;
+            kph ^= 1;
+          }
+          ahead[kLag - 1] = make_int4(row, wk.hk, wk.b, 0);
+          row += kKeys;
+          --left;
+        }
+        if (y >= kLag) {
+          if (!(ok = mbar_wait(&v_empty[vs], vph, ctl, kSiteVEmpty))) break;
+#ifdef FA_TEST_SKIP_FIRST_V_LOAD
+          // Test builds only: the run's first V tile is never loaded, so the wait
+          // for it runs out and the bounded-wait path is taken.
+          if (y > kLag)
+#endif
+          {
+            mbar_arrive_expect_tx(&v_full[vs], L::kTile);
+            tma_load_4d(ring_v + vs * L::kTile, &tm_v, &v_full[vs], 0, v.x, v.y, v.z);
+          }
+          ++nv;
+          if (++vs == SV) {
+            vs = 0;
+            vph ^= 1;
+          }
+        }
+      }
+      // every copy issued lands before this thread leaves (bounded waits)
+      for (uint32_t i = nk > SK ? nk - SK : 0; i < nk; ++i) mbar_drain(&k_full[i % SK], (i / SK) & 1);
+      for (uint32_t i = nv > SV ? nv - SV : 0; i < nv; ++i) mbar_drain(&v_full[i % SV], (i / SV) & 1);
+    } else if (warp == kWarpS && lane == 0) {
+      // ---------------------------------------------------------- S^T = K Q^T
+      constexpr uint32_t kIdS = idesc_e4m3(kKeys, 2 * C, false, false);
+      const uint64_t dQ = sdesc_sw128(smem_addr(sQ), 16, 1024), dT = sdesc_sw128(smem_addr(ring), 16, 1024);
+      uint32_t i = 0, seg = 0, sl = 0, sph = 0, bph = 1;  // tile, segment, K's slot and its phase, the buffer's
+      bool ok = true;
+      while (ok && wk.next()) {
+        const uint32_t qb = seg & 1;
+        if (!(ok = mbar_wait(&q_full[qb], (seg >> 1) & 1, ctl, kSiteQFull))) break;
+        ++seg;
+        const uint64_t dq = desc_add(dQ, qb * L::kQ);
+        for (int j = wk.k0; j < wk.k1; ++j, ++i) {
+          const uint32_t buf = i % NB;
+          if (!(ok = mbar_wait(&s_free[buf], bph, ctl, kSiteSFree) && mbar_wait(&k_full[sl], sph, ctl, kSiteKFull))) break;
           tc_fence_after();
           const uint64_t dk = desc_add(dT, sl * L::kTile);
 #pragma unroll
           for (int kk = 0; kk < kD / 32; ++kk)
-            mma_ss_f8(tmem + (i & 1) * 2 * C, desc_add(dk, kk * 32), desc_add(dQ, kk * 32), kIdS, kk > 0 ? 1u : 0u);
-          tc_commit(&s_full[i & 1]);
-          tc_commit(&empty[sl]);
-          if (--left == 0) tc_commit(q_empty);
+            mma_ss_f8(tmem + buf * 2 * C, desc_add(dk, kk * 32), desc_add(dq, kk * 32), kIdS, kk > 0 ? 1u : 0u);
+          tc_commit(&s_full[buf]);
+          tc_commit(&k_empty[sl]);
+          if (++sl == SK) {
+            sl = 0;
+            sph ^= 1;
+          }
+          if (buf == NB - 1) bph ^= 1;
+        }
+        tc_commit(&q_empty[qb]);
+      }
+      tc_commit(&drain[0]);
+      mbar_drain(&drain[0], 0);
+    } else if (warp == kWarpO && lane == 0) {
+      // ---------------------------------------------------------- O^T = V^T P^T
+      constexpr uint32_t kIdO = idesc_e4m3(kD, 2 * C, true, true);
+      const uint64_t dT = sdesc_sw128(smem_addr(ring_v), 16, 1024), dP = sdesc_sw128(smem_addr(sP), 16, 1024);
+      const uint32_t total = static_cast<uint32_t>(wk.end - wk.t);
+      uint32_t sl = 0, sph = 0, bph = 1;  // V's slot and its phase, the buffer's
+      uint32_t wg = 0, wph = 0;           // the warpgroup and its weights' phase
+      for (uint32_t y = 0; y < total; ++y) {
+        const uint32_t buf = y % NB;
+        if (!(mbar_wait(&v_full[sl], sph, ctl, kSiteVFull) && mbar_wait(&o_empty[buf], bph, ctl, kSiteDqEmpty) &&
+              mbar_wait(&p_ready[wg], wph, ctl, kSitePReady)))
+          break;
+        tc_fence_after();
+        const uint64_t dv = desc_add(dT, sl * L::kTile), dp = desc_add(dP, wg * L::kTile);
+#pragma unroll
+        for (int kk = 0; kk < kKeys / 32; ++kk)
+          mma_ss_f8(tmem + (NB + buf) * 2 * C, desc_add(dv, kk * 4096), desc_add(dp, kk * 4096), kIdO, kk > 0 ? 1u : 0u);
+        tc_commit(&pv_done[buf]);
+        tc_commit(&v_empty[sl]);
+        if (++sl == SV) {
+          sl = 0;
+          sph ^= 1;
+        }
+        if (buf == NB - 1) bph ^= 1;
+        if (++wg == W) {
+          wg = 0;
+          wph ^= 1;
         }
       }
-      tc_commit(drain);
-      mbar_drain(drain, 0);
-    } else if (warp == kWarpMask) {
-      // ---------------------------------------------------------- the tree's table
-      uint32_t n = 0;
+      tc_commit(&drain[1]);
+      mbar_drain(&drain[1], 0);
+    } else if (warp == L::kWarpQ) {
+      // ---------------------------------------------------------- q's parts, eight lanes a row, and the tree's table
+      uint32_t n = 0, nmask = 0;
       while (wk.next()) {
-        if (!wk.masked()) continue;
-        if (!__all_sync(0xffffffffu, mbar_wait(mask_empty, (n & 1) ^ 1, ctl, kSiteMaskEmpty))) break;
-        build_table(p, wk.b, wk.base(), bits, dead, reinterpret_cast<volatile int8_t *>(small + L::kOffJump));
-        warp_arrive(mask_full);
-        ++n;
-      }
-    } else if (warp == kWarpQ) {
-      // ---------------------------------------------------------- q's parts, eight lanes a row
-      uint32_t n = 0;
-      while (wk.next()) {
-        if (!__all_sync(0xffffffffu, mbar_wait(q_empty, (n & 1) ^ 1, ctl, kSiteQEmpty))) break;
+        const uint32_t qb = n & 1;
+        if (!__all_sync(0xffffffffu, mbar_wait(&q_empty[qb], ((n >> 1) & 1) ^ 1, ctl, kSiteQEmpty))) break;
         const float sign = p.scale_log2 < 0.0f ? -1.0f : 1.0f;
 #pragma unroll 2
         for (int r0 = 0; r0 < C; r0 += 4) {
@@ -359,19 +438,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             lo[y] = pack_e4m3x4(v[0] - h0.x, v[1] - h0.y, v[2] - h1.x, v[3] - h1.y);
           }
           const uint32_t at = r * kD + ((x ^ (r & 7)) * 16);
-          *reinterpret_cast<uint4 *>(sQ + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4 *>(sQ + C * kD + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          if (x == 0) row_f[(n & 3) * C + r] = unit * fabsf(p.scale_log2);
+          uint8_t *to = sQ + qb * L::kQ + at;
+          *reinterpret_cast<uint4 *>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4 *>(to + C * kD) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          if (x == 0) row_f[n % L::kSegs * C + r] = unit * fabsf(p.scale_log2);
         }
         fence_proxy_async_smem();
-        warp_arrive(q_full);
+        warp_arrive(&q_full[qb]);
         ++n;
+        if (!wk.masked()) continue;
+        if (!__all_sync(0xffffffffu, mbar_wait(mask_empty, (nmask & 1) ^ 1, ctl, kSiteMaskEmpty))) break;
+        build_table(p, wk.b, wk.base(), bits, dead, reinterpret_cast<volatile int8_t *>(small + L::kOffJump));
+        warp_arrive(mask_full);
+        ++nmask;
       }
     }
   } else if (warp >= kWarpAdd) {
     // ------------------------------------------------------------ O^T added up, a column of V per thread
+    if (R::kAdd > R::kLaunch)
+      regs_increase<R::kAdd>();
+    else
+      regs_decrease<R::kAdd>();
     const int col = (warp & 3) * 32 + lane;
-    float *fac = floats(L::kOffAdd) + (warp - kWarpAdd) * 2 * C;
+    float *fac = floats(L::kOffAdd) + (warp - kWarpAdd) * C;
     uint32_t x = 0, seg = 0, nmask = 0;
     bool ok = true;
     while (wk.next()) {
@@ -385,31 +474,31 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int y = 0; y < kPerLane; ++y) M[y] = -INFINITY;
       for (int kt = wk.k0; ok && kt < wk.k1; ++kt, ++x) {
-        const uint32_t buf = x & 1;
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[buf], (x >> 1) & 1, ctl, kSitePvDone)))) break;
+        const uint32_t buf = x % NB;
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[buf], (x / NB) & 1, ctl, kSitePvDone)))) break;
         tc_fence_after();
         // the factors of the columns that this lane looks after
-        const float vs = tile_v[x & 3];
+        const float *tm = tile_m + x % L::kTiles * (C + 4), vs = tm[C];
         bool move = false;
+        float alpha[kPerLane];
 #pragma unroll
         for (int y = 0; y < kPerLane; ++y) {
           const int r = (lane & (kLanes - 1)) + y * 32;
-          const float m = tile_m[(x & 3) * C + r];
-          float a = 1.0f;
+          const float m = tm[r];
+          alpha[y] = 1.0f;
           if (m > M[y] + kMoveBy) {
-            a = ex2(M[y] - m);  // (0 at first)
+            alpha[y] = ex2(M[y] - m);  // (0 at first)
             M[y] = m;
             move = true;
           }
           fac[r] = m == -INFINITY ? 0.0f : ex2(m - M[y]) * vs;
-          fac[C + r] = a;
         }
         __syncwarp();
         if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
-          for (int r = 0; r < C; ++r) o[r] *= fac[C + r];
+          for (int r = 0; r < C; ++r) o[r] *= __shfl_sync(0xffffffffu, alpha[r / 32], r % 32);
         }
-        const uint32_t at = tmem + (2 + buf) * 2 * C + lane_base;
+        const uint32_t at = tmem + (NB + buf) * 2 * C + lane_base;
 #pragma unroll
         for (int r = 0; r < C; r += 16) {
           uint32_t hi[16], lo[16];
@@ -435,12 +524,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool whole = wk.whole();
       const long long slot = (static_cast<long long>(blockIdx.x) * 2 + (wk.k0 == 0 ? 1 : 0)) * C;
       if (ok) {
+        uint32_t none[kPerLane];  // rows without a result: 0
 #pragma unroll
         for (int y = 0; y < kPerLane; ++y) {
           const int r = (lane & (kLanes - 1)) + y * 32, row = first_row + r;
           float l = 0.0f;
 #pragma unroll
-          for (int w = 0; w < 8; ++w) {
+          for (int w = 0; w < L::kSoftmaxWarps; ++w) {
             const float m = sum_m[(w >> 2) * C + r];
             l += m == -INFINITY ? sum_l[w * C + r] : sum_l[w * C + r] * ex2(m - M[y]);
           }
@@ -448,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool padding = wk.tail && ((dead[node >> 5] >> (node & 31)) & 1u);
           const bool any = l != 0.0f && !padding;
           fac[r] = any ? 1.0f / l : 0.0f;
-          fac[C + r] = any ? 1.0f : 0.0f;
+          none[y] = any ? 0u : 1u;
           if (warp == kWarpAdd && lane < kLanes && row < unit_rows) {
             const float lse2 = any ? (M[y] == -INFINITY ? 0.0f : M[y]) - kLift + log2f(l) : -INFINITY;
             const int h = wk.hk * p.G + row / p.Nt;
@@ -458,14 +548,15 @@ __global__ void __launch_bounds__(kThreads, 1)
               p.part_lse[slot + r] = padding ? INFINITY : lse2;
           }
         }
-        __syncwarp();
+#pragma unroll
+        for (int y = 0; y < kPerLane; ++y) none[y] = __ballot_sync(0xffffffffu, none[y]);
         if (whole) {
           const int rows = unit_rows - first_row;
           int node = first_row % p.Nt;
           __nv_bfloat16 *head = p.o + wk.b * p.so.b + (wk.hk * p.G + first_row / p.Nt) * p.so.h + col;
 #pragma unroll
           for (int r = 0; r < C; ++r) {
-            if (r < rows) head[node * p.so.n] = __float2bfloat16(fac[C + r] != 0.0f ? o[r] * fac[r] : 0.0f);
+            if (r < rows) head[node * p.so.n] = __float2bfloat16((none[r / 32] >> (r % 32)) & 1u ? 0.0f : o[r] * fac[r]);
             if (++node == p.Nt) {
               node = 0;
               head += p.so.h;
@@ -475,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float *part = p.part_o + slot * kD + col;
 #pragma unroll
           for (int r = 0; r < C; ++r)
-            if (first_row + r < unit_rows) part[r * kD] = fac[C + r] != 0.0f ? o[r] * fac[r] : 0.0f;
+            if (first_row + r < unit_rows) part[r * kD] = (none[r / 32] >> (r % 32)) & 1u ? 0.0f : o[r] * fac[r];
         }
       }
       __syncwarp();
@@ -488,16 +579,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ softmax, a key per thread
-    regs_increase<kRegsSoftmax>();
+    regs_increase<R::kSoftmax>();
     const int wg = warp >> 2, key = threadIdx.x & 127;
     float *most = floats(L::kOffMost) + wg * 4 * C;        // [4 warps][C]
     float *base = floats(L::kOffBase) + warp * 2 * C;      // 8 - m, then l's factor
-    float *lmove = floats(L::kOffMove) + warp * C;
     uint32_t x = 0, seg = 0, nmask = 0;  // tiles before the segment, segments, masked ones
+    uint32_t y0 = wg;                    // this warpgroup's next tile of the run
     bool ok = true;
     while (wk.next()) {
       const int n = wk.k1 - wk.k0;
-      const long long scale_row = (static_cast<long long>(wk.b) * p.Hkv + wk.hk) * p.blocks;
       const int from = wk.base();
       float l[C], lm[kPerLane];  // l relative to lm, of the columns that lanes look after
 #pragma unroll
@@ -506,72 +596,70 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int y = 0; y < kPerLane; ++y) lm[y] = -INFINITY;
       bool have_mask = false;
       // this key's scale, and the value scale of 16-key slice lane % 8 (0: behind the end)
-      auto k_scale = [&](int kt) {
-        const int j = kt * kKeys + key;
-        return j < wk.len ? p.k_scale[scale_row + (j >> p.block_log2)] : 0.0f;
-      };
-      auto v_scale = [&](int kt) {
-        const int j = kt * kKeys + (lane & 7) * 16;
-        return j < wk.len ? p.v_scale[scale_row + (j >> p.block_log2)] : 0.0f;
-      };
-      const int kt0 = wk.k0 + ((x & 1) ^ wg);
+      const float *k_scale = p.k_scale + (static_cast<long long>(wk.b) * p.Hkv + wk.hk) * p.blocks;
+      const float *v_scale = p.v_scale + (static_cast<long long>(wk.b) * p.Hkv + wk.hk) * p.blocks;
       float ks = 0.0f, v8 = 0.0f;
-      if (kt0 < wk.k1) {
-        ks = k_scale(kt0);
-        v8 = v_scale(kt0);
-      }
-      // (written before the products of this segment were issued; four in turn, for at most two tiles' scores are ahead)
-      const float *rf = row_f + (seg & 3) * C;
-      for (int kt = kt0; kt < wk.k1; kt += 2) {  // (a warp that gave up still meets the others)
-        const uint32_t y0 = x + (kt - wk.k0), ph = (y0 >> 1) & 1;  // (y0 & 1 is wg)
+      auto fetch = [&](int kt) {
+        const int j = kt * kKeys + key, j8 = kt * kKeys + (lane & 7) * 16;
+        ks = j < wk.len ? k_scale[j >> p.block_log2] : 0.0f;
+        v8 = j8 < wk.len ? v_scale[j8 >> p.block_log2] : 0.0f;
+      };
+      if (y0 < x + n) fetch(wk.k0 + static_cast<int>(y0 - x));
+      // (written before the products of this segment were issued)
+      const float *rf = row_f + seg % L::kSegs * C;
+      for (; y0 < x + n; y0 += W) {  // (a warp that gave up still meets the others)
+        const int kt = wk.k0 + static_cast<int>(y0 - x);
+        const uint32_t buf = y0 % NB;
+        // log2 of this value's scale over the tile's greatest (vanishing ones count as 2^-100 of it), and its inverse
         const float kn = ks, vmax = warp_max_f32(v8), own = __shfl_sync(0xffffffffu, v8, (key >> 4) & 7);
-        if (kt + 2 < wk.k1) {
-          ks = k_scale(kt + 2);
-          v8 = v_scale(kt + 2);
-        }
+        const float lr = own > 0.0f ? fmaxf(lg2(own) - lg2(vmax), -100.0f) : 0.0f, inv = ex2(-lr);
+        if (y0 + W < x + n) fetch(kt + W);
         const bool masked = kt * kKeys + kKeys > from;
         if (ok && masked && !have_mask) {
           ok = __all_sync(0xffffffffu, mbar_wait(mask_full, nmask & 1, ctl, kSiteMaskFull));
           have_mask = true;
         }
-        // log2 of this value's scale over the tile's greatest; vanishing ones count as 2^-100 of it
-        const float ratio = fmaxf(own / vmax, 7.8886090522101181e-31f);
-        const float lr = own > 0.0f && vmax > 0.0f ? log2f(ratio) : 0.0f, inv = own > 0.0f && vmax > 0.0f ? 1.0f / ratio : 1.0f;
-        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&s_full[wg], ph, ctl, kSiteSFull));
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&s_full[buf], (y0 / NB) & 1, ctl, kSiteSFull));
         if (!ok) {
           named_barrier(1 + wg, 128);
           continue;
         }
         tc_fence_after();
         float s[C];
-        const uint32_t at = tmem + wg * 2 * C + lane_base;
+        const uint32_t at = tmem + buf * 2 * C + lane_base;
+        constexpr int kChunk = C == 64 ? 16 : C;  // (more does not fit the registers)
 #pragma unroll
-        for (int r = 0; r < C; r += 16) {
-          uint32_t hi[16], lo[16];
-          tmem_ld16(at + r, hi);
-          tmem_ld16(at + C + r, lo);
-          tmem_ld_wait16(hi);
-          tmem_ld_wait16(lo);
+        for (int r = 0; r < C; r += kChunk) {
+          uint32_t hi[kChunk], lo[kChunk];
+          tmem_pair(at + r, at + C + r, hi, lo);
 #pragma unroll
-          for (int y = 0; y < 16; y += 4) {
-            const float4 f = *reinterpret_cast<const float4 *>(rf + r + y);
-            const float g[4] = {fminf(f.x * kn, FLT_MAX), fminf(f.y * kn, FLT_MAX), fminf(f.z * kn, FLT_MAX),
-                                fminf(f.w * kn, FLT_MAX)};
-#pragma unroll
-            for (int z = 0; z < 4; ++z)
-              s[r + y + z] = fmaf(__uint_as_float(hi[y + z]) + __uint_as_float(lo[y + z]), g[z], lr);
+          for (int y = 0; y < kChunk; y += 2) {
+            const float2 f = *reinterpret_cast<const float2 *>(rf + r + y);
+            const float2 e = ffma2(fadd2(make_float2(__uint_as_float(hi[y]), __uint_as_float(hi[y + 1])),
+                                         make_float2(__uint_as_float(lo[y]), __uint_as_float(lo[y + 1]))),
+                                   fmul2(f, make_float2(kn, kn)), make_float2(lr, lr));
+            s[r + y] = e.x;
+            s[r + y + 1] = e.y;
           }
         }
+        tc_fence_before();
+        warp_arrive(&s_free[buf]);
         const int node = kt * kKeys + key - from;
         if (masked) {
-          int i = first_row % p.Nt, row = first_row;
-#pragma unroll
-          for (int r = 0; r < C; ++r) {
-            const bool live = row < unit_rows && !((dead[i >> 5] >> (i & 31)) & 1u);
-            if (!sees(bits, i, live, node, p.Nt)) s[r] = -INFINITY;
-            ++row;
-            if (++i == p.Nt) i = 0;
+          // the rows that see this key (rows that are padding may: their results are replaced).  A loop, because
+          // code that runs once a unit comes cold from memory.
+          uint64_t rows = node < 0 ? ~0ull : 0ull;
+          if (node >= 0 && node < p.Nt) {
+            int i = first_row % p.Nt;
+#pragma unroll 1
+            for (int r = 0; r < C; ++r) {
+              if ((i >> 5) >= (node >> 5) && ((bits[bit_row(i) + (node >> 5)] >> (node & 31)) & 1u)) rows |= 1ull << r;
+              if (++i == p.Nt) i = 0;
+            }
           }
+#pragma unroll
+          for (int r = 0; r < C; ++r)
+            if (!((rows >> r) & 1ull)) s[r] = -INFINITY;
         }
         // the tile's maxima: over the warp's keys, then over the four warps
 #pragma unroll
@@ -582,29 +670,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         named_barrier(1 + wg, 128);
         bool move = false;
+        float alpha[kPerLane];
 #pragma unroll
         for (int y = 0; y < kPerLane; ++y) {
           const int r = (lane & (kLanes - 1)) + y * 32;
           const float m = fmaxf(fmaxf(most[r], most[C + r]), fmaxf(most[2 * C + r], most[3 * C + r]));
-          float a = 1.0f;
+          alpha[y] = 1.0f;
           if (m > lm[y] + kMoveBy) {
-            a = ex2(lm[y] - m);
+            alpha[y] = ex2(lm[y] - m);
             lm[y] = m;
             move = true;
           }
           base[r] = kLift - (m == -INFINITY ? 0.0f : m);
           base[C + r] = m == -INFINITY ? 0.0f : ex2(m - lm[y]);
-          lmove[r] = a;
-          if ((warp & 3) == 0) tile_m[(y0 & 3) * C + r] = m;
+          if ((warp & 3) == 0) tile_m[y0 % L::kTiles * (C + 4) + r] = m;
         }
-        if ((warp & 3) == 0 && lane == 0) tile_v[y0 & 3] = vmax;
+        if ((warp & 3) == 0 && lane == 0) tile_m[y0 % L::kTiles * (C + 4) + C] = vmax;
         __syncwarp();
         if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
-          for (int r = 0; r < C; ++r) l[r] *= lmove[r];
+          for (int r = 0; r < C; ++r) l[r] *= __shfl_sync(0xffffffffu, alpha[r / 32], r % 32);
         }
-        // the weights' buffer is free once tile y0 - 2's product is done
-        if (y0 >= 2 && !(ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[wg], ph ^ 1, ctl, kSitePvDone)))) continue;
+        // the weights' buffer is free once tile y0 - W's product is done (and its sums, see kTiles)
+        if (y0 >= W &&
+            !(ok = __all_sync(0xffffffffu, mbar_wait(&o_empty[(y0 - W) % NB], ((y0 - W) / NB) & 1, ctl, kSiteDqEmpty))))
+          continue;
         uint8_t *prow = sP + wg * L::kTile + key * 128;
 #pragma unroll
         for (int r = 0; r < C; r += 16) {
@@ -613,12 +703,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int y = 0; y < 16; y += 4) {
             const float4 b = *reinterpret_cast<const float4 *>(base + r + y);
             const float4 g = *reinterpret_cast<const float4 *>(base + C + r + y);
-            const float w0 = ex2(s[r + y] + b.x), w1 = ex2(s[r + y + 1] + b.y), w2 = ex2(s[r + y + 2] + b.z),
-                        w3 = ex2(s[r + y + 3] + b.w);
-            l[r + y] = fmaf(w0, g.x * inv, l[r + y]);
-            l[r + y + 1] = fmaf(w1, g.y * inv, l[r + y + 1]);
-            l[r + y + 2] = fmaf(w2, g.z * inv, l[r + y + 2]);
-            l[r + y + 3] = fmaf(w3, g.w * inv, l[r + y + 3]);
+            const float2 e0 = fadd2(make_float2(s[r + y], s[r + y + 1]), make_float2(b.x, b.y));
+            const float2 e1 = fadd2(make_float2(s[r + y + 2], s[r + y + 3]), make_float2(b.z, b.w));
+            const float w0 = ex2(e0.x), w1 = ex2(e0.y), w2 = ex2(e1.x), w3 = ex2(e1.y);
+            const float2 ii = make_float2(inv, inv);
+            const float2 n0 = ffma2(make_float2(w0, w1), fmul2(make_float2(g.x, g.y), ii), make_float2(l[r + y], l[r + y + 1]));
+            const float2 n1 =
+                ffma2(make_float2(w2, w3), fmul2(make_float2(g.z, g.w), ii), make_float2(l[r + y + 2], l[r + y + 3]));
+            l[r + y] = n0.x;
+            l[r + y + 1] = n0.y;
+            l[r + y + 2] = n1.x;
+            l[r + y + 3] = n1.y;
             parts_of(pack_f16x2(w0, w1), pack_f16x2(w2, w3), &hi[y / 4], &lo[y / 4]);
           }
           *reinterpret_cast<uint4 *>(prow + (((r / 16) ^ (key & 7)) * 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
@@ -626,10 +721,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (masked) {
           // V rows that no query row sees become zeros (0 * NaN is NaN)
-          const uint32_t e_v = 2 * y0 + 1;
-          if (!(ok = __all_sync(0xffffffffu, mbar_wait(&full[e_v % S], (e_v / S) & 1, ctl, kSiteVFull)))) continue;
+          if (!(ok = __all_sync(0xffffffffu, mbar_wait(&v_full[y0 % SV], (y0 / SV) & 1, ctl, kSiteVFull)))) continue;
           if (node >= p.Nt || (node >= 0 && ((dead[node >> 5] >> (node & 31)) & 1u))) {
-            uint4 *v = reinterpret_cast<uint4 *>(ring + (e_v % S) * L::kTile + key * 128);
+            uint4 *v = reinterpret_cast<uint4 *>(ring_v + (y0 % SV) * L::kTile + key * 128);
 #pragma unroll
             for (int y = 0; y < 8; ++y) v[y] = make_uint4(0u, 0u, 0u, 0u);
           }
@@ -667,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (warp == kWarpMma) {
+  if (warp == kWarpS) {
     tc_fence_after();
     tmem_dealloc(tmem, L::kTmem);
   }
@@ -679,7 +773,7 @@ cudaError_t launch_tc(const CUtensorMap &tk, const CUtensorMap &tv, const Tree8P
   auto kern = fa_tree_fp8_tc_kernel<C>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kRequest);
   if (e != cudaSuccess) return e;
-  kern<<<static_cast<unsigned>(p.ranges) * p.groups, kThreads, L::kRequest, stream>>>(tk, tv, p);
+  kern<<<static_cast<unsigned>(p.ranges) * p.groups, L::kThreads, L::kRequest, stream>>>(tk, tv, p);
   return cudaGetLastError();
 }
 
