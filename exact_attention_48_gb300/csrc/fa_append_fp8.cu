@@ -11,7 +11,9 @@
 // read in bf16 and written in 8 bits.  A CTA takes the tokens of one block of
 // rows and walks heads: the tokens' angles are computed once, into shared memory,
 // and a head's rows stay in registers between the search for their greatest value
-// and the rounding, so nothing is read twice.  With few tokens several heads share
+// and the rounding, so nothing is read twice; the next head's rows are on their way
+// meanwhile.  Two pieces of 8 values are a thread's share of a head, so that a CTA has
+// 256 to 1024 threads by the tokens in a block; with few tokens several heads share
 // the CTA and the heads are cut across CTAs.
 
 #include <cfloat>
@@ -24,22 +26,20 @@
 namespace fa {
 namespace {
 
-constexpr int kThreads = 256;
-
 __device__ __forceinline__ long long floor_shift(long long x, int s) { return x >> s; }  // (arithmetic: floors)
 
 // A value as e4m3 stores it: infinities become NaN (the conversion would
 // saturate them).
 __device__ __forceinline__ float storable(float x) { return fabsf(x) <= FLT_MAX ? x : NAN; }
 
-// grid: x = blocks of rows (per_b of a sequence), y = head groups.  A head's
-// slots * d / 16 pieces take ITEMS per thread, or a part of the threads.
-template <bool INTERLEAVED, int ITEMS>
-__global__ void __launch_bounds__(kThreads) fa_append_fp8_kernel(const Append8Params p) {
+// grid: x = blocks of rows (per_b of a sequence), y = head groups.  A head takes
+// slots * d / 16 threads, all of the CTA's or a part.
+template <bool INTERLEAVED, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) fa_append_fp8_kernel(const Append8Params p) {
   extern __shared__ float table[];  // cos, then sin: [slots][rot / 2]
   __shared__ uint32_t most[3][kThreads / 4];  // greatest values of the heads at work, used in turn
   const int per_row = p.d >> 4, half = p.rot >> 1, tid = threadIdx.x;
-  const int lanes = ITEMS > 1 ? kThreads : per_row * p.slots;
+  const int lanes = per_row * p.slots;
   const int heads_at_once = kThreads / lanes;
   const int b = blockIdx.x / p.per_b, j = blockIdx.x - b * p.per_b;
   const int block = 1 << p.block_log2;
@@ -67,85 +67,92 @@ __global__ void __launch_bounds__(kThreads) fa_append_fp8_kernel(const Append8Pa
   __syncthreads();
 
   const int hl = tid / lanes, in_head = tid - hl * lanes;
-  const int c = in_head & (per_row - 1), slot0 = in_head / per_row, slot_step = kThreads / per_row;
+  const int c = in_head & (per_row - 1), slot = in_head / per_row;
   const Pieces x = pieces_of<INTERLEAVED>(p.d, p.rot, c);
   const int heads = p.H + 2 * p.Hkv, step = heads_at_once * gridDim.y;
+  const bool row_on = slot < count && from + slot >= 0 && from + slot < p.Nk;  // has a row of the cache
+  const float *cs = cos_t + slot * half, *sn = sin_t + slot * half;
+  // the rows of the head that this thread takes from h0 on, and its block's scale if rows before these use it
+  uint4 w0, w1;
+  float old = 0.0f;
+  auto load = [&](int h0) {
+    const int hh = h0 + hl;
+    const bool is_q = hh < p.H, is_k = !is_q && hh < p.H + p.Hkv;
+    if (hl >= heads_at_once || hh >= heads || slot >= count || !(is_q || row_on)) return;
+    const int h = is_q ? hh : (is_k ? hh - p.H : hh - p.H - p.Hkv);
+    const __nv_bfloat16 *row = is_q   ? p.q + b * p.sq.b + h * p.sq.h + (n0 + slot) * p.sq.n
+                               : is_k ? p.k + b * p.sk.b + h * p.sk.h + (n0 + slot) * p.sk.n
+                                      : p.v + b * p.sv.b + h * p.sv.h + (n0 + slot) * p.sv.n;
+    w0 = __ldcs(reinterpret_cast<const uint4 *>(row + x.c0));
+    w1 = __ldcs(reinterpret_cast<const uint4 *>(row + x.c1));
+  };
   int turn = 0;
-  for (int h0 = blockIdx.y * heads_at_once; h0 < heads; h0 += step, turn = turn == 2 ? 0 : turn + 1) {
+  load(blockIdx.y * heads_at_once);
+  for (int h0 = blockIdx.y * heads_at_once; h0 < heads; h0 += step) {
     const int hh = h0 + hl;
     const bool is_q = hh < p.H, is_k = !is_q && hh < p.H + p.Hkv;
     const bool head_on = hl < heads_at_once && hh < heads && (is_q || any_row);
+    const bool on = head_on && slot < count && (is_q || row_on);
     const int h = is_q ? hh : (is_k ? hh - p.H : hh - p.H - p.Hkv);
-    const __nv_bfloat16 *src = is_q ? p.q + b * p.sq.b + h * p.sq.h
-                                    : (is_k ? p.k + b * p.sk.b + h * p.sk.h : p.v + b * p.sv.b + h * p.sv.h);
-    const long long sn_ = is_q ? p.sq.n : (is_k ? p.sk.n : p.sv.n);
     float *scale = (is_k ? p.ks : p.vs) + (static_cast<long long>(b) * p.Hkv + h) * p.blocks + blk;
-    float old = 0.0f;
-    if (head_on && !is_q && has_old) old = *scale;
-    float y[ITEMS][16];
+    old = head_on && !is_q && has_old ? *scale : 0.0f;
+    const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+    if (h0 + step < heads) load(h0 + step);
+    float y[16];
     float top = 0.0f;
-    // whether a thread's item is at work (of K and V: has a row of the cache)
-    auto on = [&](int it) {
-      const int s = slot0 + it * slot_step;
-      return head_on && s < count && (is_q || (from + s >= 0 && from + s < p.Nk));
-    };
-#pragma unroll
-    for (int it = 0; it < ITEMS; ++it) {
-      if (!on(it)) continue;
-      const int s = slot0 + it * slot_step;
-      const __nv_bfloat16 *row = src + (n0 + s) * sn_;
-      const uint4 w0 = __ldcs(reinterpret_cast<const uint4 *>(row + x.c0));
-      const uint4 w1 = __ldcs(reinterpret_cast<const uint4 *>(row + x.c1));
-      const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+    if (on) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float2 v = unpack2(w[i]);
-        y[it][2 * i] = v.x;
-        y[it][2 * i + 1] = v.y;
+        y[2 * i] = v.x;
+        y[2 * i + 1] = v.y;
       }
       if (is_q || is_k) {
-        const float *cs = cos_t + s * half, *sn = sin_t + s * half;
         if (INTERLEAVED) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             if (!(i < 4 ? x.t0 : x.t1)) continue;
             const int pr = i < 4 ? x.p0 + i : x.p1 + i - 4;
-            const float a = y[it][2 * i], z = y[it][2 * i + 1];
-            y[it][2 * i] = a * cs[pr] - z * sn[pr];
-            y[it][2 * i + 1] = z * cs[pr] + a * sn[pr];
+            const float a = y[2 * i], z = y[2 * i + 1];
+            y[2 * i] = a * cs[pr] - z * sn[pr];
+            y[2 * i + 1] = z * cs[pr] + a * sn[pr];
           }
         } else if (x.t0) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int pr = i < 4 ? x.p0 + i : x.p1 + i - 4;
-            const float a = y[it][i], z = y[it][8 + i];
-            y[it][i] = a * cs[pr] - z * sn[pr];
-            y[it][8 + i] = z * cs[pr] + a * sn[pr];
+            const float a = y[i], z = y[8 + i];
+            y[i] = a * cs[pr] - z * sn[pr];
+            y[8 + i] = z * cs[pr] + a * sn[pr];
           }
         }
       }
       if (is_q) {
         uint32_t o[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = pack2(y[it][2 * i], y[it][2 * i + 1]);
-        __nv_bfloat16 *dst = p.qo + b * p.sqo.b + h * p.sqo.h + (n0 + s) * p.sqo.n;
+        for (int i = 0; i < 8; ++i) o[i] = pack2(y[2 * i], y[2 * i + 1]);
+        __nv_bfloat16 *dst = p.qo + b * p.sqo.b + h * p.sqo.h + (n0 + slot) * p.sqo.n;
         __stcs(reinterpret_cast<uint4 *>(dst + x.c0), make_uint4(o[0], o[1], o[2], o[3]));
         __stcs(reinterpret_cast<uint4 *>(dst + x.c1), make_uint4(o[4], o[5], o[6], o[7]));
       } else {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          y[it][i] = storable(y[it][i]);
-          top = fmaxf(top, fabsf(y[it][i]));  // (fmaxf passes over NaN)
+          y[i] = storable(y[i]);
+          top = fmaxf(top, fabsf(y[i]));  // (fmaxf passes over NaN)
         }
       }
     }
+    if (h0 + heads_at_once <= p.H) continue;  // (only q: the same for the whole CTA)
     // the heads' greatest values (that of this turn's slot was last read two barriers ago)
-    const int next_turn = turn == 2 ? 0 : turn + 1;
+    const int now_turn = turn, next_turn = turn == 2 ? 0 : turn + 1;
+    turn = next_turn;
     if (tid < heads_at_once) most[next_turn][tid] = 0u;
-    if (top > 0.0f) atomicMax(&most[turn][hl], __float_as_uint(top));
+    // the lanes of a head within the warp first
+    for (int o = 1; o < lanes && o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (top > 0.0f && (lanes < 32 ? in_head == 0 : (tid & 31) == 0)) atomicMax(&most[now_turn][hl], __float_as_uint(top));
     __syncthreads();
     if (!head_on || is_q) continue;
-    const float now = fmaxf(old, least_scale(__uint_as_float(most[turn][hl]))), inv = 1.0f / now;
+    const float now = fmaxf(old, least_scale(__uint_as_float(most[now_turn][hl]))), inv = 1.0f / now;
     uint8_t *dst = is_k ? p.kc + b * p.skc.b + h * p.skc.h : p.vc + b * p.svc.b + h * p.svc.h;
     const long long dn = is_k ? p.skc.n : p.svc.n;
     if (has_old && now > old) {  // the rows before the new ones, 16 bytes a thread
@@ -153,22 +160,20 @@ __global__ void __launch_bounds__(kThreads) fa_append_fp8_kernel(const Append8Pa
       const float r = old / now;
       for (int e = in_head; e < rows; e += lanes) {
         uint4 *at = reinterpret_cast<uint4 *>(dst + (lo + e / per_row) * dn + (e & (per_row - 1)) * 16);
-        uint4 w = *at;
-        w.x = rescale_codes(w.x, r);
-        w.y = rescale_codes(w.y, r);
-        w.z = rescale_codes(w.z, r);
-        w.w = rescale_codes(w.w, r);
-        *at = w;
+        uint4 v = *at;
+        v.x = rescale_codes(v.x, r);
+        v.y = rescale_codes(v.y, r);
+        v.z = rescale_codes(v.z, r);
+        v.w = rescale_codes(v.w, r);
+        *at = v;
       }
     }
-#pragma unroll
-    for (int it = 0; it < ITEMS; ++it) {
-      if (!on(it)) continue;
-      uint8_t *row = dst + (from + slot0 + it * slot_step) * dn;
+    if (on) {
+      uint8_t *row = dst + (from + slot) * dn;
       uint32_t o[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        o[i] = pack_e4m3x4(y[it][4 * i] * inv, y[it][4 * i + 1] * inv, y[it][4 * i + 2] * inv, y[it][4 * i + 3] * inv);
+        o[i] = pack_e4m3x4(y[4 * i] * inv, y[4 * i + 1] * inv, y[4 * i + 2] * inv, y[4 * i + 3] * inv);
       *reinterpret_cast<uint2 *>(row + x.c0) = make_uint2(o[0], o[1]);
       *reinterpret_cast<uint2 *>(row + x.c1) = make_uint2(o[2], o[3]);
     }
@@ -176,9 +181,9 @@ __global__ void __launch_bounds__(kThreads) fa_append_fp8_kernel(const Append8Pa
   }
 }
 
-template <bool INTERLEAVED, int ITEMS>
+template <bool INTERLEAVED, int kThreads>
 cudaError_t launch_append8_t(const Append8Params &p, cudaStream_t stream) {
-  auto kern = fa_append_fp8_kernel<INTERLEAVED, ITEMS>;
+  auto kern = fa_append_fp8_kernel<INTERLEAVED, kThreads>;
   const size_t smem = sizeof(float) * p.slots * p.rot;  // up to 64 KB
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 65536);
   if (e != cudaSuccess) return e;
@@ -186,12 +191,18 @@ cudaError_t launch_append8_t(const Append8Params &p, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
+// A head's lanes, 4 (one token, d = 64) to 1024, all in one CTA.
+int threads_of(const Append8Params &p) {
+  const int lanes = p.slots * (p.d / 16);
+  return lanes > 512 ? 1024 : (lanes > 256 ? 512 : 256);
+}
+
 template <bool INTERLEAVED>
 cudaError_t launch_append8_i(const Append8Params &p, cudaStream_t stream) {
-  switch (p.slots * (p.d / 16) / kThreads) {
-    case 4: return launch_append8_t<INTERLEAVED, 4>(p, stream);
-    case 2: return launch_append8_t<INTERLEAVED, 2>(p, stream);
-    default: return launch_append8_t<INTERLEAVED, 1>(p, stream);
+  switch (threads_of(p)) {
+    case 1024: return launch_append8_t<INTERLEAVED, 1024>(p, stream);
+    case 512: return launch_append8_t<INTERLEAVED, 512>(p, stream);
+    default: return launch_append8_t<INTERLEAVED, 256>(p, stream);
   }
 }
 
@@ -203,8 +214,7 @@ cudaError_t launch_append8(bool interleaved, const Append8Params &in, cudaStream
   p.per_b = (p.N - 1 + block - 1) / block + 1;
   p.slots = 1;
   while (p.slots < p.N && p.slots < block) p.slots *= 2;
-  const int lanes = p.slots * (p.d / 16);
-  const int heads = p.H + 2 * p.Hkv, at_once = lanes < kThreads ? kThreads / lanes : 1;
+  const int heads = p.H + 2 * p.Hkv, at_once = threads_of(p) / (p.slots * (p.d / 16));
   const long long blocks = static_cast<long long>(p.B) * p.per_b;
   long long groups = (heads + at_once - 1) / at_once;
   const long long want = (4 * 152 + blocks - 1) / blocks;  // four CTAs an SM where there are heads for them

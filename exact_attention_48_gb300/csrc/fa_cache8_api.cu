@@ -204,7 +204,7 @@ fa_status_t fa_cache_compact_fp8(const void *k, const int64_t *k_strides, const 
   st = check_block(block);
   if (st != FA_OK) return st;
   if (Nk_out < 1 || Nk_out > kMaxRows || M < 1 || M > kMaxRows) return FA_ERR_INVALID_ARGUMENT;
-  if (static_cast<long long>(B) * Hkv * ((M + 127) / 128 + 1) >= (1LL << 31)) return FA_ERR_INVALID_ARGUMENT;  // the grid
+  if (static_cast<long long>(B) * Hkv * ((M + 127) / 128 + 1) >= (1LL << 30)) return FA_ERR_INVALID_ARGUMENT;  // the grid
   if (!kept || !aligned4(kept) || !row_stride(kept_b_stride) || !row_stride(kept_h_stride) || !aligned4(base))
     return FA_ERR_INVALID_ARGUMENT;
   if (!k_scale || !v_scale || !k_scale_out || !v_scale_out || !aligned4(k_scale) || !aligned4(v_scale) ||

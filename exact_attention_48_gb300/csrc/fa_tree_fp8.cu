@@ -552,8 +552,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Merge the partial results of units cut by a run's end:
 //   O = sum 2^(lse_s - M) O_s / sum 2^(lse_s - M).
-// A block takes one row of one cut unit; its warps deal the runs out among
-// themselves (a run's row is one coalesced read) and add up in a fixed order.
+// WARPS warps take one row of one cut unit, dealing the runs out among themselves
+// (a run's row is one coalesced read) and adding up in a fixed order: eight where a
+// unit is cut into many runs, one where it is cut into two or three (B16 H16 Nt32:
+// 4864 rows, 15 us with eight).
 constexpr int kMergeWarps = 8;
 
 // +inf, the mark of padding, before NaN, and NaN before every other value.
@@ -562,13 +564,15 @@ __device__ __forceinline__ float merge_max(float a, float b) {
   return x != INFINITY && (a != a || b != b) ? NAN : x;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kMergeWarps * 32) fa_tree_fp8_merge_kernel(const Tree8Params p) {
+template <int D, int WARPS>
+__global__ void __launch_bounds__(kMergeWarps * 32) fa_tree_fp8_merge_kernel(const Tree8Params p, int total) {
   constexpr int kCols = D / 32;
-  __shared__ float sh_m[kMergeWarps], sh_l[kMergeWarps], sh_o[kMergeWarps][D];
+  __shared__ float sh_m[WARPS], sh_l[WARPS], sh_o[WARPS][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int unit_rows = p.G * p.Nt, rows = p.rows;
-  const int r = blockIdx.x % unit_rows, x = blockIdx.x / unit_rows;
+  const int at_row = WARPS == 1 ? blockIdx.x * kMergeWarps + warp : blockIdx.x, w0 = WARPS == 1 ? 0 : warp;
+  if (at_row >= total) return;
+  const int r = at_row % unit_rows, x = at_row / unit_rows;
   cudaGridDependencySynchronize();  // (launched while the main kernel still runs)
   const int4 cut = p.cuts[x];
   const int b = cut.x, hk = cut.y, first = cut.z, last = cut.w;
@@ -578,7 +582,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) fa_tree_fp8_merge_kernel(con
   float m = -INFINITY, l = 0.0f, o[kCols];
 #pragma unroll
   for (int y = 0; y < kCols; ++y) o[y] = 0.0f;
-  for (int run = first + warp; run <= last; run += kMergeWarps) {
+#pragma unroll 2
+  for (int run = first + w0; run <= last; run += WARPS) {
     const long long at = ((static_cast<long long>(run) * p.groups + group) * 2 + (run == first ? 1 : 0)) * rows + lr;
     const float s = p.part_lse[at];
     float v[kCols];
@@ -592,36 +597,46 @@ __global__ void __launch_bounds__(kMergeWarps * 32) fa_tree_fp8_merge_kernel(con
     for (int y = 0; y < kCols; ++y) o[y] = o[y] * fa + v[y] * fb;
     m = mn;
   }
+  const int node = r % p.Nt, h = hk * p.G + r / p.Nt;
+  __nv_bfloat16 *dst = p.o + b * p.so.b + h * p.so.h + node * p.so.n;
+  float *lse = p.lse + (static_cast<long long>(b) * p.H + h) * p.Nt + node;
+  if constexpr (WARPS == 1) {
+    const bool any = m != -INFINITY && m != INFINITY;  // +inf: padding
+#pragma unroll
+    for (int y = 0; y < kCols; ++y) dst[y * 32 + lane] = __float2bfloat16(any ? o[y] / l : 0.0f);
+    if (lane == 0) *lse = any ? (m + log2f(l)) * kLn2 : -INFINITY;
+    return;
+  }
   if (lane == 0) {
-    sh_m[warp] = m;
-    sh_l[warp] = l;
+    sh_m[w0] = m;
+    sh_l[w0] = l;
   }
 #pragma unroll
-  for (int y = 0; y < kCols; ++y) sh_o[warp][y * 32 + lane] = o[y];
+  for (int y = 0; y < kCols; ++y) sh_o[w0][y * 32 + lane] = o[y];
   __syncthreads();
   if (threadIdx.x >= D) return;
   float M = -INFINITY;
 #pragma unroll
-  for (int w = 0; w < kMergeWarps; ++w) M = merge_max(M, sh_m[w]);
+  for (int w = 0; w < WARPS; ++w) M = merge_max(M, sh_m[w]);
   float sum = 0.0f, out = 0.0f;
 #pragma unroll
-  for (int w = 0; w < kMergeWarps; ++w) {
+  for (int w = 0; w < WARPS; ++w) {
     const float mw = sh_m[w], f = mw == -INFINITY ? 0.0f : (mw == M ? 1.0f : ex2(mw - M));
     sum += sh_l[w] * f;
     out += sh_o[w][threadIdx.x] * f;
   }
-  const bool any = M != -INFINITY && M != INFINITY;  // +inf: padding
-  const int node = r % p.Nt, h = hk * p.G + r / p.Nt;
-  p.o[b * p.so.b + h * p.so.h + node * p.so.n + threadIdx.x] = __float2bfloat16(any ? out / sum : 0.0f);
-  if (threadIdx.x == 0)
-    p.lse[(static_cast<long long>(b) * p.H + h) * p.Nt + node] = any ? (M + log2f(sum)) * kLn2 : -INFINITY;
+  const bool any = M != -INFINITY && M != INFINITY;
+  dst[threadIdx.x] = __float2bfloat16(any ? out / sum : 0.0f);
+  if (threadIdx.x == 0) *lse = any ? (M + log2f(sum)) * kLn2 : -INFINITY;
 }
 
 template <int D>
 cudaError_t launch_merge8(const Tree8Params &p, cudaStream_t stream) {
   const long long cuts = p.cuts_by_unit ? static_cast<long long>(p.B) * p.Hkv : p.ranges;  // at most 152
+  const bool many = p.ranges >= 4ll * p.B * p.Hkv;  // a unit is cut into about ranges / units + 1 runs
+  const int rows = static_cast<int>(cuts * p.G * p.Nt);  // (at most 152 runs a group of rows: below 2^24)
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(cuts * p.G * p.Nt));
+  cfg.gridDim = dim3(static_cast<unsigned>(many ? rows : (rows + kMergeWarps - 1) / kMergeWarps));
   cfg.blockDim = dim3(kMergeWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -629,7 +644,8 @@ cudaError_t launch_merge8(const Tree8Params &p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fa_tree_fp8_merge_kernel<D>, p);
+  return many ? cudaLaunchKernelEx(&cfg, fa_tree_fp8_merge_kernel<D, kMergeWarps>, p, rows)
+              : cudaLaunchKernelEx(&cfg, fa_tree_fp8_merge_kernel<D, 1>, p, rows);
 }
 
 template <int D, int RT>

@@ -10,14 +10,16 @@
 //
 // What bounds it.  The tests need single values, which all nodes' threads fetch at
 // once; the sums need a row of p (and of q) where a sibling is left to try, and one
-// for the next token: a few dependent passes over a row.  A sequence's row is cut
-// over a cluster of CTAs, which add their sums through distributed shared memory;
-// S is kept by all of them and they take the same decisions.
+// for the next token: a few dependent passes over a row, each some 2 us of latency.
+// A sequence's row is cut over a cluster of CTAs, which add their sums through
+// distributed shared memory; all of them know every sum and take the same decisions.
+// Without a draft's row a rejection changes one value of R, so that one pass a node
+// gives all its sums.
 //
 // Precision.  Which token a number falls on is decided by a sum over the whole
-// vocabulary, so R and S are pairs of fp32 (hi + lo, about 48 bits): fp64 runs at
-// a sixty-fourth of the fp32 rate here, and a row in it would take longer than
-// its memory traffic.  The few comparisons are in fp64.
+// vocabulary, so R and S are pairs of fp32 (hi + lo, about 48 bits), and so are the
+// comparisons: fp64 runs at a sixty-fourth of the fp32 rate here, 256 cycles for one
+// addition of a 512-thread CTA.
 
 #include <cooperative_groups.h>
 #include <cstdint>
@@ -29,17 +31,16 @@ namespace cg = cooperative_groups;
 namespace fa {
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxNodes = 128, kMaxRanks = 8;
-constexpr int kUnroll = 8;
+constexpr int kUnroll = 16;
 constexpr int kTile = 32 * kUnroll;   // least elements of a warp's tile
-constexpr int kMaxTiles = 2048;       // tiles of a CTA's share of a row
+constexpr int kMaxTiles = 1024;       // tiles of a CTA's share of a row
 
 // A number as the sum of two fp32, |lo| at most half a unit of hi's last place.
 struct Pair {
   float hi, lo;
 };
-__device__ __forceinline__ double value(Pair a) { return static_cast<double>(a.hi) + a.lo; }
 __device__ __forceinline__ Pair quick_sum(float a, float b) {  // |a| >= |b|
   const float s = __fadd_rn(a, b);
   return Pair{s, __fsub_rn(b, __fsub_rn(s, a))};
@@ -52,13 +53,42 @@ __device__ __forceinline__ Pair add(Pair a, Pair b) {
   const Pair s = two_sum(a.hi, b.hi);
   return quick_sum(s.hi, __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo)));
 }
+__device__ __forceinline__ Pair times(Pair a, float b) {
+  const float ph = __fmul_rn(a.hi, b), pl = __fmaf_rn(a.hi, b, -ph);
+  return quick_sum(ph, __fmaf_rn(a.lo, b, pl));
+}
+__device__ __forceinline__ Pair times(Pair a, Pair b) {
+  const float ph = __fmul_rn(a.hi, b.hi), pl = __fmaf_rn(a.hi, b.hi, -ph);
+  return quick_sum(ph, __fadd_rn(pl, __fmaf_rn(a.hi, b.lo, __fmul_rn(a.lo, b.hi))));
+}
+__device__ __forceinline__ Pair minus(Pair a, Pair b) {
+  const Pair d = two_sum(a.hi, -b.hi);
+  return quick_sum(d.hi, __fadd_rn(d.lo, __fsub_rn(a.lo, b.lo)));
+}
+__device__ __forceinline__ bool below(Pair a, Pair b) { return minus(a, b).hi < 0.0f; }
 // r - s q, or 0 if that is less.
 __device__ __forceinline__ Pair less(Pair r, Pair s, float q) {
-  const float ph = __fmul_rn(s.hi, q), pl = __fmaf_rn(s.hi, q, -ph);
-  const Pair p = quick_sum(ph, __fmaf_rn(s.lo, q, pl));
-  const Pair d = two_sum(r.hi, -p.hi);
-  const Pair x = quick_sum(d.hi, __fadd_rn(d.lo, __fsub_rn(r.lo, p.lo)));
+  const Pair x = minus(r, times(s, q));
   return x.hi > 0.0f ? x : Pair{0.0f, 0.0f};
+}
+__device__ __forceinline__ Pair from_lane(Pair a, int lane) {
+  return Pair{__shfl_sync(0xffffffffu, a.hi, lane), __shfl_sync(0xffffffffu, a.lo, lane)};
+}
+// The sum over the lanes' 2^n neighbours, in all of them.
+__device__ __forceinline__ Pair lanes_sum(Pair a, int width) {
+  for (int o = 1; o < width; o <<= 1)
+    a = add(a, Pair{__shfl_xor_sync(0xffffffffu, a.hi, o), __shfl_xor_sync(0xffffffffu, a.lo, o)});
+  return a;
+}
+// Sums over the lanes up to each one.
+__device__ __forceinline__ Pair lanes_scan(Pair a) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const Pair z{__shfl_up_sync(0xffffffffu, a.hi, o), __shfl_up_sync(0xffffffffu, a.lo, o)};
+    if (lane >= o) a = add(z, a);
+  }
+  return a;
 }
 
 struct Shared {
@@ -66,21 +96,25 @@ struct Shared {
   float u[kMaxNodes], p[kMaxNodes], q[kMaxNodes];  // the node's number, and its token's p and q at its parent
   int rejected[kMaxNodes];                         // tokens rejected at the node being worked on
   Pair sums[kMaxNodes];                            // S before the first, the second, ... child
+  Pair taken;                                      // what the last rejection took of R, without a draft's row
   Pair tile[kMaxTiles];                            // this CTA's sums of R
   Pair warp[kWarps];
-  Pair rank[kMaxRanks];                            // every CTA's sum
-  double scan[kWarps];
-  int found, last;
+  Pair rank[2][kMaxRanks];                         // every CTA's sum, of two passes in turn
 };
 
 // R(y) after the first k children of a node.
 __device__ __forceinline__ Pair rest(const Shared &s, int k, float p, float q, int y, bool drafted) {
   Pair r{p > 0.0f ? p : 0.0f, 0.0f};
-  for (int j = 0; j < k; ++j) r = less(r, s.sums[j], drafted ? q : (y == s.rejected[j] ? 1.0f : 0.0f));
+  if (drafted) {
+    for (int j = 0; j < k; ++j) r = less(r, s.sums[j], q);
+  } else {
+    for (int j = 0; j < k; ++j)
+      if (y == s.rejected[j]) r = less(r, s.sums[j], 1.0f);
+  }
   return r;
 }
 
-__global__ void __launch_bounds__(kThreads) fa_verify_kernel(const VerifyParams p) {
+__global__ void __launch_bounds__(kThreads, 4) fa_verify_kernel(const VerifyParams p) {
   __shared__ Shared s;
   cg::cluster_group cluster = cg::this_cluster();
   const int ranks = p.ranks, rank = blockIdx.x % ranks, b = blockIdx.x / ranks;
@@ -92,175 +126,177 @@ __global__ void __launch_bounds__(kThreads) fa_verify_kernel(const VerifyParams 
   const int per_tile = kTile * ((share + kTile * kMaxTiles - 1) / (kTile * kMaxTiles));
   const int tiles = (v1 - v0 + per_tile - 1) / per_tile;
   const float *target = p.target + b * p.tb, *draft = drafted ? p.draft + b * p.db : nullptr;
+  int *accepted = p.accepted + static_cast<long long>(b) * p.Nt;
 
-  if (tid < p.Nt) {
-    const int up = p.parents[b * p.par_b + tid], x = p.tokens[b * p.tok_b + tid];
-    const bool asks = tid > 0 && up >= 0 && up < tid && x >= 0 && x < p.V;
-    s.parent[tid] = tid == 0 ? up : (asks ? up : -2);
-    s.token[tid] = x;
-    s.u[tid] = p.uniforms[b * p.uni_b + tid];
-    s.p[tid] = asks ? target[up * p.tn + x] : 0.0f;
-    s.q[tid] = asks ? (drafted ? draft[up * p.dn + x] : 1.0f) : 0.0f;
+  if (tid < kMaxNodes) {
+    int up = -2;
+    if (tid < p.Nt) {
+      const int x = p.tokens[b * p.tok_b + tid];
+      up = p.parents[b * p.par_b + tid];
+      const bool asks = tid > 0 && up >= 0 && up < tid && x >= 0 && x < p.V;
+      s.token[tid] = x;
+      s.u[tid] = p.uniforms[b * p.uni_b + tid];
+      s.p[tid] = asks ? target[up * p.tn + x] : 0.0f;
+      s.q[tid] = asks ? (drafted ? draft[up * p.dn + x] : 1.0f) : 0.0f;
+      if (tid > 0 && !asks) up = -2;
+    }
+    s.parent[tid] = up;
   }
   if (tid == 0) s.sums[0] = Pair{1.0f, 0.0f};
   __syncthreads();
   if (s.parent[0] != -1) {  // (the same for the whole cluster)
     if (rank == 0) {
-      for (int i = tid; i < p.Nt; i += kThreads) p.accepted[static_cast<long long>(b) * p.Nt + i] = -1;
+      for (int i = tid; i < p.Nt; i += kThreads) accepted[i] = -1;
       if (tid == 0) p.counts[b] = 0, p.next[b] = -1;
     }
     return;
   }
 
-  int node = 0, k = 0, have = 0, count = 1;  // the node, children tried, sums known past the first
-  // sums[k]: the sum of R after k children, of all CTAs; tile sums on the way
+  // Every warp walks the tree, on the same numbers.
+  int node = 0, k = 0, count = 1, pass = 0;  // the node, children tried, nodes accepted, passes made
+  // the sum of R after k children, of all CTAs; tile sums on the way
   auto sum_rest = [&]() {
     const float *pr = target + node * p.tn, *qr = drafted ? draft + node * p.dn : nullptr;
     Pair mine{0.0f, 0.0f};
     for (int i = warp; i < tiles; i += kWarps) {
       const int at = v0 + i * per_tile, end = min(v1, at + per_tile);
-      Pair acc{0.0f, 0.0f};
+      float hi = 0.0f, lo = 0.0f;  // (the errors of the additions gathered in lo)
       for (int y0 = at + lane; y0 < end; y0 += kTile) {
         float pv[kUnroll], qv[kUnroll];
 #pragma unroll
         for (int j = 0; j < kUnroll; ++j) {
           const int y = y0 + 32 * j;
           pv[j] = y < end ? pr[y] : 0.0f;
-          qv[j] = drafted && k > 0 && y < end ? qr[y] : 0.0f;
+        }
+        if (drafted && k > 0) {
+#pragma unroll
+          for (int j = 0; j < kUnroll; ++j) {
+            const int y = y0 + 32 * j;
+            qv[j] = y < end ? qr[y] : 0.0f;
+          }
         }
 #pragma unroll
-        for (int j = 0; j < kUnroll; ++j) acc = add(acc, rest(s, k, pv[j], qv[j], y0 + 32 * j, drafted));
+        for (int j = 0; j < kUnroll; ++j) {
+          const Pair r = rest(s, k, pv[j], qv[j], y0 + 32 * j, drafted);
+          const Pair t = two_sum(hi, r.hi);
+          hi = t.hi;
+          lo = __fadd_rn(lo, __fadd_rn(t.lo, r.lo));
+        }
       }
-#pragma unroll
-      for (int o = 16; o; o >>= 1)
-        acc = add(acc, Pair{__shfl_xor_sync(0xffffffffu, acc.hi, o), __shfl_xor_sync(0xffffffffu, acc.lo, o)});
-      if (lane == 0) s.tile[i] = acc;
-      mine = add(mine, acc);
+      const Pair sum = lanes_sum(two_sum(hi, lo), 32);
+      if (lane == 0) s.tile[i] = sum;
+      mine = add(mine, sum);
     }
     if (lane == 0) s.warp[warp] = mine;
     __syncthreads();
-    if (tid < ranks) {
-      Pair all{0.0f, 0.0f};
-      for (int w = 0; w < kWarps; ++w) all = add(all, s.warp[w]);
-      *cluster.map_shared_rank(&s.rank[rank], tid) = all;
+    Pair *shared_sums = s.rank[pass & 1];
+    if (warp == 0) {
+      const Pair all = lanes_sum(s.warp[lane % kWarps], kWarps);
+      if (lane < ranks) *cluster.map_shared_rank(&shared_sums[rank], lane) = all;
     }
     cluster.sync();
-    Pair all{0.0f, 0.0f};
-    for (int r = 0; r < ranks; ++r) all = add(all, s.rank[r]);
-    return all;
+    ++pass;
+    return lanes_sum(lane % kMaxRanks < ranks ? shared_sums[lane % kMaxRanks] : Pair{0.0f, 0.0f}, kMaxRanks);
   };
 
-  if (rank == 0 && tid == 0) p.accepted[static_cast<long long>(b) * p.Nt] = 0;
-  for (int i = 1; i < p.Nt; ++i) {
-    if (s.parent[i] != node) continue;
-    if (k > have) {
-      const Pair all = sum_rest();
-      if (tid == 0) s.sums[k] = all;
-      cluster.sync();  // (the sums are read by all before the next ones come)
-      have = k;
-    }
-    const Pair r = rest(s, k, s.p[i], s.q[i], s.token[i], drafted);
-    const double total = k ? value(s.sums[k]) : 1.0;
-    if (static_cast<double>(s.u[i]) * s.q[i] * total < value(r)) {
-      if (rank == 0 && tid == 0) p.accepted[static_cast<long long>(b) * p.Nt + count] = i;
-      node = i;
-      k = have = 0;
-      ++count;
-      __syncthreads();
-    } else {
-      __syncthreads();
-      if (tid == 0) s.rejected[k] = s.token[i];
-      ++k;
-      __syncthreads();
+  if (rank == 0 && tid == 0) accepted[0] = 0;
+  int have = 0;  // sums[0 .. have] are known
+  for (int w = 0; w < kMaxNodes / 32; ++w) {
+    // the children of the node among nodes 32 w .. 32 w + 31 (those of an accepted one come after it)
+    uint32_t kids = __ballot_sync(0xffffffffu, s.parent[32 * w + lane] == node && 32 * w + lane > 0);
+    while (kids) {
+      const int i = 32 * w + __ffs(kids) - 1;
+      kids &= kids - 1;
+      if (k > have) {
+        Pair all;
+        if (!drafted && have > 0)
+          all = minus(s.sums[k - 1], s.taken);  // (k - 1 children were tried with a sum of this node's row)
+        else
+          all = sum_rest();
+        if (tid == 0) s.sums[k] = all;
+        __syncthreads();
+        have = k;
+      }
+      const Pair r = rest(s, k, s.p[i], s.q[i], s.token[i], drafted);
+      const Pair ask = times(times(Pair{s.u[i], 0.0f}, s.q[i]), s.sums[k]);
+      if (below(ask, r)) {
+        if (rank == 0 && tid == 0) accepted[count] = i;
+        node = i;
+        k = have = 0;
+        ++count;
+        kids = __ballot_sync(0xffffffffu, s.parent[32 * w + lane] == node);
+      } else {
+        __syncthreads();  // (the others have read what changes)
+        if (tid == 0) {
+          s.rejected[k] = s.token[i];
+          s.taken = minus(r, less(r, s.sums[k], 1.0f));  // of R, without a draft's row
+        }
+        ++k;
+        __syncthreads();
+      }
     }
   }
 
   // ---- the token that follows
   Pair all = sum_rest();
   if (!(all.hi > 0.0f) && k > 0) {  // nothing is left: the target's row itself
-    cluster.sync();
     k = 0;
     all = sum_rest();
   }
-  const double total = value(all);
   const float u0 = fminf(fmaxf(s.u[0], 0.0f), 0.99999994f);
-  const double mark = static_cast<double>(u0) * total;
-  double below = 0.0;
-  int owner = -1, fallback = -1;
-  double before = 0.0;
-  for (int r = 0; r < ranks; ++r) {
-    const double v = value(s.rank[r]);
-    if (v > 0.0) {
-      fallback = r;
-      if (owner < 0 && below + v > mark) owner = r, before = below;
-    }
-    below += v;
-  }
-  if (owner < 0 && fallback >= 0) {  // rounding at the very end: the last CTA with anything
-    owner = fallback;
-    before = -1.0;
-  }
+  const Pair mark = times(all, u0);
+  // the CTA whose share the mark falls into (or, by rounding at the very end, the last one with anything)
+  const Pair own = lane < ranks ? s.rank[(pass - 1) & 1][lane] : Pair{0.0f, 0.0f};
+  const Pair upto = lanes_scan(own);
+  const uint32_t any = __ballot_sync(0xffffffffu, own.hi > 0.0f);
+  const uint32_t past = __ballot_sync(0xffffffffu, own.hi > 0.0f && below(mark, upto));
+  const int owner = past ? __ffs(past) - 1 : 31 - __clz(any);  // (-1: nothing at all)
+  const Pair before = owner > 0 ? from_lane(upto, owner - 1) : Pair{0.0f, 0.0f};
   if (rank == 0) {
     for (int i = tid; i < p.Nt; i += kThreads)
-      if (i >= count) p.accepted[static_cast<long long>(b) * p.Nt + i] = -1;
+      if (i >= count) accepted[i] = -1;
     if (tid == 0) {
       p.counts[b] = count;
       if (owner < 0) p.next[b] = -1;
     }
   }
-  if (rank == owner) {
-    // the tile: the first whose running sum is past the mark, or the last with anything
-    if (tid == 0) s.found = -1, s.last = -1;
-    __syncthreads();
-    if (tid == 0) {
-      double run = before < 0.0 ? 0.0 : before;
-      for (int i = 0; i < tiles; ++i) {
-        const double v = value(s.tile[i]);
-        if (!(v > 0.0)) continue;
-        s.last = i;
-        if (before >= 0.0 && run + v > mark) {
-          s.found = i;
-          s.scan[0] = run;
-          break;
-        }
-        run += v;
-      }
-    }
-    __syncthreads();
-    const bool exact = s.found >= 0;
-    const int tile = exact ? s.found : s.last, at = v0 + tile * per_tile, end = min(v1, at + per_tile);
-    double run = exact ? s.scan[0] : 0.0;
+  if (rank == owner && warp == 0) {
+    // a warp's search: the first of its lanes' parts, in order, whose running sum is past the mark, or the last with
+    // anything; `run`: what lies before
+    Pair run = before;
+    auto find = [&](Pair part) {
+      const Pair upto_lane = lanes_scan(part);
+      const uint32_t some = __ballot_sync(0xffffffffu, part.hi > 0.0f);
+      const uint32_t hit = __ballot_sync(0xffffffffu, part.hi > 0.0f && below(mark, add(run, upto_lane)));
+      const int at = hit ? __ffs(hit) - 1 : (some ? 31 - __clz(some) : 0);
+      if (at > 0) run = add(run, from_lane(upto_lane, at - 1));
+      return at;
+    };
+    // tiles, a run of them per lane, then one of those per lane in turn
+    const int per_lane = (tiles + 31) / 32;
+    Pair part{0.0f, 0.0f};
+    for (int i = lane * per_lane; i < min(tiles, (lane + 1) * per_lane); ++i) part = add(part, s.tile[i]);
+    int tile = find(part) * per_lane;
+    part = lane < per_lane && tile + lane < tiles ? s.tile[tile + lane] : Pair{0.0f, 0.0f};
+    tile += find(part);
+    // the tile's elements, likewise
     const float *pr = target + node * p.tn, *qr = drafted ? draft + node * p.dn : nullptr;
-    __syncthreads();
-    if (tid == 0) s.found = p.V, s.last = -1;
-    for (int y0 = at; y0 < end; y0 += kThreads) {
-      __syncthreads();
-      if (s.found < p.V) break;
-      const int y = y0 + tid;
-      const bool on = y < end;
-      const Pair r = on ? rest(s, k, pr[y], drafted && k > 0 ? qr[y] : 0.0f, y, drafted) : Pair{0.0f, 0.0f};
-      const double mine = value(r);
-      double incl = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const double z = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += z;
-      }
-      if (lane == 31) s.scan[warp] = incl;
-      __syncthreads();
-      double up_to = run;
-      for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) up_to += s.scan[w];
-        run += s.scan[w];
-      }
-      if (mine > 0.0) {
-        atomicMax(&s.last, y);
-        if (exact && up_to + incl > mark) atomicMin(&s.found, y);
-      }
-      __syncthreads();
+    auto element = [&](int y) {
+      return rest(s, k, pr[y], drafted && k > 0 ? qr[y] : 0.0f, y, drafted);
+    };
+    int at = v0 + tile * per_tile, n = min(v1, at + per_tile) - at;
+    while (n > 0) {
+      const int each = (n + 31) / 32;
+      const int lo = min(n, lane * each), hi = min(n, lo + each);
+      part = Pair{0.0f, 0.0f};
+#pragma unroll 8
+      for (int y = lo; y < hi; ++y) part = add(part, element(at + y));
+      const int l = find(part);
+      at += min(n, l * each);
+      n = min(n - min(n, l * each), each);
+      if (each == 1) break;
     }
-    __syncthreads();
-    if (tid == 0) p.next[b] = s.found < p.V ? s.found : s.last;
+    if (lane == 0) p.next[b] = at;
   }
   cluster.sync();  // no CTA leaves while another may write its shared memory
 }
@@ -269,7 +305,7 @@ __global__ void __launch_bounds__(kThreads) fa_verify_kernel(const VerifyParams 
 
 cudaError_t launch_verify(VerifyParams p, cudaStream_t stream) {
   int ranks = 1;
-  while (ranks < kMaxRanks && p.V > ranks * 4096) ranks *= 2;
+  while (ranks < kMaxRanks && p.V > ranks * 2048) ranks *= 2;
   p.ranks = ranks;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(p.B) * ranks);

@@ -532,7 +532,7 @@ FA_API fa_status_t fa_fwd_tree_fp8(const void *q, const int64_t *q_strides, cons
  * are neither lose their values; blocks that no row moves to stay as they are.
  *   k_scale, v_scale         : [B, Hkv, ceil(Nk / block)]
  *   k_scale_out, v_scale_out : [B, Hkv, ceil(Nk_out / block)]
- *   B * Hkv * (ceil(M / 128) + 1) < 2^31
+ *   B * Hkv * (ceil(M / 128) + 1) < 2^30
  * Either every output is its input (same pointers and strides, Nk_out = Nk: in
  * place; the lists must then ascend as for fa_cache_compact), or no output shares
  * an element with an argument.

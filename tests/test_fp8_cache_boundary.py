@@ -119,7 +119,7 @@ def compact(lib, **kw):
     # in place but for one output
     (dict(ko=at(0), vo=at(1), kso=at(2), vso=at(3)), INVALID),
     (dict(ko=at(0), vo=at(1), kso=at(2), Nout=100), INVALID),
-    (dict(B=1 << 12, Hkv=1 << 11, M=1 << 15), INVALID),
+    (dict(B=1 << 11, Hkv=1 << 11, M=1 << 15), INVALID),
 ])
 def test_compact_refuses(lib, kw, code):
     assert compact(lib, **kw) == code
