@@ -31,11 +31,11 @@ namespace cg = cooperative_groups;
 namespace fa {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kMaxNodes = 128, kMaxRanks = 8;
-constexpr int kUnroll = 16;
+constexpr int kUnroll = 8;
 constexpr int kTile = 32 * kUnroll;   // least elements of a warp's tile
-constexpr int kMaxTiles = 1024;       // tiles of a CTA's share of a row
+constexpr int kMaxTiles = 1024;       // tiles of a CTA's share of a row (32 a lane of its search)
 
 // A number as the sum of two fp32, |lo| at most half a unit of hi's last place.
 struct Pair {
@@ -114,7 +114,47 @@ __device__ __forceinline__ Pair rest(const Shared &s, int k, float p, float q, i
   return r;
 }
 
-__global__ void __launch_bounds__(kThreads, 4) fa_verify_kernel(const VerifyParams p) {
+// A node's rows, after its first k children.
+struct Node {
+  const float *p, *q;  // q: null without a draft's row
+  int k;
+};
+
+// R of kUnroll elements y0, y0 + step, ... (0 from `end` on).  All are asked for before any is used, and every address
+// is valid: a load behind a branch would wait for the one before it.
+__device__ __forceinline__ void rests(Pair (&r)[kUnroll], const Shared &s, const Node &n, int y0, int step, int end) {
+  float q[kUnroll];
+#pragma unroll
+  for (int e = 0; e < kUnroll; ++e) r[e] = Pair{__ldg(n.p + min(y0 + e * step, end - 1)), 0.0f};
+  if (n.q && n.k > 0) {
+#pragma unroll
+    for (int e = 0; e < kUnroll; ++e) q[e] = __ldg(n.q + min(y0 + e * step, end - 1));
+  }
+#pragma unroll
+  for (int e = 0; e < kUnroll; ++e)
+    if (y0 + e * step >= end || !(r[e].hi > 0.0f)) r[e].hi = 0.0f;
+  if (n.q && n.k > 0) {  // the first rejection: S is 1, and p - q a pair
+#pragma unroll
+    for (int e = 0; e < kUnroll; ++e) {
+      const Pair x = two_sum(r[e].hi, -q[e]);
+      r[e] = x.hi > 0.0f ? x : Pair{0.0f, 0.0f};
+    }
+  }
+  for (int j = n.q ? 1 : 0; j < n.k; ++j) {
+    const Pair S = s.sums[j];
+    if (n.q) {
+#pragma unroll
+      for (int e = 0; e < kUnroll; ++e) r[e] = less(r[e], S, q[e]);
+    } else {
+      const int x = s.rejected[j];
+#pragma unroll
+      for (int e = 0; e < kUnroll; ++e)
+        if (y0 + e * step == x) r[e] = less(r[e], S, 1.0f);
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 2) fa_verify_kernel(const VerifyParams p) {
   __shared__ Shared s;
   cg::cluster_group cluster = cg::this_cluster();
   const int ranks = p.ranks, rank = blockIdx.x % ranks, b = blockIdx.x / ranks;
@@ -156,31 +196,19 @@ __global__ void __launch_bounds__(kThreads, 4) fa_verify_kernel(const VerifyPara
   int node = 0, k = 0, count = 1, pass = 0;  // the node, children tried, nodes accepted, passes made
   // the sum of R after k children, of all CTAs; tile sums on the way
   auto sum_rest = [&]() {
-    const float *pr = target + node * p.tn, *qr = drafted ? draft + node * p.dn : nullptr;
+    const Node n{target + node * p.tn, drafted ? draft + node * p.dn : nullptr, k};
     Pair mine{0.0f, 0.0f};
     for (int i = warp; i < tiles; i += kWarps) {
       const int at = v0 + i * per_tile, end = min(v1, at + per_tile);
       float hi = 0.0f, lo = 0.0f;  // (the errors of the additions gathered in lo)
-      for (int y0 = at + lane; y0 < end; y0 += kTile) {
-        float pv[kUnroll], qv[kUnroll];
+      for (int y0 = at + lane; y0 - lane < end; y0 += kTile) {
+        Pair r[kUnroll];
+        rests(r, s, n, y0, 32, end);
 #pragma unroll
-        for (int j = 0; j < kUnroll; ++j) {
-          const int y = y0 + 32 * j;
-          pv[j] = y < end ? pr[y] : 0.0f;
-        }
-        if (drafted && k > 0) {
-#pragma unroll
-          for (int j = 0; j < kUnroll; ++j) {
-            const int y = y0 + 32 * j;
-            qv[j] = y < end ? qr[y] : 0.0f;
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < kUnroll; ++j) {
-          const Pair r = rest(s, k, pv[j], qv[j], y0 + 32 * j, drafted);
-          const Pair t = two_sum(hi, r.hi);
+        for (int e = 0; e < kUnroll; ++e) {
+          const Pair t = two_sum(hi, r[e].hi);
           hi = t.hi;
-          lo = __fadd_rn(lo, __fadd_rn(t.lo, r.lo));
+          lo = __fadd_rn(lo, __fadd_rn(t.lo, r[e].lo));
         }
       }
       const Pair sum = lanes_sum(two_sum(hi, lo), 32);
@@ -279,24 +307,44 @@ __global__ void __launch_bounds__(kThreads, 4) fa_verify_kernel(const VerifyPara
     int tile = find(part) * per_lane;
     part = lane < per_lane && tile + lane < tiles ? s.tile[tile + lane] : Pair{0.0f, 0.0f};
     tile += find(part);
-    // the tile's elements, likewise
-    const float *pr = target + node * p.tn, *qr = drafted ? draft + node * p.dn : nullptr;
-    auto element = [&](int y) {
-      return rest(s, k, pr[y], drafted && k > 0 ? qr[y] : 0.0f, y, drafted);
-    };
-    int at = v0 + tile * per_tile, n = min(v1, at + per_tile) - at;
-    while (n > 0) {
-      const int each = (n + 31) / 32;
-      const int lo = min(n, lane * each), hi = min(n, lo + each);
+    // the tile's elements, 256 at a time, eight a lane
+    const Node n{target + node * p.tn, drafted ? draft + node * p.dn : nullptr, k};
+    const int at = v0 + tile * per_tile, end = min(v1, at + per_tile);
+    int last = at;  // the last element with anything so far
+    for (int c = at; c < end; c += kTile) {
+      Pair r[kUnroll];
+      rests(r, s, n, c + lane * kUnroll, 1, end);
       part = Pair{0.0f, 0.0f};
-#pragma unroll 8
-      for (int y = lo; y < hi; ++y) part = add(part, element(at + y));
-      const int l = find(part);
-      at += min(n, l * each);
-      n = min(n - min(n, l * each), each);
-      if (each == 1) break;
+      int mine = -1;
+#pragma unroll
+      for (int e = 0; e < kUnroll; ++e) {
+        part = add(part, r[e]);
+        if (r[e].hi > 0.0f) mine = e;
+      }
+      const Pair upto_lane = lanes_scan(part);
+      const uint32_t some = __ballot_sync(0xffffffffu, mine >= 0);
+      const uint32_t hit = __ballot_sync(0xffffffffu, mine >= 0 && below(mark, add(run, upto_lane)));
+      if (some) {
+        const int l = 31 - __clz(some);
+        last = c + l * kUnroll + __shfl_sync(0xffffffffu, mine, l);
+      }
+      if (hit) {
+        const int l = __ffs(hit) - 1;
+        if (l > 0) run = add(run, from_lane(upto_lane, l - 1));
+        // (every lane goes through its own eight; the lane in question has the answer)
+        int found = -1;
+#pragma unroll
+        for (int e = 0; e < kUnroll; ++e) {
+          run = add(run, r[e]);
+          if (found < 0 && r[e].hi > 0.0f && below(mark, run)) found = e;
+        }
+        if (found < 0) found = mine;  // (rounding: its last one)
+        last = c + l * kUnroll + __shfl_sync(0xffffffffu, found, l);
+        break;
+      }
+      run = add(run, from_lane(upto_lane, 31));
     }
-    if (lane == 0) p.next[b] = at;
+    if (lane == 0) p.next[b] = last;
   }
   cluster.sync();  // no CTA leaves while another may write its shared memory
 }
@@ -304,8 +352,9 @@ __global__ void __launch_bounds__(kThreads, 4) fa_verify_kernel(const VerifyPara
 }  // namespace
 
 cudaError_t launch_verify(VerifyParams p, cudaStream_t stream) {
+  // CTAs of a sequence: enough to read its rows at once, but all of the batch's at work together (two an SM)
   int ranks = 1;
-  while (ranks < kMaxRanks && p.V > ranks * 2048) ranks *= 2;
+  while (ranks < kMaxRanks && p.V > ranks * 2048 && 2ll * ranks * p.B <= 2 * 152) ranks *= 2;
   p.ranks = ranks;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(p.B) * ranks);
