@@ -292,4 +292,17 @@ __device__ __forceinline__ void build_table(const P &p, int b, int base, uint32_
   __syncwarp();
 }
 
+// Keys 32 q .. 32 q + 31 of a tile whose first key is node n0 of the tree (or
+// before it) that node i sees: rows before the tree, and its bit row.
+__device__ __forceinline__ uint32_t visible(const uint32_t *bits, int i, bool live, int f) {
+  if (!live || f >= 128) return 0u;
+  if (f <= -32) return ~0u;  // rows before the tree
+  const uint32_t *r = bits + bit_row(i);
+  const int top = i >> 5;    // words 0..top; nodes past it are not seen
+  if (f < 0) return (r[0] << -f) | ((1u << -f) - 1u);
+  const int x = f >> 5;
+  const uint32_t lo = x <= top ? r[x] : 0u, hi = x + 1 <= top ? r[x + 1] : 0u;
+  return __funnelshift_r(lo, hi, f & 31);
+}
+
 }  // namespace fa

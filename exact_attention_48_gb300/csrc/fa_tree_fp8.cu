@@ -665,9 +665,8 @@ constexpr int kWholeTiles = 8;
 
 Tree8Plan plan_tree8(int B, int H, int Hkv, int Nt, int Nk, int d) {
   Tree8Plan pl{};
-  const int rows = H / Hkv * Nt, most = d == 128 ? 64 : 128;  // (rows below 2^31: H < 2^24, Nt <= 128)
-  pl.rows = 16;
-  while (pl.rows < rows && pl.rows < most) pl.rows *= 2;
+  const int rows = H / Hkv * Nt;  // (below 2^31: H < 2^24, Nt <= 128)
+  pl.rows = rows <= 16 ? 16 : (rows <= 32 ? 32 : (d == 64 && rows <= 64 ? 64 : 128));
   pl.groups = (rows + pl.rows - 1) / pl.rows;
   const int per_unit = (Nk + kKeys - 1) / kKeys;
   const long long units = static_cast<long long>(B) * Hkv;
@@ -686,7 +685,7 @@ cudaError_t launch_tree8(const CUtensorMap &tk, const CUtensorMap &tv, const Tre
                          cudaStream_t stream) {
   cudaError_t e;
   if (p.d == 128) {
-    e = launch_tree8_tc(tk, tv, p, stream);
+    e = p.rows <= 32 ? launch_tree8_tc(tk, tv, p, stream) : launch_tree8_rows(tk, tv, p, stream);
   } else {
     switch (p.rows) {
       case 16: e = launch_rows<64, 1>(tk, tv, p, stream); break;

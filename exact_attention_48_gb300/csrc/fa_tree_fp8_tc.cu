@@ -42,6 +42,7 @@
 #include <cuda_fp16.h>
 
 #include "fa_cache8.h"
+#include "fa_parts.cuh"
 #include "fa_runs.cuh"
 #include "ptx.cuh"
 
@@ -68,12 +69,6 @@ struct Roles<32> {
   static constexpr int kGroups = 3;
   static constexpr uint32_t kLaunch = 96, kSoftmax = 112, kAdd = 96, kControl = 48;
 };
-template <>
-struct Roles<64> {
-  static constexpr int kGroups = 2;
-  static constexpr uint32_t kLaunch = 128, kSoftmax = 160, kAdd = 128, kControl = 64;
-};
-
 template <int C>
 struct LayoutTc {
   using R = Roles<C>;
@@ -122,42 +117,6 @@ struct LayoutTc {
   static_assert(kOffBar % 8 == 0 && kOffRange % 8 == 0 && kOffScan % 8 == 0 && kOffMost % 16 == 0, "alignment");
   static_assert(kRequest <= 232448, "shared memory budget");
 };
-
-__device__ __forceinline__ float lg2(float x) {
-  float y;
-  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  const __half2 v = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t *>(&v);
-}
-__device__ __forceinline__ uint2 codes_to_f16(uint32_t w) {
-  uint2 r;
-  asm("{\n\t.reg .b16 lo, hi;\n\t"
-      "mov.b32 {lo, hi}, %2;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
-      : "=r"(r.x), "=r"(r.y)
-      : "r"(w));
-  return r;
-}
-// Four weights (two f16 pairs) as their two e4m3 parts.
-__device__ __forceinline__ void parts_of(uint32_t a, uint32_t b, uint32_t *hi, uint32_t *lo) {
-  asm("{\n\t.reg .b16 ha, hb, la, lb;\n\t.reg .b32 x, y;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f16x2 ha, %2;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f16x2 hb, %3;\n\t"
-      "mov.b32 %0, {ha, hb};\n\t"
-      "cvt.rn.f16x2.e4m3x2 x, ha;\n\t"
-      "cvt.rn.f16x2.e4m3x2 y, hb;\n\t"
-      "sub.rn.f16x2 x, %2, x;\n\t"
-      "sub.rn.f16x2 y, %3, y;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f16x2 la, x;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f16x2 lb, y;\n\t"
-      "mov.b32 %1, {la, lb};\n\t}"
-      : "=&r"(*hi), "=&r"(*lo)
-      : "r"(a), "r"(b));
-}
 
 // 32 lanes x 16 or 32 columns from each of two places.
 __device__ __forceinline__ void tmem_pair(uint32_t a, uint32_t b, uint32_t (&x)[16], uint32_t (&y)[16]) {
@@ -414,33 +373,16 @@ __global__ void __launch_bounds__(LayoutTc<C>::kThreads, 1)
             w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
             w[4] = z.x, w[5] = z.y, w[6] = z.z, w[7] = z.w;
           }
-          float most = 0.0f;
-#pragma unroll
-          for (int y = 0; y < 8; ++y) {
-            const float a = fabsf(__uint_as_float(w[y] << 16)), z = fabsf(__uint_as_float(w[y] & 0xffff0000u));
-            if (a <= FLT_MAX) most = fmaxf(most, a);
-            if (z <= FLT_MAX) most = fmaxf(most, z);
-          }
+          float most = greatest(w);
 #pragma unroll
           for (int o = 1; o < 8; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
           const float unit = least_scale(most), by = sign / unit;
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            float v[4] = {__uint_as_float(w[2 * y] << 16), __uint_as_float(w[2 * y] & 0xffff0000u),
-                          __uint_as_float(w[2 * y + 1] << 16), __uint_as_float(w[2 * y + 1] & 0xffff0000u)};
-#pragma unroll
-            for (int z = 0; z < 4; ++z) v[z] = fabsf(v[z]) <= FLT_MAX ? v[z] * by : NAN;
-            hi[y] = pack_e4m3x4(v[0], v[1], v[2], v[3]);
-            const uint2 h = codes_to_f16(hi[y]);
-            const float2 h0 = __half22float2(*reinterpret_cast<const __half2 *>(&h.x));
-            const float2 h1 = __half22float2(*reinterpret_cast<const __half2 *>(&h.y));
-            lo[y] = pack_e4m3x4(v[0] - h0.x, v[1] - h0.y, v[2] - h1.x, v[3] - h1.y);
-          }
+          uint4 hi, lo;
+          q_parts(w, by, &hi, &lo);
           const uint32_t at = r * kD + ((x ^ (r & 7)) * 16);
           uint8_t *to = sQ + qb * L::kQ + at;
-          *reinterpret_cast<uint4 *>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4 *>(to + C * kD) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          *reinterpret_cast<uint4 *>(to) = hi;
+          *reinterpret_cast<uint4 *>(to + C * kD) = lo;
           if (x == 0) row_f[n % L::kSegs * C + r] = unit * fabsf(p.scale_log2);
         }
         fence_proxy_async_smem();
@@ -780,11 +722,7 @@ cudaError_t launch_tc(const CUtensorMap &tk, const CUtensorMap &tv, const Tree8P
 }  // namespace
 
 cudaError_t launch_tree8_tc(const CUtensorMap &tk, const CUtensorMap &tv, const Tree8Params &p, cudaStream_t stream) {
-  switch (p.rows) {
-    case 16: return launch_tc<16>(tk, tv, p, stream);
-    case 32: return launch_tc<32>(tk, tv, p, stream);
-    default: return launch_tc<64>(tk, tv, p, stream);
-  }
+  return p.rows == 16 ? launch_tc<16>(tk, tv, p, stream) : launch_tc<32>(tk, tv, p, stream);
 }
 
 }  // namespace fa
