@@ -5,7 +5,6 @@
 
 #include <cfloat>
 #include <cstdint>
-#include <cuda_fp16.h>
 
 #include "ptx.cuh"
 
@@ -16,35 +15,25 @@ __device__ __forceinline__ float lg2(float x) {
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  const __half2 v = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t *>(&v);
-}
-__device__ __forceinline__ uint2 codes_to_f16(uint32_t w) {
-  uint2 r;
-  asm("{\n\t.reg .b16 lo, hi;\n\t"
-      "mov.b32 {lo, hi}, %2;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
-      : "=r"(r.x), "=r"(r.y)
-      : "r"(w));
-  return r;
-}
-// Four weights (two f16 pairs) as their two e4m3 parts.
-__device__ __forceinline__ void parts_of(uint32_t a, uint32_t b, uint32_t *hi, uint32_t *lo) {
-  asm("{\n\t.reg .b16 ha, hb, la, lb;\n\t.reg .b32 x, y;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f16x2 ha, %2;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f16x2 hb, %3;\n\t"
-      "mov.b32 %0, {ha, hb};\n\t"
-      "cvt.rn.f16x2.e4m3x2 x, ha;\n\t"
-      "cvt.rn.f16x2.e4m3x2 y, hb;\n\t"
-      "sub.rn.f16x2 x, %2, x;\n\t"
-      "sub.rn.f16x2 y, %3, y;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f16x2 la, x;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f16x2 lb, y;\n\t"
-      "mov.b32 %1, {la, lb};\n\t}"
-      : "=&r"(*hi), "=&r"(*lo)
-      : "r"(a), "r"(b));
+// Four values as their two e4m3 parts.  (From fp32: the conversions of f16 pairs take several instructions each.)
+__device__ __forceinline__ void parts_of(float a, float b, float c, float d, uint32_t *hi, uint32_t *lo) {
+  const uint32_t h = pack_e4m3x4(a, b, c, d);
+  float r0, r1, r2, r3;
+  asm("{\n\t.reg .b32 n, x, y;\n\t.reg .b16 l, u, a0, a1, b0, b1;\n\t"
+      "xor.b32 n, %4, 0x80808080;\n\t"
+      "mov.b32 {l, u}, n;\n\t"
+      "cvt.rn.f16x2.e4m3x2 x, l;\n\t"
+      "cvt.rn.f16x2.e4m3x2 y, u;\n\t"
+      "mov.b32 {a0, a1}, x;\n\t"
+      "mov.b32 {b0, b1}, y;\n\t"
+      "add.rn.f32.f16 %0, a0, %5;\n\t"
+      "add.rn.f32.f16 %1, a1, %6;\n\t"
+      "add.rn.f32.f16 %2, b0, %7;\n\t"
+      "add.rn.f32.f16 %3, b1, %8;\n\t}"
+      : "=&f"(r0), "=&f"(r1), "=&f"(r2), "=&f"(r3)
+      : "r"(h), "f"(a), "f"(b), "f"(c), "f"(d));
+  *hi = h;
+  *lo = pack_e4m3x4(r0, r1, r2, r3);
 }
 
 // The greatest finite magnitude of 16 bf16 values.
@@ -68,11 +57,7 @@ __device__ __forceinline__ void q_parts(const uint32_t (&w)[8], float by, uint4 
                   __uint_as_float(w[2 * y + 1] << 16), __uint_as_float(w[2 * y + 1] & 0xffff0000u)};
 #pragma unroll
     for (int x = 0; x < 4; ++x) v[x] = fabsf(v[x]) <= FLT_MAX ? v[x] * by : NAN;
-    a[y] = pack_e4m3x4(v[0], v[1], v[2], v[3]);
-    const uint2 h = codes_to_f16(a[y]);
-    const float2 h0 = __half22float2(*reinterpret_cast<const __half2 *>(&h.x));
-    const float2 h1 = __half22float2(*reinterpret_cast<const __half2 *>(&h.y));
-    z[y] = pack_e4m3x4(v[0] - h0.x, v[1] - h0.y, v[2] - h1.x, v[3] - h1.y);
+    parts_of(v[0], v[1], v[2], v[3], &a[y], &z[y]);
   }
   *hi = make_uint4(a[0], a[1], a[2], a[3]);
   *lo = make_uint4(z[0], z[1], z[2], z[3]);

@@ -453,18 +453,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool live = masked && node >= 0 && !((dead[node >> 5] >> (node & 31)) & 1u);
         // the greatest e = score + log2 r of the tile
         float m = -INFINITY;
-#pragma unroll 1
-        for (int q = 0; q < 4; ++q) {
-          uint32_t s[32];
-          tmem_ld32(tS + q * 32, s);
+        auto greatest_of = [&](const uint32_t (&s)[32], int q) {
           const float2 kq = *reinterpret_cast<const float2 *>(sc + 2 * q), lq = *reinterpret_cast<const float2 *>(sc + 8 + 2 * q);
-          tmem_ld_wait(s);
-          if (masked) {
-            const uint32_t see = visible(bits, node, live, n0 + 32 * q);
-#pragma unroll
-            for (int y = 0; y < 32; ++y)
-              if (!((see >> y) & 1u)) s[y] = 0xff800000u;  // -inf
-          }
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             float t = fmax3(__uint_as_float(s[16 * h]), __uint_as_float(s[16 * h + 1]), __uint_as_float(s[16 * h + 2]));
@@ -475,18 +465,39 @@ __global__ void __launch_bounds__(kThreads, 1)
             // (a factor of 0 times -inf is NaN, which fmaxf passes over)
             m = fmaxf(m, fmaf(t, f * (h ? kq.y : kq.x), h ? lq.y : lq.x));
           }
+        };
+        uint32_t sa[32];
+        if (masked) {  // (a loop: code that runs once a unit comes cold from memory)
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            tmem_ld32(tS + q * 32, sa);
+            const uint32_t see = visible(bits, node, live, n0 + 32 * q);
+            tmem_ld_wait(sa);
+#pragma unroll
+            for (int y = 0; y < 32; ++y)
+              if (!((see >> y) & 1u)) sa[y] = 0xff800000u;  // -inf
+            greatest_of(sa, q);
+          }
+        } else {
+          uint32_t sb[32];
+#pragma unroll 1
+          for (int q = 0; q < 4; q += 2) {
+            tmem_ld32(tS + q * 32, sa);
+            tmem_ld32(tS + q * 32 + 32, sb);
+            tmem_ld_wait(sa);
+            tmem_ld_wait(sb);
+            greatest_of(sa, q);
+            greatest_of(sb, q + 1);
+          }
         }
         const float b = kLift - (m == -INFINITY ? 0.0f : m);
         float lt = 0.0f;  // sum of the weights over r
-#pragma unroll 1
-        for (int q = 0; q < 4; ++q) {
-          uint32_t s[32];
-          tmem_ld32(tS + q * 32, s);
+        // 32 keys' weights, over scores that have been read: their two parts, 8 columns each
+        auto weights = [&](const uint32_t (&s)[32], int q, auto mask_tag) {
           const float2 kq = *reinterpret_cast<const float2 *>(sc + 2 * q), lq = *reinterpret_cast<const float2 *>(sc + 8 + 2 * q);
           const float2 iq = *reinterpret_cast<const float2 *>(sc + 16 + 2 * q);
-          const uint32_t see = masked ? visible(bits, node, live, n0 + 32 * q) : ~0u;
+          const uint32_t see = mask_tag ? visible(bits, node, live, n0 + 32 * q) : ~0u;
           uint32_t pk[16];
-          tmem_ld_wait(s);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const float g = f * (h ? kq.y : kq.x), e = (h ? lq.y : lq.x) + b;
@@ -498,18 +509,38 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float2 e0 = ffma2(make_float2(__uint_as_float(s[z]), __uint_as_float(s[z + 1])), gg, ee);
               const float2 e1 = ffma2(make_float2(__uint_as_float(s[z + 2]), __uint_as_float(s[z + 3])), gg, ee);
               float2 w0 = make_float2(ex2(e0.x), ex2(e0.y)), w1 = make_float2(ex2(e1.x), ex2(e1.y));
-              if (masked) {
+              if (mask_tag) {
                 w0.x = (see >> z) & 1u ? w0.x : 0.0f;
                 w0.y = (see >> (z + 1)) & 1u ? w0.y : 0.0f;
                 w1.x = (see >> (z + 2)) & 1u ? w1.x : 0.0f;
                 w1.y = (see >> (z + 3)) & 1u ? w1.y : 0.0f;
               }
               sum = fadd2(sum, fadd2(w0, w1));
-              parts_of(pack_f16x2(w0.x, w0.y), pack_f16x2(w1.x, w1.y), &pk[z / 4], &pk[8 + z / 4]);
+              parts_of(w0.x, w0.y, w1.x, w1.y, &pk[z / 4], &pk[8 + z / 4]);
             }
             lt = fmaf(sum.x + sum.y, h ? iq.y : iq.x, lt);
           }
-          tmem_st16(tS + q * 16, pk);  // (over scores that have been read: its two parts of 32 keys, 8 columns each)
+          tmem_st16(tS + q * 16, pk);
+        };
+        if (masked) {
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            tmem_ld32(tS + q * 32, sa);
+            tmem_ld_wait(sa);
+            weights(sa, q, MaskTag<true>{});
+          }
+        } else {  // (a loop as well: unrolled, its code does not stay in the instruction cache, 247 us for 189)
+          tmem_ld32(tS, sa);
+          tmem_ld_wait(sa);
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            uint32_t sb[32];
+            tmem_ld32(tS + (q < 3 ? q + 1 : q) * 32, sb);  // the next scores are on their way meanwhile
+            weights(sa, q, MaskTag<false>{});
+            tmem_ld_wait(sb);
+#pragma unroll
+            for (int y = 0; y < 32; ++y) sa[y] = sb[y];
+          }
         }
         tmem_st_wait();
         if (m > lm + kMoveBy) {

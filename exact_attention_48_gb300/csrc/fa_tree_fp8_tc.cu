@@ -20,8 +20,8 @@
 // Rounding.  A row of q is divided by a power of two so that its greatest value lies
 // in (224, 448]; bf16's 8 bits are 4 + 4, so its parts are exact but where the second
 // falls below e4m3's least step: off by at most 2^-10, 2^-17.8 of the row's greatest
-// value.  A weight is rounded to f16 and to its parts: off by at most 2^-8 of itself,
-// or 2^-9 of 2^8 at its tile's greatest.  Scores, maxima, sums and O are fp32.
+// value.  A weight is rounded to its parts likewise: off by at most 2^-9 of itself, or
+// 2^-10 with its tile's greatest at 2^8.  Scores, maxima, sums and O are fp32.
 //
 // What bounds it.  HBM, 2 d bytes a key, up to about 64 rows: a 128-key tile takes
 // an SM 1400 cycles of its share of the traffic, its products some 560 (a tcgen05
@@ -39,7 +39,6 @@
 
 #include <cfloat>
 #include <cstdint>
-#include <cuda_fp16.h>
 
 #include "fa_cache8.h"
 #include "fa_parts.cuh"
@@ -656,7 +655,7 @@ __global__ void __launch_bounds__(LayoutTc<C>::kThreads, 1)
             l[r + y + 1] = n0.y;
             l[r + y + 2] = n1.x;
             l[r + y + 3] = n1.y;
-            parts_of(pack_f16x2(w0, w1), pack_f16x2(w2, w3), &hi[y / 4], &lo[y / 4]);
+            parts_of(w0, w1, w2, w3, &hi[y / 4], &lo[y / 4]);
           }
           *reinterpret_cast<uint4 *>(prow + (((r / 16) ^ (key & 7)) * 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
           *reinterpret_cast<uint4 *>(prow + (((r / 16 + C / 16) ^ (key & 7)) * 16)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
