@@ -13,10 +13,11 @@
 // each, 1440 cycles of a tile of 128 keys and 128 rows, as many as its share of the
 // HBM traffic takes (1400).  A softmax takes a warp some 700 instructions.
 //
-// CTA (512 threads): warps 0..3 and 4..7 softmax, a row per thread, alternate tiles;
-// warps 8..11 q's parts and O added up in registers, a row per thread; warp 12 TMA
-// producer, warp 13 issues S and owns TMEM, warp 14 issues O, warp 15 the tree's
-// table.  TMEM: three S of 128 columns (S of tile x + 2 is formed while tile x's
+// CTA (640 threads): warps 0..3 and 4..7 softmax, a row per thread, alternate tiles;
+// warps 8..11 and 12..15 add up O in registers, half a row per thread (one warpgroup
+// alone held the next product up: 182 us for B2 H32 Hkv8 Nt64 Nk65536), the first of
+// them brings q's parts; warp 16 TMA producer, warp 17 issues S and owns TMEM, warp 18
+// issues O, warp 19 the tree's table.  TMEM: three S of 128 columns (S of tile x + 2 is formed while tile x's
 // weights, over its S, still wait for their product) and O.  The tiles of all units
 // form one list that is cut into equal runs (fa_runs.cuh), and a CTA's products run on
 // from unit to unit.
@@ -32,14 +33,14 @@ namespace fa {
 namespace {
 
 constexpr int kD = 128, kRows = 128;
-constexpr int kThreads = 512;
-constexpr int kWarpAdd = 8, kWarpProducer = 12, kWarpS = 13, kWarpO = 14, kWarpMask = 15;
+constexpr int kThreads = 640;
+constexpr int kWarpAdd = 8, kWarpProducer = 16, kWarpS = 17, kWarpO = 18, kWarpMask = 19;
 constexpr float kMoveBy = 8.0f;   // a running maximum moves only when exceeded by more (log2 units)
 constexpr float kLift = 8.0f;     // weights reach 2^kLift
 constexpr float kLn2 = 0.69314718055994530942f;
-// Register split: 512 threads launched with 128 each; the rows' O takes 128 of a thread.
-constexpr uint32_t kRegsSoftmax = 128, kRegsAdd = 192, kRegsControl = 64;
-static_assert(256 * kRegsSoftmax + 128 * kRegsAdd + 128 * kRegsControl <= kThreads * 128, "register split");
+// Register split: 640 threads launched with 96 each.
+constexpr uint32_t kRegsSoftmax = 104, kRegsAdd = 104, kRegsControl = 64;
+static_assert(256 * kRegsSoftmax + 256 * kRegsAdd + 128 * kRegsControl <= kThreads * 96, "register split");
 
 struct LayoutRows {
   static constexpr uint32_t kTile = kKeys * kD;        // a K or V tile, or one part of q: 16 KB
@@ -54,8 +55,8 @@ struct LayoutRows {
   static constexpr uint32_t kOffDead = kOffBits + 32 * (1 + 2 + 3 + 4) * 4;
   static constexpr uint32_t kOffJump = kOffDead + 16;
   static constexpr uint32_t kOffRange = kOffJump + 128;
-  static constexpr uint32_t kOffScan = kOffRange + 48;             // 16 warps' sums
-  static constexpr uint32_t kOffScale = kOffScan + 16 * 8;         // [8 warps][3][8]: a tile's scales
+  static constexpr uint32_t kOffScan = kOffRange + 48;             // 20 warps' sums
+  static constexpr uint32_t kOffScale = kOffScan + 20 * 8;         // [8 warps][3][8]: a tile's scales
   static constexpr uint32_t kOffTileM = kOffScale + 8 * 24 * 4;    // [4 tiles][128] m, and [4] the greatest vs
   static constexpr uint32_t kOffTileV = kOffTileM + 4 * kRows * 4;
   static constexpr uint32_t kOffL = kOffTileV + 16;                // [2][128] l, [2][128] its base
@@ -124,11 +125,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&drain[i], 1);
     }
     mbar_init(pv_done, 1);
-    mbar_init(o_empty, warps);
+    mbar_init(o_empty, 2 * warps);
     mbar_init(mask_full, 1);
-    mbar_init(mask_empty, 3 * warps);
+    mbar_init(mask_empty, 4 * warps);
     mbar_init(l_full, 2 * warps);
-    mbar_init(l_empty, warps);
+    mbar_init(l_empty, 2 * warps);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -287,32 +288,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     // (no rows: q's rows here stay what they are, and only rows that nothing reads come of them)
     regs_increase<kRegsAdd>();
   } else if (warp >= kWarpAdd) {
-    // ------------------------------------------------------------ q's parts; O added up, a row per thread
+    // ------------------------------------------------------------ O added up, half a row per thread; q's parts
     regs_increase<kRegsAdd>();
     const int r = (warp & 3) * 32 + lane, row = first_row + r;
+    const bool first = warp < kWarpAdd + 4;
+    const int c0 = first ? 0 : kD / 2;
     const bool used = r < rows;
     const int node = used ? row % p.Nt : -1, gh = used ? row / p.Nt : 0;
     // q of segment `seg`, into the buffer of the segment before the last one (whose products are all done: this
     // thread has seen their sums)
     auto load_q = [&](const Walk<Tree8Params> &w, uint32_t seg) {
-      uint32_t v[8][8];
+      // (read twice, the second time from a cache: held, a row would take 64 registers)
       const uint4 *src = reinterpret_cast<const uint4 *>(p.q + w.b * p.sq.b + (w.hk * p.G + gh) * p.sq.h +
                                                          (used ? node : 0) * p.sq.n);
-      float most = 0.0f;
-#pragma unroll
-      for (int x = 0; x < 8; ++x) {
+      auto piece = [&](int x, uint32_t (&v)[8]) {
         const uint4 a = used ? src[2 * x] : make_uint4(0u, 0u, 0u, 0u), z = used ? src[2 * x + 1] : make_uint4(0u, 0u, 0u, 0u);
-        v[x][0] = a.x, v[x][1] = a.y, v[x][2] = a.z, v[x][3] = a.w;
-        v[x][4] = z.x, v[x][5] = z.y, v[x][6] = z.z, v[x][7] = z.w;
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+        v[4] = z.x, v[5] = z.y, v[6] = z.z, v[7] = z.w;
+      };
+      float most = 0.0f;
+#pragma unroll 4
+      for (int x = 0; x < 8; ++x) {
+        uint32_t v[8];
+        piece(x, v);
+        most = fmaxf(most, greatest(v));
       }
-#pragma unroll
-      for (int x = 0; x < 8; ++x) most = fmaxf(most, greatest(v[x]));
       const float unit = least_scale(most), by = (p.scale_log2 < 0.0f ? -1.0f : 1.0f) / unit;
       uint8_t *to = sQ + (seg & 1) * L::kQ + r * kD;
-#pragma unroll
+#pragma unroll 2
       for (int x = 0; x < 8; ++x) {
+        uint32_t v[8];
+        piece(x, v);
         uint4 hi, lo;
-        q_parts(v[x], by, &hi, &lo);
+        q_parts(v, by, &hi, &lo);
         *reinterpret_cast<uint4 *>(to + ((x ^ (r & 7)) * 16)) = hi;
         *reinterpret_cast<uint4 *>(to + L::kTile + ((x ^ (r & 7)) * 16)) = lo;
       }
@@ -321,8 +329,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       warp_arrive(&q_full[seg & 1]);
     };
     Walk<Tree8Params> wn(p, *run);  // a segment ahead
-    bool more = wn.next();
-    load_q(wn, 0);
+    bool more = first && wn.next();
+    if (first) load_q(wn, 0);
     uint32_t x = 0, seg = 0, nmask = 0;
     bool ok = true;
     while (wk.next()) {
@@ -331,9 +339,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             wk.tail ? make_int4(-1, 0, 0, 0)
                     : make_int4(wk.b, wk.hk, c, static_cast<int>(divide((wk.u0 + wk.tiles) * run->runs - 1, run->total)));
       if (more && (more = wn.next())) load_q(wn, seg + 1);
-      float o[kD];
+      float o[kD / 2];
 #pragma unroll
-      for (int y = 0; y < kD; ++y) o[y] = 0.0f;
+      for (int y = 0; y < kD / 2; ++y) o[y] = 0.0f;
       float M = -INFINITY;
       for (int kt = wk.k0; ok && kt < wk.k1; ++kt, ++x) {
         if (!(ok = __all_sync(0xffffffffu, mbar_wait(pv_done, x & 1, ctl, kSitePvDone)))) break;
@@ -344,22 +352,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float a = move ? ex2(M - m) : 1.0f;  // (0 at first)
           if (move) M = m;
 #pragma unroll
-          for (int y = 0; y < kD; ++y) o[y] *= a;
+          for (int y = 0; y < kD / 2; ++y) o[y] *= a;
         }
         const float f = m == -INFINITY ? 0.0f : ex2(m - M) * vs;
         const float2 ff = make_float2(f, f);
+        const uint32_t tO = tmem + L::kO + lane_base + c0;
+        auto gather = [&](const uint32_t (&w)[16], int q) {
 #pragma unroll
-        for (int q = 0; q < kD; q += 32) {
-          uint32_t w[32];
-          tmem_ld32(tmem + L::kO + lane_base + q, w);
-          tmem_ld_wait(w);
-#pragma unroll
-          for (int y = 0; y < 32; y += 2) {
+          for (int y = 0; y < 16; y += 2) {
             const float2 n = ffma2(make_float2(__uint_as_float(w[y]), __uint_as_float(w[y + 1])), ff,
                                    make_float2(o[q + y], o[q + y + 1]));
             o[q + y] = n.x;
             o[q + y + 1] = n.y;
           }
+        };
+#pragma unroll
+        for (int q = 0; q < kD / 2; q += 32) {
+          uint32_t wa[16], wb[16];
+          tmem_ld16(tO + q, wa);
+          tmem_ld16(tO + q + 16, wb);
+          tmem_ld_wait16(wa);
+          tmem_ld_wait16(wb);
+          gather(wa, q);
+          gather(wb, q + 16);
         }
         tc_fence_before();
         warp_arrive(o_empty);
@@ -380,20 +395,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float lse2 = any ? (M == -INFINITY ? 0.0f : M) - kLift + log2f(l) : -INFINITY;
         const int h = wk.hk * p.G + gh;
         if (wk.whole()) {
-          p.lse[(static_cast<long long>(wk.b) * p.H + h) * p.Nt + node] = any ? lse2 * kLn2 : -INFINITY;
-          uint4 *dst = reinterpret_cast<uint4 *>(p.o + wk.b * p.so.b + h * p.so.h + node * p.so.n);
+          if (first) p.lse[(static_cast<long long>(wk.b) * p.H + h) * p.Nt + node] = any ? lse2 * kLn2 : -INFINITY;
+          uint4 *dst = reinterpret_cast<uint4 *>(p.o + wk.b * p.so.b + h * p.so.h + node * p.so.n + c0);
 #pragma unroll
-          for (int y = 0; y < kD; y += 8)
+          for (int y = 0; y < kD / 2; y += 8)
             dst[y / 8] = any ? make_uint4(pack_bf16x2(o[y] * inv, o[y + 1] * inv), pack_bf16x2(o[y + 2] * inv, o[y + 3] * inv),
                                           pack_bf16x2(o[y + 4] * inv, o[y + 5] * inv),
                                           pack_bf16x2(o[y + 6] * inv, o[y + 7] * inv))
                              : make_uint4(0u, 0u, 0u, 0u);
         } else {
           const long long at = (static_cast<long long>(blockIdx.x) * 2 + (wk.k0 == 0 ? 1 : 0)) * kRows + r;
-          p.part_lse[at] = padding ? INFINITY : lse2;
-          float4 *dst = reinterpret_cast<float4 *>(p.part_o + at * kD);
+          if (first) p.part_lse[at] = padding ? INFINITY : lse2;
+          float4 *dst = reinterpret_cast<float4 *>(p.part_o + at * kD + c0);
 #pragma unroll
-          for (int y = 0; y < kD; y += 4)
+          for (int y = 0; y < kD / 2; y += 4)
             dst[y / 4] = any ? make_float4(o[y] * inv, o[y + 1] * inv, o[y + 2] * inv, o[y + 3] * inv)
                              : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         }
@@ -405,8 +420,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ++seg;
     }
-  } else if ((warp & 3) < warps) {
+  } else if ((warp & 3) >= warps) {
+    regs_increase<kRegsSoftmax>();
+  } else {
     // ------------------------------------------------------------ softmax, a row per thread
+    regs_increase<kRegsSoftmax>();
     const int wg = warp >> 2, r = (warp & 3) * 32 + lane;
     const int node = r < rows ? (first_row + r) % p.Nt : -1;
     float *sc = floats(L::kOffScale) + warp * 24;  // [3][8]: K's scales, log2 of V's over the greatest, its inverse
@@ -479,15 +497,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             greatest_of(sa, q);
           }
         } else {
-          uint32_t sb[32];
 #pragma unroll 1
-          for (int q = 0; q < 4; q += 2) {
+          for (int q = 0; q < 4; ++q) {
             tmem_ld32(tS + q * 32, sa);
-            tmem_ld32(tS + q * 32 + 32, sb);
             tmem_ld_wait(sa);
-            tmem_ld_wait(sb);
             greatest_of(sa, q);
-            greatest_of(sb, q + 1);
           }
         }
         const float b = kLift - (m == -INFINITY ? 0.0f : m);
@@ -530,16 +544,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             weights(sa, q, MaskTag<true>{});
           }
         } else {  // (a loop as well: unrolled, its code does not stay in the instruction cache, 247 us for 189)
-          tmem_ld32(tS, sa);
-          tmem_ld_wait(sa);
 #pragma unroll 1
           for (int q = 0; q < 4; ++q) {
-            uint32_t sb[32];
-            tmem_ld32(tS + (q < 3 ? q + 1 : q) * 32, sb);  // the next scores are on their way meanwhile
+            tmem_ld32(tS + q * 32, sa);
+            tmem_ld_wait(sa);
             weights(sa, q, MaskTag<false>{});
-            tmem_ld_wait(sb);
-#pragma unroll
-            for (int y = 0; y < 32; ++y) sa[y] = sb[y];
           }
         }
         tmem_st_wait();
