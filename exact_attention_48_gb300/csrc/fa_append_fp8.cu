@@ -11,8 +11,9 @@
 // read in bf16 and written in 8 bits.  A CTA takes the tokens of one block of
 // rows and walks heads: the tokens' angles are computed once, into shared memory,
 // and a head's rows stay in registers between the search for their greatest value
-// and the rounding, so nothing is read twice; the next head's rows are on their way
-// meanwhile.  Two pieces of 8 values are a thread's share of a head, so that a CTA has
+// and the rounding, so nothing is read twice; the next three heads' rows are on their
+// way meanwhile, copied asynchronously to places in shared memory that each thread
+// has for itself (one head ahead in registers: B4 H32 Hkv8 N4001 d128 104 us).  Two pieces of 8 values are a thread's share of a head, so that a CTA has
 // 256 to 1024 threads by the tokens in a block; with few tokens several heads share
 // the CTA and the heads are cut across CTAs.
 
@@ -28,6 +29,12 @@ namespace {
 
 __device__ __forceinline__ long long floor_shift(long long x, int s) { return x >> s; }  // (arithmetic: floors)
 
+constexpr int kAhead = 3;  // heads on their way
+
+__device__ __forceinline__ void copy16(void *dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+
 // A value as e4m3 stores it: infinities become NaN (the conversion would
 // saturate them).
 __device__ __forceinline__ float storable(float x) { return fabsf(x) <= FLT_MAX ? x : NAN; }
@@ -36,7 +43,7 @@ __device__ __forceinline__ float storable(float x) { return fabsf(x) <= FLT_MAX 
 // slots * d / 16 threads, all of the CTA's or a part.
 template <bool INTERLEAVED, int kThreads>
 __global__ void __launch_bounds__(kThreads, 1024 / kThreads) fa_append_fp8_kernel(const Append8Params p) {
-  extern __shared__ float table[];  // cos, then sin: [slots][rot / 2]
+  extern __shared__ float4 shared[];  // rows on their way [kAhead][2][threads], then cos and sin [slots][rot / 2]
   __shared__ uint32_t most[3][kThreads / 4];  // greatest values of the heads at work, used in turn
   const int per_row = p.d >> 4, half = p.rot >> 1, tid = threadIdx.x;
   const int lanes = per_row * p.slots;
@@ -54,50 +61,55 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) fa_append_fp8_kerne
   const bool has_old = start > lo && start > 0 && any_row;
   const int blk = any_row ? static_cast<int>(lo >> p.block_log2) : 0;
 
-  for (int i = tid; i < 3 * (kThreads / 4); i += kThreads) most[i / (kThreads / 4)][i % (kThreads / 4)] = 0u;
-  float *cos_t = table, *sin_t = table + p.slots * half;
-  for (int e = tid; e < count * half; e += kThreads) {
-    const int s = e / half, i = e - s * half;
-    const long long pos = p.positions ? p.positions[b * p.pos_b + n0 + s] : from + s;
-    float cs, sn;
-    angle_of(pos, p.inv_freq[i], &cs, &sn);
-    cos_t[e] = cs * p.factor;
-    sin_t[e] = sn * p.factor;
-  }
-  __syncthreads();
-
+  float *cos_t = reinterpret_cast<float *>(shared + kAhead * 2 * kThreads), *sin_t = cos_t + p.slots * half;
   const int hl = tid / lanes, in_head = tid - hl * lanes;
   const int c = in_head & (per_row - 1), slot = in_head / per_row;
   const Pieces x = pieces_of<INTERLEAVED>(p.d, p.rot, c);
   const int heads = p.H + 2 * p.Hkv, step = heads_at_once * gridDim.y;
   const bool row_on = slot < count && from + slot >= 0 && from + slot < p.Nk;  // has a row of the cache
-  const float *cs = cos_t + slot * half, *sn = sin_t + slot * half;
-  // the rows of the head that this thread takes from h0 on, and its block's scale if rows before these use it
-  uint4 w0, w1;
-  float old = 0.0f;
-  auto load = [&](int h0) {
+  // the rows of the head that this thread takes from h0 on
+  auto ask = [&](int h0, int place) {
     const int hh = h0 + hl;
     const bool is_q = hh < p.H, is_k = !is_q && hh < p.H + p.Hkv;
-    if (hl >= heads_at_once || hh >= heads || slot >= count || !(is_q || row_on)) return;
-    const int h = is_q ? hh : (is_k ? hh - p.H : hh - p.H - p.Hkv);
-    const __nv_bfloat16 *row = is_q   ? p.q + b * p.sq.b + h * p.sq.h + (n0 + slot) * p.sq.n
-                               : is_k ? p.k + b * p.sk.b + h * p.sk.h + (n0 + slot) * p.sk.n
-                                      : p.v + b * p.sv.b + h * p.sv.h + (n0 + slot) * p.sv.n;
-    w0 = __ldcs(reinterpret_cast<const uint4 *>(row + x.c0));
-    w1 = __ldcs(reinterpret_cast<const uint4 *>(row + x.c1));
+    if (hh < heads && slot < count && (is_q || row_on)) {
+      const int h = is_q ? hh : (is_k ? hh - p.H : hh - p.H - p.Hkv);
+      const __nv_bfloat16 *row = is_q   ? p.q + b * p.sq.b + h * p.sq.h + (n0 + slot) * p.sq.n
+                                 : is_k ? p.k + b * p.sk.b + h * p.sk.h + (n0 + slot) * p.sk.n
+                                        : p.v + b * p.sv.b + h * p.sv.h + (n0 + slot) * p.sv.n;
+      float4 *to = shared + place * 2 * kThreads + tid;
+      copy16(to, row + x.c0);
+      copy16(to + kThreads, row + x.c1);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  int turn = 0;
-  load(blockIdx.y * heads_at_once);
-  for (int h0 = blockIdx.y * heads_at_once; h0 < heads; h0 += step) {
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) ask(blockIdx.y * heads_at_once + i * step, i);
+
+  for (int i = tid; i < 3 * (kThreads / 4); i += kThreads) most[i / (kThreads / 4)][i % (kThreads / 4)] = 0u;
+  for (int e = tid; e < count * half; e += kThreads) {
+    const int s = e / half, i = e - s * half;
+    const long long pos = p.positions ? p.positions[b * p.pos_b + n0 + s] : from + s;
+    float cs_e, sn_e;
+    angle_of(pos, p.inv_freq[i], &cs_e, &sn_e);
+    cos_t[e] = cs_e * p.factor;
+    sin_t[e] = sn_e * p.factor;
+  }
+  __syncthreads();
+  int turn = 0, place = 0;
+  for (int h0 = blockIdx.y * heads_at_once; h0 < heads; h0 += step, place = place == kAhead - 1 ? 0 : place + 1) {
     const int hh = h0 + hl;
     const bool is_q = hh < p.H, is_k = !is_q && hh < p.H + p.Hkv;
-    const bool head_on = hl < heads_at_once && hh < heads && (is_q || any_row);
+    const bool head_on = hh < heads && (is_q || any_row);
     const bool on = head_on && slot < count && (is_q || row_on);
     const int h = is_q ? hh : (is_k ? hh - p.H : hh - p.H - p.Hkv);
     float *scale = (is_k ? p.ks : p.vs) + (static_cast<long long>(b) * p.Hkv + h) * p.blocks + blk;
-    old = head_on && !is_q && has_old ? *scale : 0.0f;
+    // the block's scale, if rows before these use it
+    const float old = head_on && !is_q && has_old ? *scale : 0.0f;
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+    const uint4 *mine = reinterpret_cast<const uint4 *>(shared + place * 2 * kThreads + tid);
+    const uint4 w0 = mine[0], w1 = mine[kThreads];  // (what this thread asked for itself)
     const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-    if (h0 + step < heads) load(h0 + step);
+    ask(h0 + kAhead * step, place);
     float y[16];
     float top = 0.0f;
     if (on) {
@@ -108,22 +120,29 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) fa_append_fp8_kerne
         y[2 * i + 1] = v.y;
       }
       if (is_q || is_k) {
+        // (whole quadruples: single values would meet in the same banks)
+        float cs[8], sn[8];
+#pragma unroll
+        for (int i = 0; i < 8; i += 4) {
+          const int at = slot * half + ((i ? x.t1 : x.t0) ? (i ? x.p1 : x.p0) : 0);  // (pieces past rot have no angles)
+          const float4 u = *reinterpret_cast<const float4 *>(cos_t + at), v = *reinterpret_cast<const float4 *>(sin_t + at);
+          cs[i] = u.x, cs[i + 1] = u.y, cs[i + 2] = u.z, cs[i + 3] = u.w;
+          sn[i] = v.x, sn[i + 1] = v.y, sn[i + 2] = v.z, sn[i + 3] = v.w;
+        }
         if (INTERLEAVED) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             if (!(i < 4 ? x.t0 : x.t1)) continue;
-            const int pr = i < 4 ? x.p0 + i : x.p1 + i - 4;
             const float a = y[2 * i], z = y[2 * i + 1];
-            y[2 * i] = a * cs[pr] - z * sn[pr];
-            y[2 * i + 1] = z * cs[pr] + a * sn[pr];
+            y[2 * i] = a * cs[i] - z * sn[i];
+            y[2 * i + 1] = z * cs[i] + a * sn[i];
           }
         } else if (x.t0) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const int pr = i < 4 ? x.p0 + i : x.p1 + i - 4;
             const float a = y[i], z = y[8 + i];
-            y[i] = a * cs[pr] - z * sn[pr];
-            y[8 + i] = z * cs[pr] + a * sn[pr];
+            y[i] = a * cs[i] - z * sn[i];
+            y[8 + i] = z * cs[i] + a * sn[i];
           }
         }
       }
@@ -184,8 +203,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) fa_append_fp8_kerne
 template <bool INTERLEAVED, int kThreads>
 cudaError_t launch_append8_t(const Append8Params &p, cudaStream_t stream) {
   auto kern = fa_append_fp8_kernel<INTERLEAVED, kThreads>;
-  const size_t smem = sizeof(float) * p.slots * p.rot;  // up to 64 KB
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 65536);
+  const size_t smem = kAhead * 2 * kThreads * 16 + sizeof(float) * p.slots * p.rot;  // up to 96 + 64 KB
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             kAhead * 2 * kThreads * 16 + 65536);
   if (e != cudaSuccess) return e;
   kern<<<dim3(static_cast<unsigned>(p.B) * p.per_b, p.head_groups), kThreads, smem, stream>>>(p);
   return cudaGetLastError();

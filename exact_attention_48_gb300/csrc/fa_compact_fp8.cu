@@ -122,7 +122,7 @@ __device__ __forceinline__ long long first_window(long long base) { return base 
 // (K and V of a window in one CTA, 108 registers and two CTAs an SM: B16 Hkv16
 // 16384 to 8192 rows d128 324 us.)
 template <int D>
-__global__ void __launch_bounds__(kThreads, 5) fa_compact_fp8_gather_kernel(const Compact8Params p, int windows) {
+__global__ void __launch_bounds__(kThreads, 6) fa_compact_fp8_gather_kernel(const Compact8Params p, int windows) {
   __shared__ uint32_t most[8], moved[8];
   const int x = blockIdx.x >> 1, bh = x / windows, b = bh / p.Hkv, h = bh - b * p.Hkv;
   const long long base = p.base ? p.base[b] : 0;
