@@ -66,7 +66,7 @@ struct Append8Params {
   int block_log2, blocks;
   int per_b;                  // blocks of rows that the N tokens of a sequence may touch
   int slots;                  // tokens of a CTA: min(N, rows of a block) rounded up to a power of two
-  int head_groups;
+  int q_groups, kv_groups;    // CTAs along the heads of q, of k and of v
 };
 cudaError_t launch_append8(bool interleaved, const Append8Params &p, cudaStream_t stream);
 
