@@ -63,4 +63,15 @@ __device__ __forceinline__ void q_parts(const uint32_t (&w)[8], float by, uint4 
   *lo = make_uint4(z[0], z[1], z[2], z[3]);
 }
 
+// Tiles of rows of D codes, as TMA leaves them: where 16-byte piece x of row r lies, and the
+// descriptor of one (K-major, or MN-major with slabs of D columns `lbo` bytes apart).
+template <int D>
+__device__ __forceinline__ uint32_t piece_at(int r, int x) {
+  return r * D + (D == 128 ? (x ^ (r & 7)) : (x ^ ((r >> 1) & 3))) * 16;
+}
+template <int D>
+__device__ __forceinline__ uint64_t sdesc_codes(const void *tile, uint32_t lbo = 16) {
+  return D == 128 ? sdesc_sw128(smem_addr(tile), lbo, 1024) : sdesc_sw64(smem_addr(tile), lbo, 512);
+}
+
 }  // namespace fa

@@ -1,6 +1,6 @@
 // fa_tree_fp8_rows.cu -- attention of the newest rows of each sequence, or of a
-// tree of drafted tokens, over a cache held in 8 bits: d = 128 and more than 16
-// query rows of a cache head, on tcgen05's 8-bit form.
+// tree of drafted tokens, over a cache held in 8 bits, more than 32 query rows of a
+// cache head, on tcgen05's 8-bit form.
 //
 // The mathematics and the rounding are those of fa_tree_fp8_tc.cu (q and the
 // weights as two e4m3 parts, weights relative to their own tile's greatest, a fresh O
@@ -9,9 +9,11 @@
 // the transposed form takes them over lanes and warps (64 rows 3300 cycles a tile
 // there); up to 128 rows cost the same.
 //
-// What bounds it.  The products: 16 instructions of 128 x 128 x 32 a tile, 90 cycles
-// each, 1440 cycles of a tile of 128 keys and 128 rows, as many as its share of the
-// HBM traffic takes (1400).  A softmax takes a warp some 700 instructions.
+// What bounds it.  The products at d = 128: 16 instructions of 128 x 128 x 32 a tile, 90
+// cycles each, 1440 cycles of a tile of 128 keys and 128 rows, as many as its share of
+// the HBM traffic takes (1400).  A softmax takes a warp some 700 instructions.
+// B2 H32 Hkv8 Nt64 Nk65536 (two CTAs a tile of 128 rows each): 157 us, 2100 cycles a
+// tile, the way from a tile's O to the next one's start.  d = 64: 130 us.
 //
 // CTA (640 threads): warps 0..3 and 4..7 softmax, a row per thread, alternate tiles;
 // warps 8..11 and 12..15 add up O in registers, half a row per thread (one warpgroup
@@ -32,7 +34,7 @@
 namespace fa {
 namespace {
 
-constexpr int kD = 128, kRows = 128;
+constexpr int kRows = 128;
 constexpr int kThreads = 640;
 constexpr int kWarpAdd = 8, kWarpProducer = 16, kWarpS = 17, kWarpO = 18, kWarpMask = 19;
 constexpr float kMoveBy = 8.0f;   // a running maximum moves only when exceeded by more (log2 units)
@@ -42,9 +44,10 @@ constexpr float kLn2 = 0.69314718055994530942f;
 constexpr uint32_t kRegsSoftmax = 104, kRegsAdd = 104, kRegsControl = 64;
 static_assert(256 * kRegsSoftmax + 256 * kRegsAdd + 128 * kRegsControl <= kThreads * 96, "register split");
 
+template <int D>
 struct LayoutRows {
-  static constexpr uint32_t kTile = kKeys * kD;        // a K or V tile, or one part of q: 16 KB
-  static constexpr int kSlotsK = 4, kSlotsV = 5;
+  static constexpr uint32_t kTile = kKeys * D;         // a K or V tile, or one part of q
+  static constexpr int kSlotsK = D == 128 ? 4 : 8, kSlotsV = kSlotsK + 1;
   // V tiles are asked for kLag tiles after their K (S runs about so far ahead of O).
   static constexpr int kLag = 2;
   static constexpr int kBufs = 3;                      // of S
@@ -73,10 +76,11 @@ struct LayoutRows {
   static_assert(kRequest <= 232448, "shared memory budget");
 };
 
+template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     fa_tree_fp8_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                             const Tree8Params p) {
-  using L = LayoutRows;
+  using L = LayoutRows<D>;
   constexpr int SK = L::kSlotsK, SV = L::kSlotsV, NB = L::kBufs, kLag = L::kLag;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *small = smem_raw;
@@ -211,7 +215,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kWarpS && lane == 0) {
       // ---------------------------------------------------------- S = Q K^T
       constexpr uint32_t kIdS = idesc_e4m3(kRows, kKeys, false, false);
-      const uint64_t dQ = sdesc_sw128(smem_addr(sQ), 16, 1024), dT = sdesc_sw128(smem_addr(ring), 16, 1024);
+      constexpr int kSteps = D / 32;
+      const uint64_t dQ = sdesc_codes<D>(sQ), dT = sdesc_codes<D>(ring);
       uint32_t seg = 0, sl = 0, sph = 0, buf = 0, bph = 1;  // segment, K's slot and its phase, S's buffer and its phase
       bool ok = true;
       while (ok && wk.next()) {
@@ -224,9 +229,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           const uint64_t dk = desc_add(dT, sl * L::kTile);
 #pragma unroll
-          for (int kk = 0; kk < 2 * kD / 32; ++kk)  // both parts of q, one after the other
-            mma_ss_f8(tmem + buf * 128, desc_add(dq, (kk >> 2) * L::kTile + (kk & 3) * 32), desc_add(dk, (kk & 3) * 32),
-                      kIdS, kk > 0 ? 1u : 0u);
+          for (int kk = 0; kk < 2 * kSteps; ++kk)  // both parts of q, one after the other
+            mma_ss_f8(tmem + buf * 128, desc_add(dq, kk / kSteps * L::kTile + kk % kSteps * 32),
+                      desc_add(dk, kk % kSteps * 32), kIdS, kk > 0 ? 1u : 0u);
           tc_commit(&s_full[buf]);
           tc_commit(&k_empty[sl]);
           if (++sl == SK) {
@@ -243,8 +248,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_drain(&drain[0], 0);
     } else if (warp == kWarpO && lane == 0) {
       // ---------------------------------------------------------- O = P V
-      constexpr uint32_t kIdO = idesc_e4m3(kRows, kD, false, true);
-      const uint64_t dT = sdesc_sw128(smem_addr(ring_v), 16, 1024);
+      constexpr uint32_t kIdO = idesc_e4m3(kRows, D, false, true);
+      const uint64_t dT = sdesc_codes<D>(ring_v);
       const uint32_t total = static_cast<uint32_t>(wk.end - wk.t);
       uint32_t sl = 0, sph = 0, buf = 0, bph = 0;  // V's slot and its phase, the weights' buffer and its phase
       for (uint32_t y = 0; y < total; ++y) {
@@ -256,8 +261,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t tp = tmem + buf * 128;
 #pragma unroll
         for (int kk = 0; kk < kKeys / 32; ++kk) {
-          mma_ts_f8(tmem + L::kO, tp + kk * 16, desc_add(dv, kk * 4096), kIdO, kk > 0 ? 1u : 0u);
-          mma_ts_f8(tmem + L::kO, tp + kk * 16 + 8, desc_add(dv, kk * 4096), kIdO, 1u);
+          mma_ts_f8(tmem + L::kO, tp + kk * 16, desc_add(dv, kk * 32 * D), kIdO, kk > 0 ? 1u : 0u);
+          mma_ts_f8(tmem + L::kO, tp + kk * 16 + 8, desc_add(dv, kk * 32 * D), kIdO, 1u);
         }
         tc_commit(pv_done);
         tc_commit(&s_free[buf]);
@@ -292,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     regs_increase<kRegsAdd>();
     const int r = (warp & 3) * 32 + lane, row = first_row + r;
     const bool first = warp < kWarpAdd + 4;
-    const int c0 = first ? 0 : kD / 2;
+    const int c0 = first ? 0 : D / 2;
     const bool used = r < rows;
     const int node = used ? row % p.Nt : -1, gh = used ? row / p.Nt : 0;
     // q of segment `seg`, into the buffer of the segment before the last one (whose products are all done: this
@@ -308,21 +313,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       float most = 0.0f;
 #pragma unroll 4
-      for (int x = 0; x < 8; ++x) {
+      for (int x = 0; x < D / 16; ++x) {
         uint32_t v[8];
         piece(x, v);
         most = fmaxf(most, greatest(v));
       }
       const float unit = least_scale(most), by = (p.scale_log2 < 0.0f ? -1.0f : 1.0f) / unit;
-      uint8_t *to = sQ + (seg & 1) * L::kQ + r * kD;
+      uint8_t *to = sQ + (seg & 1) * L::kQ;
 #pragma unroll 2
-      for (int x = 0; x < 8; ++x) {
+      for (int x = 0; x < D / 16; ++x) {
         uint32_t v[8];
         piece(x, v);
         uint4 hi, lo;
         q_parts(v, by, &hi, &lo);
-        *reinterpret_cast<uint4 *>(to + ((x ^ (r & 7)) * 16)) = hi;
-        *reinterpret_cast<uint4 *>(to + L::kTile + ((x ^ (r & 7)) * 16)) = lo;
+        *reinterpret_cast<uint4 *>(to + piece_at<D>(r, x)) = hi;
+        *reinterpret_cast<uint4 *>(to + L::kTile + piece_at<D>(r, x)) = lo;
       }
       row_f[seg % 3 * kRows + r] = unit * fabsf(p.scale_log2);
       fence_proxy_async_smem();
@@ -339,9 +344,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             wk.tail ? make_int4(-1, 0, 0, 0)
                     : make_int4(wk.b, wk.hk, c, static_cast<int>(divide((wk.u0 + wk.tiles) * run->runs - 1, run->total)));
       if (more && (more = wn.next())) load_q(wn, seg + 1);
-      float o[kD / 2];
+      float o[D / 2];
 #pragma unroll
-      for (int y = 0; y < kD / 2; ++y) o[y] = 0.0f;
+      for (int y = 0; y < D / 2; ++y) o[y] = 0.0f;
       float M = -INFINITY;
       for (int kt = wk.k0; ok && kt < wk.k1; ++kt, ++x) {
         if (!(ok = __all_sync(0xffffffffu, mbar_wait(pv_done, x & 1, ctl, kSitePvDone)))) break;
@@ -352,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float a = move ? ex2(M - m) : 1.0f;  // (0 at first)
           if (move) M = m;
 #pragma unroll
-          for (int y = 0; y < kD / 2; ++y) o[y] *= a;
+          for (int y = 0; y < D / 2; ++y) o[y] *= a;
         }
         const float f = m == -INFINITY ? 0.0f : ex2(m - M) * vs;
         const float2 ff = make_float2(f, f);
@@ -367,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         };
 #pragma unroll
-        for (int q = 0; q < kD / 2; q += 32) {
+        for (int q = 0; q < D / 2; q += 32) {
           uint32_t wa[16], wb[16];
           tmem_ld16(tO + q, wa);
           tmem_ld16(tO + q + 16, wb);
@@ -398,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (first) p.lse[(static_cast<long long>(wk.b) * p.H + h) * p.Nt + node] = any ? lse2 * kLn2 : -INFINITY;
           uint4 *dst = reinterpret_cast<uint4 *>(p.o + wk.b * p.so.b + h * p.so.h + node * p.so.n + c0);
 #pragma unroll
-          for (int y = 0; y < kD / 2; y += 8)
+          for (int y = 0; y < D / 2; y += 8)
             dst[y / 8] = any ? make_uint4(pack_bf16x2(o[y] * inv, o[y + 1] * inv), pack_bf16x2(o[y + 2] * inv, o[y + 3] * inv),
                                           pack_bf16x2(o[y + 4] * inv, o[y + 5] * inv),
                                           pack_bf16x2(o[y + 6] * inv, o[y + 7] * inv))
@@ -406,9 +411,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           const long long at = (static_cast<long long>(blockIdx.x) * 2 + (wk.k0 == 0 ? 1 : 0)) * kRows + r;
           if (first) p.part_lse[at] = padding ? INFINITY : lse2;
-          float4 *dst = reinterpret_cast<float4 *>(p.part_o + at * kD + c0);
+          float4 *dst = reinterpret_cast<float4 *>(p.part_o + at * D + c0);
 #pragma unroll
-          for (int y = 0; y < kD / 2; y += 4)
+          for (int y = 0; y < D / 2; y += 4)
             dst[y / 4] = any ? make_float4(o[y] * inv, o[y + 1] * inv, o[y + 2] * inv, o[y + 3] * inv)
                              : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         }
@@ -565,9 +570,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int key = r; key < kKeys; key += warps * 32) {
             const int i = n0 + key;
             if (i < p.Nt && (i < 0 || !((dead[i >> 5] >> (i & 31)) & 1u))) continue;
-            uint4 *v = reinterpret_cast<uint4 *>(ring_v + (y0 % SV) * L::kTile + key * 128);
+            uint4 *v = reinterpret_cast<uint4 *>(ring_v + (y0 % SV) * L::kTile + key * D);
 #pragma unroll
-            for (int y = 0; y < 8; ++y) v[y] = make_uint4(0u, 0u, 0u, 0u);
+            for (int y = 0; y < D / 16; ++y) v[y] = make_uint4(0u, 0u, 0u, 0u);
           }
           fence_proxy_async_smem();
         }
@@ -605,15 +610,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+template <int D>
+cudaError_t launch_rows(const CUtensorMap &tk, const CUtensorMap &tv, const Tree8Params &p, cudaStream_t stream) {
+  constexpr uint32_t kBytes = LayoutRows<D>::kRequest;
+  auto kern = fa_tree_fp8_rows_kernel<D>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+  if (e != cudaSuccess) return e;
+  kern<<<static_cast<unsigned>(p.ranges) * p.groups, kThreads, kBytes, stream>>>(tk, tv, p);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t launch_tree8_rows(const CUtensorMap &tk, const CUtensorMap &tv, const Tree8Params &p, cudaStream_t stream) {
-  const cudaError_t e = cudaFuncSetAttribute(fa_tree_fp8_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             LayoutRows::kRequest);
-  if (e != cudaSuccess) return e;
-  fa_tree_fp8_rows_kernel<<<static_cast<unsigned>(p.ranges) * p.groups, kThreads, LayoutRows::kRequest, stream>>>(tk, tv,
-                                                                                                                   p);
-  return cudaGetLastError();
+  return p.d == 128 ? launch_rows<128>(tk, tv, p, stream) : launch_rows<64>(tk, tv, p, stream);
 }
 
 }  // namespace fa

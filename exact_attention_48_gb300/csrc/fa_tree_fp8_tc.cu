@@ -1,5 +1,6 @@
 // fa_tree_fp8_tc.cu -- attention of the newest rows of each sequence, or of a tree
-// of drafted tokens, over a cache held in 8 bits: d = 128, on tcgen05's 8-bit form.
+// of drafted tokens, over a cache held in 8 bits, up to 32 query rows of a cache
+// head, on tcgen05's 8-bit form.
 //
 // Both products run on the cache's codes as TMA leaves them in shared memory, with
 // nothing converted: S^T = K Q^T (a lane per key, a column per query row) and
@@ -23,21 +24,25 @@
 // value.  A weight is rounded to its parts likewise: off by at most 2^-9 of itself, or
 // 2^-10 with its tile's greatest at 2^8.  Scores, maxima, sums and O are fp32.
 //
-// What bounds it.  HBM, 2 d bytes a key, up to about 64 rows: a 128-key tile takes
-// an SM 1400 cycles of its share of the traffic, its products some 560 (a tcgen05
-// instruction takes 60 or more whatever its N) and its softmax about 10 issue slots
-// a row and warp.  More rows come in groups of 64, a CTA each, whose tiles mostly
-// come from L2.
+// What bounds it.  HBM, 2 d bytes a key: a 128-key tile takes an SM 1400 cycles of its
+// share of the traffic, its products some 560 (a tcgen05 instruction takes 60 or more
+// whatever its N) and its softmax about 10 issue slots a row and warp.  16 rows:
+// B16 H16 T1 Nk16384 (1.1 GB) 169 us, 0.97 of the copy bandwidth; B2 H32 Hkv8 T5
+// Nk100001 (0.4 GB) 104 us, where a run of 22 tiles has a start, an end and a second
+// launch to pay for.  32 rows: B16 H16 T32 Nk16384 (lengths of half on average, 0.8 GB)
+// 205 us, and the latency of a tile's way through the softmax (1950 cycles a tile with
+// three warpgroups, all that the registers hold) bounds it.  Converting codes to f16 for
+// mma.sync took 210, 170 and 470 us.  d = 64: a tile has half the bytes and takes the same
+// steps, 133 us for the first (0.54 GB, 0.61 of the copy bandwidth; 160 by mma.sync).
 //
-// CTA: two to four warpgroups of softmax, a key per thread, which take the tiles in
-// turn; one that adds up O^T, a column of V per thread; then the TMA producer (and the
-// tiles' scales), a warp that issues S^T and owns TMEM, one that issues O^T (one thread
+// CTA: three or four warpgroups of softmax, a key per thread, which take the tiles in
+// turn; one that adds up O^T, a column of V per thread; then the TMA producer, a
+// warp that issues S^T and owns TMEM, one that issues O^T (one thread
 // for both took 1950 cycles a tile, most of them in the instructions themselves), and
-// one for q's parts and the tree's table.  TMEM: four S^T and four O^T of 2 C columns (two
-// each for 64 rows).  The tiles of all units form one list that is cut into equal runs
-// (fa_runs.cuh), and a CTA's products run on from unit to unit.
+// one for q's parts and the tree's table.  TMEM: four S^T and four O^T of 2 C columns.
+// The tiles of all units form one list that is cut into equal runs (fa_runs.cuh), and a
+// CTA's products run on from unit to unit.
 
-#include <cfloat>
 #include <cstdint>
 
 #include "fa_cache8.h"
@@ -48,7 +53,6 @@
 namespace fa {
 namespace {
 
-constexpr int kD = 128;
 constexpr float kMoveBy = 8.0f;   // a running maximum moves only when exceeded by more (log2 units)
 constexpr float kLift = 8.0f;     // weights reach 2^kLift
 constexpr float kLn2 = 0.69314718055994530942f;
@@ -68,7 +72,7 @@ struct Roles<32> {
   static constexpr int kGroups = 3;
   static constexpr uint32_t kLaunch = 96, kSoftmax = 112, kAdd = 96, kControl = 48;
 };
-template <int C>
+template <int D, int C>
 struct LayoutTc {
   using R = Roles<C>;
   static constexpr int kGroups = R::kGroups, kSoftmaxWarps = 4 * kGroups;
@@ -76,22 +80,22 @@ struct LayoutTc {
   static_assert(128 * (kGroups * R::kSoftmax + R::kAdd + R::kControl) <= kThreads * R::kLaunch, "register split");
   static constexpr int kWarpAdd = kSoftmaxWarps, kWarpProducer = kWarpAdd + 4, kWarpS = kWarpProducer + 1;
   static constexpr int kWarpO = kWarpProducer + 2, kWarpQ = kWarpProducer + 3;
-  static constexpr uint32_t kTile = kKeys * kD;        // a K or V tile, 16 KB
+  static constexpr uint32_t kTile = kKeys * D;         // a K or V tile
   // Slots of K and of V.  V tiles are asked for kLag tiles after their K: S^T runs about so far ahead of O^T, and a V
   // tile that came with its K would hold its slot meanwhile.
-  static constexpr int kSlotsK = 4, kSlotsV = 5, kLag = C == 64 ? 2 : 3;
-  static constexpr int kBufs = C == 64 ? 2 : 4;        // of S^T, and of O^T
+  static constexpr int kSlotsK = D == 128 ? 4 : 8, kSlotsV = kSlotsK + 1, kLag = 3;
+  static constexpr int kBufs = 4;                      // of S^T, and of O^T
   static constexpr uint32_t kTmem = 2 * kBufs * 2 * C;
   static_assert(kTmem <= 512, "TMEM columns");
   // How many of what one role leaves to another are used in turn.
   // A tile's maxima: tile x + 2 kGroups' are written by a warpgroup that saw tile x's sums done at its tile before.
-  static constexpr int kTiles = kGroups == 2 ? 4 : 8;
+  static constexpr int kTiles = 8;
   static_assert(kTiles >= 2 * kGroups, "tile x's maxima have been read by then");
   // A segment's row factors: segment n + NB + 3's are written when S^T of segment n + NB + 1 is done, so that of a tile
   // beyond x + NB, x any of segment n's, and that takes tile x's scores read.
-  static constexpr int kSegs = kBufs == 2 ? 5 : 8;
+  static constexpr int kSegs = 8;
   static_assert(kSegs >= kBufs + 3, "segment n's factors have been read by then");
-  static constexpr uint32_t kQ = 2 * C * kD;           // q's parts (two segments' in turn)
+  static constexpr uint32_t kQ = 2 * C * D;            // q's parts (two segments' in turn)
   // first the small things, then (1 KB aligned) ring, P, q
   static constexpr uint32_t kOffBits = 0;
   static constexpr uint32_t kOffDead = kOffBits + 32 * (1 + 2 + 3 + 4) * 4;
@@ -111,7 +115,8 @@ struct LayoutTc {
   static constexpr int kNumBars = 2 * (kSlotsK + kSlotsV) + 4 * kBufs + kGroups + 10;
   static constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;            // TMEM address, abort flag
   static constexpr uint32_t kSmall = (kOffMisc + 16 + 15) / 16 * 16;
-  static constexpr uint32_t kRing = (kSlotsK + kSlotsV) * kTile, kP = kGroups * kTile;
+  static constexpr uint32_t kRing = (kSlotsK + kSlotsV) * kTile;
+  static constexpr uint32_t kPTile = kKeys * 128, kP = kGroups * kPTile;  // weights: 128 bytes a key, 2 C used
   static constexpr uint32_t kRequest = kSmall + 1008 + kRing + kP + 2 * kQ;
   static_assert(kOffBar % 8 == 0 && kOffRange % 8 == 0 && kOffScan % 8 == 0 && kOffMost % 16 == 0, "alignment");
   static_assert(kRequest <= 232448, "shared memory budget");
@@ -136,7 +141,6 @@ __device__ __forceinline__ void tmem_pair(uint32_t a, uint32_t b, uint32_t (&x)[
 template <int N>
 __device__ __forceinline__ float lane_sums(float (&v)[N]) {
   const int lane = threadIdx.x & 31;
-  int n = N;
 #pragma unroll
   for (int o = N / 2; o; o >>= 1) {
     const bool up = lane & o;
@@ -146,21 +150,21 @@ __device__ __forceinline__ float lane_sums(float (&v)[N]) {
       const float keep = up ? v[x + o] : v[x], send = up ? v[x] : v[x + o];
       v[x] = keep + __shfl_xor_sync(0xffffffffu, send, o);
     }
-    n >>= 1;
   }
   if (N == 16) v[0] += __shfl_xor_sync(0xffffffffu, v[0], 16);
   return v[0];
 }
 
-template <int C>
-__global__ void __launch_bounds__(LayoutTc<C>::kThreads, 1)
+template <int D, int C>
+__global__ void __launch_bounds__(LayoutTc<D, C>::kThreads, 1)
     fa_tree_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                           const Tree8Params p) {
-  using L = LayoutTc<C>;
+  using L = LayoutTc<D, C>;
   using R = Roles<C>;
+  constexpr int kAddWarps = D / 32;  // with columns of V
   constexpr int SK = L::kSlotsK, SV = L::kSlotsV, NB = L::kBufs, W = L::kGroups, kLag = L::kLag;
   constexpr int kWarpAdd = L::kWarpAdd, kWarpProducer = L::kWarpProducer, kWarpS = L::kWarpS, kWarpO = L::kWarpO;
-  constexpr int kLanes = C < 32 ? C : 32, kPerLane = C / kLanes;  // columns that lanes look after
+  // (lane l of a warp looks after column l % C where a thing is done once a column)
   extern __shared__ uint8_t smem_raw[];
   uint8_t *small = smem_raw;
   uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + L::kSmall + 1023) &
@@ -201,7 +205,7 @@ __global__ void __launch_bounds__(LayoutTc<C>::kThreads, 1)
       mbar_init(&s_full[i], 1);
       mbar_init(&s_free[i], 4);
       mbar_init(&pv_done[i], 1);
-      mbar_init(&o_empty[i], 4);
+      mbar_init(&o_empty[i], kAddWarps);
     }
     for (int i = 0; i < W; ++i) mbar_init(&p_ready[i], 4);
     for (int i = 0; i < 2; ++i) {
@@ -209,9 +213,9 @@ __global__ void __launch_bounds__(LayoutTc<C>::kThreads, 1)
       mbar_init(&q_empty[i], 1);
     }
     mbar_init(mask_full, 1);
-    mbar_init(mask_empty, L::kSoftmaxWarps + 4);
+    mbar_init(mask_empty, L::kSoftmaxWarps + kAddWarps);
     mbar_init(l_full, L::kSoftmaxWarps);
-    mbar_init(l_empty, 4);
+    mbar_init(l_empty, kAddWarps);
     mbar_init(&drain[0], 1);
     mbar_init(&drain[1], 1);
     *abort_flag = 0;
@@ -295,7 +299,7 @@ __global__ void __launch_bounds__(LayoutTc<C>::kThreads, 1)
     } else if (warp == kWarpS && lane == 0) {
       // ---------------------------------------------------------- S^T = K Q^T
       constexpr uint32_t kIdS = idesc_e4m3(kKeys, 2 * C, false, false);
-      const uint64_t dQ = sdesc_sw128(smem_addr(sQ), 16, 1024), dT = sdesc_sw128(smem_addr(ring), 16, 1024);
+      const uint64_t dQ = sdesc_codes<D>(sQ), dT = sdesc_codes<D>(ring);
       uint32_t i = 0, seg = 0, sl = 0, sph = 0, bph = 1;  // tile, segment, K's slot and its phase, the buffer's
       bool ok = true;
       while (ok && wk.next()) {
@@ -309,7 +313,7 @@ __global__ void __launch_bounds__(LayoutTc<C>::kThreads, 1)
           tc_fence_after();
           const uint64_t dk = desc_add(dT, sl * L::kTile);
 #pragma unroll
-          for (int kk = 0; kk < kD / 32; ++kk)
+          for (int kk = 0; kk < D / 32; ++kk)
             mma_ss_f8(tmem + buf * 2 * C, desc_add(dk, kk * 32), desc_add(dq, kk * 32), kIdS, kk > 0 ? 1u : 0u);
           tc_commit(&s_full[buf]);
           tc_commit(&k_empty[sl]);
@@ -325,8 +329,9 @@ __global__ void __launch_bounds__(LayoutTc<C>::kThreads, 1)
       mbar_drain(&drain[0], 0);
     } else if (warp == kWarpO && lane == 0) {
       // ---------------------------------------------------------- O^T = V^T P^T
-      constexpr uint32_t kIdO = idesc_e4m3(kD, 2 * C, true, true);
-      const uint64_t dT = sdesc_sw128(smem_addr(ring_v), 16, 1024), dP = sdesc_sw128(smem_addr(sP), 16, 1024);
+      // (at d = 64 rows 64.. of the product are what follows the tile in shared memory: nothing reads them)
+      constexpr uint32_t kIdO = idesc_e4m3(128, 2 * C, true, true);
+      const uint64_t dT = sdesc_codes<D>(ring_v, L::kTile), dP = sdesc_sw128(smem_addr(sP), 16, 1024);
       const uint32_t total = static_cast<uint32_t>(wk.end - wk.t);
       uint32_t sl = 0, sph = 0, bph = 1;  // V's slot and its phase, the buffer's
       uint32_t wg = 0, wph = 0;           // the warpgroup and its weights' phase
@@ -336,10 +341,10 @@ __global__ void __launch_bounds__(LayoutTc<C>::kThreads, 1)
               mbar_wait(&p_ready[wg], wph, ctl, kSitePReady)))
           break;
         tc_fence_after();
-        const uint64_t dv = desc_add(dT, sl * L::kTile), dp = desc_add(dP, wg * L::kTile);
+        const uint64_t dv = desc_add(dT, sl * L::kTile), dp = desc_add(dP, wg * L::kPTile);
 #pragma unroll
         for (int kk = 0; kk < kKeys / 32; ++kk)
-          mma_ss_f8(tmem + (NB + buf) * 2 * C, desc_add(dv, kk * 4096), desc_add(dp, kk * 4096), kIdO, kk > 0 ? 1u : 0u);
+          mma_ss_f8(tmem + (NB + buf) * 2 * C, desc_add(dv, kk * 32 * D), desc_add(dp, kk * 4096), kIdO, kk > 0 ? 1u : 0u);
         tc_commit(&pv_done[buf]);
         tc_commit(&v_empty[sl]);
         if (++sl == SV) {
@@ -355,15 +360,16 @@ __global__ void __launch_bounds__(LayoutTc<C>::kThreads, 1)
       tc_commit(&drain[1]);
       mbar_drain(&drain[1], 0);
     } else if (warp == L::kWarpQ) {
-      // ---------------------------------------------------------- q's parts, eight lanes a row, and the tree's table
+      // ---------------------------------------------------------- q's parts, D / 16 lanes a row, and the tree's table
+      constexpr int kLanes = D / 16;
       uint32_t n = 0, nmask = 0;
       while (wk.next()) {
         const uint32_t qb = n & 1;
         if (!__all_sync(0xffffffffu, mbar_wait(&q_empty[qb], ((n >> 1) & 1) ^ 1, ctl, kSiteQEmpty))) break;
         const float sign = p.scale_log2 < 0.0f ? -1.0f : 1.0f;
 #pragma unroll 2
-        for (int r0 = 0; r0 < C; r0 += 4) {
-          const int r = r0 + (lane >> 3), x = lane & 7, row = first_row + r;
+        for (int r0 = 0; r0 < C; r0 += 32 / kLanes) {
+          const int r = r0 + lane / kLanes, x = lane % kLanes, row = first_row + r;
           uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
           if (row < unit_rows) {
             const uint4 *src = reinterpret_cast<const uint4 *>(p.q + wk.b * p.sq.b + (wk.hk * p.G + row / p.Nt) * p.sq.h +
@@ -374,14 +380,13 @@ __global__ void __launch_bounds__(LayoutTc<C>::kThreads, 1)
           }
           float most = greatest(w);
 #pragma unroll
-          for (int o = 1; o < 8; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+          for (int o = 1; o < kLanes; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
           const float unit = least_scale(most), by = sign / unit;
           uint4 hi, lo;
           q_parts(w, by, &hi, &lo);
-          const uint32_t at = r * kD + ((x ^ (r & 7)) * 16);
-          uint8_t *to = sQ + qb * L::kQ + at;
+          uint8_t *to = sQ + qb * L::kQ + piece_at<D>(r, x);
           *reinterpret_cast<uint4 *>(to) = hi;
-          *reinterpret_cast<uint4 *>(to + C * kD) = lo;
+          *reinterpret_cast<uint4 *>(to + C * D) = lo;
           if (x == 0) row_f[n % L::kSegs * C + r] = unit * fabsf(p.scale_log2);
         }
         fence_proxy_async_smem();
@@ -394,13 +399,19 @@ __global__ void __launch_bounds__(LayoutTc<C>::kThreads, 1)
         ++nmask;
       }
     }
+  } else if (warp >= kWarpAdd + kAddWarps) {
+    // (the other warps of the warpgroup have no column of V)
+    if (R::kAdd > R::kLaunch)
+      regs_increase<R::kAdd>();
+    else
+      regs_decrease<R::kAdd>();
   } else if (warp >= kWarpAdd) {
     // ------------------------------------------------------------ O^T added up, a column of V per thread
     if (R::kAdd > R::kLaunch)
       regs_increase<R::kAdd>();
     else
       regs_decrease<R::kAdd>();
-    const int col = (warp & 3) * 32 + lane;
+    const int col = (warp & 3) * 32 + lane, mine = lane & (C - 1);
     float *fac = floats(L::kOffAdd) + (warp - kWarpAdd) * C;
     uint32_t x = 0, seg = 0, nmask = 0;
     bool ok = true;
@@ -409,35 +420,24 @@ __global__ void __launch_bounds__(LayoutTc<C>::kThreads, 1)
         p.cuts[p.cuts_by_unit ? wk.b * p.Hkv + wk.hk : c] =
             wk.tail ? make_int4(-1, 0, 0, 0)
                     : make_int4(wk.b, wk.hk, c, static_cast<int>(divide((wk.u0 + wk.tiles) * run->runs - 1, run->total)));
-      float o[C], M[kPerLane];
+      float o[C], M = -INFINITY;
 #pragma unroll
       for (int r = 0; r < C; ++r) o[r] = 0.0f;
-#pragma unroll
-      for (int y = 0; y < kPerLane; ++y) M[y] = -INFINITY;
       for (int kt = wk.k0; ok && kt < wk.k1; ++kt, ++x) {
         const uint32_t buf = x % NB;
         if (!(ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[buf], (x / NB) & 1, ctl, kSitePvDone)))) break;
         tc_fence_after();
-        // the factors of the columns that this lane looks after
+        // the factor of the column that this lane looks after
         const float *tm = tile_m + x % L::kTiles * (C + 4), vs = tm[C];
-        bool move = false;
-        float alpha[kPerLane];
-#pragma unroll
-        for (int y = 0; y < kPerLane; ++y) {
-          const int r = (lane & (kLanes - 1)) + y * 32;
-          const float m = tm[r];
-          alpha[y] = 1.0f;
-          if (m > M[y] + kMoveBy) {
-            alpha[y] = ex2(M[y] - m);  // (0 at first)
-            M[y] = m;
-            move = true;
-          }
-          fac[r] = m == -INFINITY ? 0.0f : ex2(m - M[y]) * vs;
-        }
+        const float m = tm[mine];
+        const bool move = m > M + kMoveBy;
+        const float alpha = move ? ex2(M - m) : 1.0f;  // (0 at first)
+        if (move) M = m;
+        fac[mine] = m == -INFINITY ? 0.0f : ex2(m - M) * vs;
         __syncwarp();
         if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
-          for (int r = 0; r < C; ++r) o[r] *= __shfl_sync(0xffffffffu, alpha[r / 32], r % 32);
+          for (int r = 0; r < C; ++r) o[r] *= __shfl_sync(0xffffffffu, alpha, r);
         }
         const uint32_t at = tmem + (NB + buf) * 2 * C + lane_base;
 #pragma unroll
@@ -465,49 +465,43 @@ __global__ void __launch_bounds__(LayoutTc<C>::kThreads, 1)
       const bool whole = wk.whole();
       const long long slot = (static_cast<long long>(blockIdx.x) * 2 + (wk.k0 == 0 ? 1 : 0)) * C;
       if (ok) {
-        uint32_t none[kPerLane];  // rows without a result: 0
+        const int row = first_row + mine;
+        float l = 0.0f;
 #pragma unroll
-        for (int y = 0; y < kPerLane; ++y) {
-          const int r = (lane & (kLanes - 1)) + y * 32, row = first_row + r;
-          float l = 0.0f;
-#pragma unroll
-          for (int w = 0; w < L::kSoftmaxWarps; ++w) {
-            const float m = sum_m[(w >> 2) * C + r];
-            l += m == -INFINITY ? sum_l[w * C + r] : sum_l[w * C + r] * ex2(m - M[y]);
-          }
-          const int node = row < unit_rows ? row % p.Nt : 0;
-          const bool padding = wk.tail && ((dead[node >> 5] >> (node & 31)) & 1u);
-          const bool any = l != 0.0f && !padding;
-          fac[r] = any ? 1.0f / l : 0.0f;
-          none[y] = any ? 0u : 1u;
-          if (warp == kWarpAdd && lane < kLanes && row < unit_rows) {
-            const float lse2 = any ? (M[y] == -INFINITY ? 0.0f : M[y]) - kLift + log2f(l) : -INFINITY;
-            const int h = wk.hk * p.G + row / p.Nt;
-            if (whole)
-              p.lse[(static_cast<long long>(wk.b) * p.H + h) * p.Nt + node] = any ? lse2 * kLn2 : -INFINITY;
-            else
-              p.part_lse[slot + r] = padding ? INFINITY : lse2;
-          }
+        for (int w = 0; w < L::kSoftmaxWarps; ++w) {
+          const float m = sum_m[(w >> 2) * C + mine];
+          l += m == -INFINITY ? sum_l[w * C + mine] : sum_l[w * C + mine] * ex2(m - M);
         }
-#pragma unroll
-        for (int y = 0; y < kPerLane; ++y) none[y] = __ballot_sync(0xffffffffu, none[y]);
+        const int row_node = row < unit_rows ? row % p.Nt : 0;
+        const bool padding = wk.tail && ((dead[row_node >> 5] >> (row_node & 31)) & 1u);
+        const bool any = l != 0.0f && !padding;
+        fac[mine] = any ? 1.0f / l : 0.0f;
+        if (warp == kWarpAdd && lane < C && row < unit_rows) {
+          const float lse2 = any ? (M == -INFINITY ? 0.0f : M) - kLift + log2f(l) : -INFINITY;
+          const int h = wk.hk * p.G + row / p.Nt;
+          if (whole)
+            p.lse[(static_cast<long long>(wk.b) * p.H + h) * p.Nt + row_node] = any ? lse2 * kLn2 : -INFINITY;
+          else
+            p.part_lse[slot + mine] = padding ? INFINITY : lse2;
+        }
+        const uint32_t none = __ballot_sync(0xffffffffu, !any);  // rows without a result: 0
         if (whole) {
           const int rows = unit_rows - first_row;
           int node = first_row % p.Nt;
           __nv_bfloat16 *head = p.o + wk.b * p.so.b + (wk.hk * p.G + first_row / p.Nt) * p.so.h + col;
 #pragma unroll
           for (int r = 0; r < C; ++r) {
-            if (r < rows) head[node * p.so.n] = __float2bfloat16((none[r / 32] >> (r % 32)) & 1u ? 0.0f : o[r] * fac[r]);
+            if (r < rows) head[node * p.so.n] = __float2bfloat16((none >> r) & 1u ? 0.0f : o[r] * fac[r]);
             if (++node == p.Nt) {
               node = 0;
               head += p.so.h;
             }
           }
         } else {
-          float *part = p.part_o + slot * kD + col;
+          float *part = p.part_o + slot * D + col;
 #pragma unroll
           for (int r = 0; r < C; ++r)
-            if (first_row + r < unit_rows) part[r * kD] = (none[r / 32] >> (r % 32)) & 1u ? 0.0f : o[r] * fac[r];
+            if (first_row + r < unit_rows) part[r * D] = (none >> r) & 1u ? 0.0f : o[r] * fac[r];
         }
       }
       __syncwarp();
@@ -521,7 +515,7 @@ __global__ void __launch_bounds__(LayoutTc<C>::kThreads, 1)
   } else {
     // ------------------------------------------------------------ softmax, a key per thread
     regs_increase<R::kSoftmax>();
-    const int wg = warp >> 2, key = threadIdx.x & 127;
+    const int wg = warp >> 2, key = threadIdx.x & 127, mine = lane & (C - 1);
     float *most = floats(L::kOffMost) + wg * 4 * C;        // [4 warps][C]
     float *base = floats(L::kOffBase) + warp * 2 * C;      // 8 - m, then l's factor
     uint32_t x = 0, seg = 0, nmask = 0;  // tiles before the segment, segments, masked ones
@@ -530,11 +524,9 @@ __global__ void __launch_bounds__(LayoutTc<C>::kThreads, 1)
     while (wk.next()) {
       const int n = wk.k1 - wk.k0;
       const int from = wk.base();
-      float l[C], lm[kPerLane];  // l relative to lm, of the columns that lanes look after
+      float l[C], lm = -INFINITY;  // l of all columns, relative to lm, which a lane has of its own
 #pragma unroll
       for (int r = 0; r < C; ++r) l[r] = 0.0f;
-#pragma unroll
-      for (int y = 0; y < kPerLane; ++y) lm[y] = -INFINITY;
       bool have_mask = false;
       // this key's scale, and the value scale of 16-key slice lane % 8 (0: behind the end)
       const float *k_scale = p.k_scale + (static_cast<long long>(wk.b) * p.Hkv + wk.hk) * p.blocks;
@@ -568,19 +560,17 @@ __global__ void __launch_bounds__(LayoutTc<C>::kThreads, 1)
         tc_fence_after();
         float s[C];
         const uint32_t at = tmem + buf * 2 * C + lane_base;
-        constexpr int kChunk = C == 64 ? 16 : C;  // (more does not fit the registers)
+        {
+          uint32_t hi[C], lo[C];
+          tmem_pair(at, at + C, hi, lo);
 #pragma unroll
-        for (int r = 0; r < C; r += kChunk) {
-          uint32_t hi[kChunk], lo[kChunk];
-          tmem_pair(at + r, at + C + r, hi, lo);
-#pragma unroll
-          for (int y = 0; y < kChunk; y += 2) {
-            const float2 f = *reinterpret_cast<const float2 *>(rf + r + y);
+          for (int y = 0; y < C; y += 2) {
+            const float2 f = *reinterpret_cast<const float2 *>(rf + y);
             const float2 e = ffma2(fadd2(make_float2(__uint_as_float(hi[y]), __uint_as_float(hi[y + 1])),
                                          make_float2(__uint_as_float(lo[y]), __uint_as_float(lo[y + 1]))),
                                    fmul2(f, make_float2(kn, kn)), make_float2(lr, lr));
-            s[r + y] = e.x;
-            s[r + y + 1] = e.y;
+            s[y] = e.x;
+            s[y + 1] = e.y;
           }
         }
         tc_fence_before();
@@ -589,18 +579,18 @@ __global__ void __launch_bounds__(LayoutTc<C>::kThreads, 1)
         if (masked) {
           // the rows that see this key (rows that are padding may: their results are replaced).  A loop, because
           // code that runs once a unit comes cold from memory.
-          uint64_t rows = node < 0 ? ~0ull : 0ull;
+          uint32_t rows = node < 0 ? ~0u : 0u;
           if (node >= 0 && node < p.Nt) {
             int i = first_row % p.Nt;
 #pragma unroll 1
             for (int r = 0; r < C; ++r) {
-              if ((i >> 5) >= (node >> 5) && ((bits[bit_row(i) + (node >> 5)] >> (node & 31)) & 1u)) rows |= 1ull << r;
+              if ((i >> 5) >= (node >> 5) && ((bits[bit_row(i) + (node >> 5)] >> (node & 31)) & 1u)) rows |= 1u << r;
               if (++i == p.Nt) i = 0;
             }
           }
 #pragma unroll
           for (int r = 0; r < C; ++r)
-            if (!((rows >> r) & 1ull)) s[r] = -INFINITY;
+            if (!((rows >> r) & 1u)) s[r] = -INFINITY;
         }
         // the tile's maxima: over the warp's keys, then over the four warps
 #pragma unroll
@@ -610,33 +600,24 @@ __global__ void __launch_bounds__(LayoutTc<C>::kThreads, 1)
           if (lane == 0) *reinterpret_cast<float4 *>(most + (warp & 3) * C + r) = v;
         }
         named_barrier(1 + wg, 128);
-        bool move = false;
-        float alpha[kPerLane];
-#pragma unroll
-        for (int y = 0; y < kPerLane; ++y) {
-          const int r = (lane & (kLanes - 1)) + y * 32;
-          const float m = fmaxf(fmaxf(most[r], most[C + r]), fmaxf(most[2 * C + r], most[3 * C + r]));
-          alpha[y] = 1.0f;
-          if (m > lm[y] + kMoveBy) {
-            alpha[y] = ex2(lm[y] - m);
-            lm[y] = m;
-            move = true;
-          }
-          base[r] = kLift - (m == -INFINITY ? 0.0f : m);
-          base[C + r] = m == -INFINITY ? 0.0f : ex2(m - lm[y]);
-          if ((warp & 3) == 0) tile_m[y0 % L::kTiles * (C + 4) + r] = m;
-        }
+        const float m = fmaxf(fmaxf(most[mine], most[C + mine]), fmaxf(most[2 * C + mine], most[3 * C + mine]));
+        const bool move = m > lm + kMoveBy;
+        const float alpha = move ? ex2(lm - m) : 1.0f;
+        if (move) lm = m;
+        base[mine] = kLift - (m == -INFINITY ? 0.0f : m);
+        base[C + mine] = m == -INFINITY ? 0.0f : ex2(m - lm);
+        if ((warp & 3) == 0) tile_m[y0 % L::kTiles * (C + 4) + mine] = m;
         if ((warp & 3) == 0 && lane == 0) tile_m[y0 % L::kTiles * (C + 4) + C] = vmax;
         __syncwarp();
         if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
-          for (int r = 0; r < C; ++r) l[r] *= __shfl_sync(0xffffffffu, alpha[r / 32], r % 32);
+          for (int r = 0; r < C; ++r) l[r] *= __shfl_sync(0xffffffffu, alpha, r);
         }
         // the weights' buffer is free once tile y0 - W's product is done (and its sums, see kTiles)
         if (y0 >= W &&
             !(ok = __all_sync(0xffffffffu, mbar_wait(&o_empty[(y0 - W) % NB], ((y0 - W) / NB) & 1, ctl, kSiteDqEmpty))))
           continue;
-        uint8_t *prow = sP + wg * L::kTile + key * 128;
+        uint8_t *prow = sP + wg * L::kPTile + key * 128;
 #pragma unroll
         for (int r = 0; r < C; r += 16) {
           uint32_t hi[4], lo[4];
@@ -664,9 +645,9 @@ __global__ void __launch_bounds__(LayoutTc<C>::kThreads, 1)
           // V rows that no query row sees become zeros (0 * NaN is NaN)
           if (!(ok = __all_sync(0xffffffffu, mbar_wait(&v_full[y0 % SV], (y0 / SV) & 1, ctl, kSiteVFull)))) continue;
           if (node >= p.Nt || (node >= 0 && ((dead[node >> 5] >> (node & 31)) & 1u))) {
-            uint4 *v = reinterpret_cast<uint4 *>(ring_v + (y0 % SV) * L::kTile + key * 128);
+            uint4 *v = reinterpret_cast<uint4 *>(ring_v + (y0 % SV) * L::kTile + key * D);
 #pragma unroll
-            for (int y = 0; y < 8; ++y) v[y] = make_uint4(0u, 0u, 0u, 0u);
+            for (int y = 0; y < D / 16; ++y) v[y] = make_uint4(0u, 0u, 0u, 0u);
           }
         }
         fence_proxy_async_smem();
@@ -679,16 +660,10 @@ __global__ void __launch_bounds__(LayoutTc<C>::kThreads, 1)
       // ---- l over the warp's keys
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(l_empty, (seg & 1) ^ 1, ctl, kSiteLseEmpty));
       if (ok) {
-#pragma unroll
-        for (int y = 0; y < kPerLane; ++y) {
-          float v[kLanes];
-#pragma unroll
-          for (int r = 0; r < kLanes; ++r) v[r] = l[y * 32 + r];
-          const float sum = lane_sums<kLanes>(v);
-          if (lane < kLanes) {
-            sum_l[warp * C + y * 32 + lane] = sum;
-            if ((warp & 3) == 0) sum_m[wg * C + y * 32 + lane] = lm[y];
-          }
+        const float sum = lane_sums<C>(l);
+        if (lane < C) {
+          sum_l[warp * C + lane] = sum;
+          if ((warp & 3) == 0) sum_m[wg * C + lane] = lm;
         }
       }
       warp_arrive(l_full);
@@ -708,10 +683,10 @@ __global__ void __launch_bounds__(LayoutTc<C>::kThreads, 1)
   }
 }
 
-template <int C>
+template <int D, int C>
 cudaError_t launch_tc(const CUtensorMap &tk, const CUtensorMap &tv, const Tree8Params &p, cudaStream_t stream) {
-  using L = LayoutTc<C>;
-  auto kern = fa_tree_fp8_tc_kernel<C>;
+  using L = LayoutTc<D, C>;
+  auto kern = fa_tree_fp8_tc_kernel<D, C>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kRequest);
   if (e != cudaSuccess) return e;
   kern<<<static_cast<unsigned>(p.ranges) * p.groups, L::kThreads, L::kRequest, stream>>>(tk, tv, p);
@@ -721,7 +696,8 @@ cudaError_t launch_tc(const CUtensorMap &tk, const CUtensorMap &tv, const Tree8P
 }  // namespace
 
 cudaError_t launch_tree8_tc(const CUtensorMap &tk, const CUtensorMap &tv, const Tree8Params &p, cudaStream_t stream) {
-  return p.rows == 16 ? launch_tc<16>(tk, tv, p, stream) : launch_tc<32>(tk, tv, p, stream);
+  if (p.d == 64) return p.rows == 16 ? launch_tc<64, 16>(tk, tv, p, stream) : launch_tc<64, 32>(tk, tv, p, stream);
+  return p.rows == 16 ? launch_tc<128, 16>(tk, tv, p, stream) : launch_tc<128, 32>(tk, tv, p, stream);
 }
 
 }  // namespace fa

@@ -342,6 +342,12 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t start, uint32_t lbo, ui
   return d;
 }
 
+// The same for the 64-byte-swizzled layout: rows (MN-major: 64 elements of 8 bits) of
+// 64 bytes, 8-row groups of 512; slabs of an MN-major tile `lbo` bytes apart.
+__device__ __forceinline__ uint64_t sdesc_sw64(uint32_t start, uint32_t lbo, uint32_t sbo) {
+  return (sdesc_sw128(start, lbo, sbo) & ~(7ull << 61)) | (4ull << 61);
+}
+
 // A descriptor moved by `bytes` inside its tile.  Shared-memory addresses
 // stay below 256 KB, so the 14-bit start field never carries into the
 // leading-dimension field.

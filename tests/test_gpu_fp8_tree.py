@@ -8,11 +8,8 @@ that times scale * sum |k|.  It is a sum of 2 d products, exact in fp32, added i
 an order of the hardware's: off by at most 2 d * 2^-23 of scale * sum |q k| (A below;
 each addition by at most 2^-23 of the running sum of magnitudes, truncation
 included), then a few 2^-24 of itself, which A exceeds too: e is the sum of both.
-Every weight is off by e and by the exponential's 2^-22, then by its rounding.  d = 64: to
-f16, 2^-11, or 2^-31 of its row's greatest (V's scales relative to each other times that:
-at most 2^16 in these tests, on weights below 2^-20 of the greatest, so below 2^-15 of the
-greatest product and covered by a second 2^-11 of sum P|v|).  d = 128: to f16, 2^-11, and
-to two e4m3 parts: the first leaves at most half a step, 2^(a - 4) of a weight in
+Every weight is off by e and by the exponential's 2^-22, then by its rounding to two e4m3
+parts: the first leaves at most half a step, 2^(a - 4) of a weight in
 [2^a, 2^(a + 1)), and the second at most a sixteenth of a power of two below that, 2^(a - 9),
 or 2^-10 where it falls below e4m3's normal range: 2^-9 of the weight, or 2^-10 with the
 tile's greatest product of a weight and its value's scale at 2^8, so 2^-18 of that times
@@ -61,10 +58,7 @@ def check(o, lse, q, kv, vv, parents, n, Nt, scale, what, v8):
                                                             if bool(mask.any()) else 0.0) * abs(scale)
         assert bool((lse[h][~on] == -math.inf).all()) and bool((o[h][~on] == 0).all()), what
         err = (o[h].double() - wo).abs()[on]
-        if d == 64:
-            tol = 2 * (2 * e + 2.0 ** -11 + 2.0 ** -22) * pv[on]
-        else:
-            tol = (4 * e + 2.0 ** -21 + 2.0 ** -11 + 2.0 ** -9) * pv[on] + floor_of(q[h], kv, mask, wl, scale, *v8)[on]
+        tol = (4 * e + 2.0 ** -21 + 2.0 ** -9) * pv[on] + floor_of(q[h], kv, mask, wl, scale, *v8)[on]
         tol += 2.0 ** -8 * wo.abs()[on] + 1e-30
         assert bool((err <= tol).all()), f"{what} head {h}: {float(err.max()):.3e}, {float((err / tol).max()):.2f} of the bound"
         err = (lse[h].double() - wl).abs()[on]
