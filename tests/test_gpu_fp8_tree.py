@@ -124,6 +124,18 @@ def test_long_and_many_units():
 
 
 @pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G,Nt", [(4, 4), (17, 1), (2, 16), (1, 33), (4, 16), (5, 13), (2, 64), (43, 3), (8, 40)])
+def test_rows_of_a_group(G, Nt, d):
+    """Query rows of a cache head around the kernels' 16, 32 and 128, over caches whose units are cut by the runs' ends,
+    and of which a run holds several."""
+    g = ref.gen(2020 + G + Nt)
+    run(g, 3, 5 * G, 5, Nt, 2900, d, 64, "bnhd", [2900, 2000, 1300], tree_of(g, 3, Nt), heads=[(0, 0), (0, 4), (1, 2), (2, 0)])
+    lens = [1100 - 29 * b for b in range(36)]
+    run(g, 36, 8 * G, 8, Nt, 1100, d, 32, lens=lens, heads=[(0, 0), (1, 7), (9, 3), (20, 5), (35, 7)])
+    run(g, 36, 2 * G, 2, Nt, 500, d, 16, lens=[n % 501 for n in lens], heads=[(0, 0), (1, 1), (9, 0), (20, 1), (35, 1)])
+
+
+@pytest.mark.parametrize("d", [64, 128])
 def test_lengths(d):
     """Every residue of the length against slices and tiles; lengths of zero, below Nt, negative, past Nk."""
     g = ref.gen(2002)
@@ -131,13 +143,17 @@ def test_lengths(d):
     lens = [0, 1, 2, 3, 15, 16, 17, 18, 19, 31, 32, 33, 127, 128, 129, 130, 131, 143, 144, 255, 256, 257, 299, 300, 301, -5, 99999]
     for parents in (None, ref.ints([-1, 0, 0])):
         run(g, len(lens), 2, 1, Nt, Nk, d, 16, lens=lens, parents=parents)
+    for H, Nt in ((2, 12), (3, 25)):
+        run(g, len(lens), H, 1, Nt, Nk, d, 64, lens=lens, parents=tree_of(g, len(lens), Nt))
 
 
 def test_padding_and_invalid_parents():
     g = ref.gen(2003)
     par = ref.ints([[-1, 0, 1, -2, 3, 4, 9, 1, -1, 5], [-1, -1, -1, 2, 2, 2, 3, 7, 0, 8], [-2] + [0] * 9, [1] + [-1] * 9])
     run(g, 4, 6, 2, 10, 500, 64, 32, lens=[500, 300, 200, 140], parents=par)
-    run(g, 4, 6, 2, 10, 3000, 128, 64, lens=[3000, 2900, 2000, 140], parents=par)
+    run(g, 4, 6, 2, 10, 2990, 128, 64, lens=[2990, 2900, 2000, 140], parents=par)
+    run(g, 4, 10, 2, 10, 2990, 128, 64, lens=[2990, 2900, 2000, 140], parents=par)
+    run(g, 4, 10, 2, 10, 700, 64, 16, lens=[700, 640, 500, 140], parents=par)
 
 
 def test_chain_is_the_causal_tree():
@@ -243,6 +259,37 @@ def test_nan_reaches_its_rows():
         o, lse = fa_fwd_tree_fp8(q, k, bad, ks, vs, par, block=16)
         assert bool(torch.isnan(o[..., 5]).all()) and torch.equal(lse, clean[1])
         assert torch.equal(o[..., :5], clean[0][..., :5]) and torch.equal(o[..., 6:], clean[0][..., 6:])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G", [5, 12])
+def test_nan_and_many_rows(G, d):
+    """The same for the other kernels: NaN keys and queries reach the rows that see them, garbage behind none."""
+    g = ref.gen(2021)
+    Nk, n = 2500, 2222
+    q = ref.draw(g, 1, 2 * G, 4, d)
+    k, ks = r8.cache(g, 1, 2, Nk, d, 16)
+    v, vs = r8.cache(g, 1, 2, Nk, d, 16)
+    par, lens = ref.ints([-1, 0, 0, 1]), ref.ints([n])
+    clean = fa_fwd_tree_fp8(q, k, v, ks, vs, par, lens, block=16)
+    for t in (k, v):
+        t.view(torch.uint8)[:, :, n:] = 0x7F
+    ks[..., -(-n // 16):] = math.nan
+    vs[..., -(-n // 16):] = math.inf
+    o, lse = fa_fwd_tree_fp8(q, k, v, ks, vs, par, lens, block=16)
+    assert torch.equal(o, clean[0]) and torch.equal(lse, clean[1]) and bool(torch.isfinite(o).all())
+    bad = k.clone()
+    bad.view(torch.uint8)[0, 0, n - 3, 5] = 0x7F    # node 1: seen by nodes 1 and 3
+    o, lse = fa_fwd_tree_fp8(q, bad, v, ks, vs, par, lens, block=16)
+    assert bool(torch.isnan(o[0, :G, [1, 3]]).all()) and bool(torch.isnan(lse[0, :G, [1, 3]]).all())
+    assert torch.equal(o[0, :G, [0, 2]], clean[0][0, :G, [0, 2]]) and torch.equal(lse[0, :G, [0, 2]], clean[1][0, :G, [0, 2]])
+    assert torch.equal(o[0, G:], clean[0][0, G:])
+    qn = q.clone()
+    qn[0, 1, 2, 9] = math.inf
+    o, lse = fa_fwd_tree_fp8(qn, k, v, ks, vs, par, lens, block=16)
+    assert bool(torch.isnan(o[0, 1, 2]).all()) and bool(torch.isnan(lse[0, 1, 2]))
+    o[0, 1, 2], lse[0, 1, 2] = clean[0][0, 1, 2], clean[1][0, 1, 2]
+    assert torch.equal(o, clean[0]) and torch.equal(lse, clean[1])
 
 
 def test_same_bits_again_graphs_and_streams():
