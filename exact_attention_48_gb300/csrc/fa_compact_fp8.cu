@@ -5,12 +5,20 @@
 // codes that fall below e4m3's normal range); one whose scale it is is moved bit
 // by bit.
 //
-// HBM bounds both forms.  A CTA works on windows of 128 destination rows, one to
-// eight blocks: it reads the rows' codes into registers and the scales of the
-// blocks they come from, finds each block's greatest, and writes.  Out of place
-// every window is a CTA of its own.  In place a destination row may be the source
-// of an earlier destination only (kept ascends and kept[i] >= i), so one CTA takes
-// a head's windows of K or V in order.
+// HBM bounds both forms.  A CTA works on windows of whole blocks of destination rows
+// (128 rows out of place): it reads the rows' codes into registers and the scales of
+// the blocks they come from, finds each block's greatest, and writes.  Out of place
+// every window is a CTA of its own: B16 Hkv16 16384 to 8192 rows d128 (1.1 GB) 209 us,
+// 0.77 of the copy bandwidth.
+//
+// In place a destination row may be the source of an earlier destination only (kept
+// ascends and kept[i] >= i), so a head's windows of K or V go in order.  Columns do
+// not depend on each other, only the scales do: where there are few heads, a cluster
+// of up to 8 CTAs shares a head, each with its columns of longer windows; a
+// cluster barrier a window lets the first of them write a window's scales only when
+// all have read them.  The next window's rows and the list after it are on their way
+// meanwhile (a later window's sources lie behind the rows written here).  B16 Hkv16 16384 to
+// 8192 rows d128 301 us; B1 Hkv2 131072 to 65536 rows 246 us, 1214 with a CTA a head.
 
 #include <cstdint>
 
@@ -49,7 +57,7 @@ struct Window {
   static constexpr int kPieces = D / 16, kPass = kThreads / kPieces, kItems = kWindow / kPass;
   uint4 w[kItems];
   float s[kItems];     // the row's scale before, 0: no row
-  bool stays[kItems];  // it is where it belongs
+  bool stays[kItems];  // it is a row of the output that stays
 
   // Window rows r0 + [0, 128): the rows that move there, and rows before `base`
   // of a block that is written (they stay, and count).
@@ -76,7 +84,6 @@ struct Window {
       const long long src = base + from;
       if (from < 0 || src < 0 || src >= p.Nk) continue;
       s[it] = x.scale[src >> p.block_log2];
-      stays[it] = p.in_place && src == dst;
       w[it] = __ldcs(reinterpret_cast<const uint4 *>(x.src + src * x.src_n + c * 16));
     }
   }
@@ -138,44 +145,140 @@ __global__ void __launch_bounds__(kThreads, 6) fa_compact_fp8_gather_kernel(cons
   w.write(p, side, most, moved, r0);
 }
 
+__device__ __forceinline__ void meet(int log2_cluster) {
+  if (log2_cluster)
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  else
+    __syncthreads();
+}
+
+constexpr int kSlideItems = 4;  // rows of a thread
+
+// In place.  grid: x = (head, K or V, rank in the cluster).  A row takes t = 2^lt threads
+// of a CTA, a window 1024 / t rows.
 template <int D>
-__global__ void __launch_bounds__(kThreads) fa_compact_fp8_slide_kernel(const Compact8Params p, int windows) {
-  __shared__ uint32_t most[2][8], moved[2][8];
-  const int tensor = blockIdx.x & 1, bh = blockIdx.x >> 1, b = bh / p.Hkv, h = bh - b * p.Hkv;
-  const long long base = p.base ? p.base[b] : 0;
+__global__ void __launch_bounds__(kThreads, 4) fa_compact_fp8_slide_kernel(const Compact8Params p, int windows,
+                                                                        int log2_cluster) {
+  constexpr int kLogPieces = D == 128 ? 3 : 2, kMostBlocks = 1024 / 16;
+  __shared__ uint32_t most[3][kMostBlocks], moved[3][kMostBlocks];  // used in turn
+  const int tid = threadIdx.x, lt = kLogPieces - log2_cluster, step = kThreads >> lt, window = step * kSlideItems;
+  const int rank = blockIdx.x & ((1 << log2_cluster) - 1), of = blockIdx.x >> log2_cluster;
+  const int tensor = of & 1, bh = of >> 1, b = bh / p.Hkv, h = bh - b * p.Hkv;
+  const int c = (rank << lt) + (tid & ((1 << lt) - 1)), first = tid >> lt;  // column piece, row of the window
+  const long long base = p.base ? p.base[b] : 0, begin = (base >> 7) * kWindow;  // (arithmetic: floors)
+  const long long shared_blk = (base > 0 ? base : 0) >> p.block_log2;            // rows before base in it stay, and count
   const int *kept = p.kept + b * p.kept_b + h * p.kept_h;
   const Side x = side_of(p, tensor, b, h);
-  if (threadIdx.x < 16) (&most[0][0])[threadIdx.x] = (&moved[0][0])[threadIdx.x] = 0u;
+  for (int i = tid; i < kMostBlocks; i += kThreads) most[0][i] = moved[0][i] = 0u;
+
+  // The rows that move to the thread's rows of window i: an old row, or -1.
+  int from[kSlideItems];
+  auto list = [&](int i) {
+#pragma unroll
+    for (int it = 0; it < kSlideItems; ++it) {
+      const long long dst = begin + static_cast<long long>(i) * window + it * step + first, e = dst - base;
+      from[it] = -1;
+      if (i >= windows || dst < 0 || dst >= p.Nk) continue;
+      if (e < 0) {
+        if ((dst >> p.block_log2) == shared_blk) from[it] = static_cast<int>(dst);
+      } else if (e < p.M) {
+        const int k = kept[e];
+        const long long src = base + k;
+        if (k >= 0 && src >= 0 && src < p.Nk) from[it] = static_cast<int>(src);
+      }
+    }
+  };
+  uint4 w[kSlideItems], wn[kSlideItems];
+  float s[kSlideItems], sn[kSlideItems];  // the rows' scales before, 0: no row
+  uint32_t stays = 0, staysn;             // rows that are where they belong, a bit each
+  auto read = [&](int i) {
+    staysn = 0;
+#pragma unroll
+    for (int it = 0; it < kSlideItems; ++it) {
+      const int src = from[it];
+      sn[it] = 0.0f;
+      if (src < 0) continue;
+      sn[it] = x.scale[src >> p.block_log2];
+      wn[it] = __ldcs(reinterpret_cast<const uint4 *>(x.src + src * x.src_n + c * 16));
+      if (src == begin + static_cast<long long>(i) * window + it * step + first) staysn |= 1u << it;
+    }
+  };
+  list(0);
+  read(0);
+  list(1);
+  int turn = 0;
   for (int i = 0; i < windows; ++i) {
-    const long long r0 = (first_window(base) + i) * kWindow;
-    Window<D> w;
-    w.read(p, x, kept, base, r0);
-    __syncthreads();  // every row and scale has been read; the last window's counts are no longer needed
-    w.count(p, most[i & 1], moved[i & 1], base, r0);
-    if (threadIdx.x < 8) most[~i & 1][threadIdx.x] = moved[~i & 1][threadIdx.x] = 0u;
-    __syncthreads();
-    w.write(p, x, most[i & 1], moved[i & 1], r0);
+    const long long r0 = begin + static_cast<long long>(i) * window;
+    const int now_turn = turn, next_turn = turn == 2 ? 0 : turn + 1;
+    turn = next_turn;
+#pragma unroll
+    for (int it = 0; it < kSlideItems; ++it) w[it] = wn[it], s[it] = sn[it];
+    stays = staysn;
+    __syncthreads();  // the counts are zero
+    read(i + 1);
+    list(i + 2);
+    for (int j = tid; j < kMostBlocks; j += kThreads) most[next_turn][j] = moved[next_turn][j] = 0u;
+#pragma unroll
+    for (int it = 0; it < kSlideItems; ++it) {
+      const int row = it * step + first;
+      if (!(s[it] > 0.0f) || (tid & ((1 << lt) - 1))) continue;
+      atomicMax(&most[now_turn][row >> p.block_log2], __float_as_uint(s[it]));
+      if (r0 + row >= base) moved[now_turn][row >> p.block_log2] = 1u;
+    }
+    meet(log2_cluster);  // every rank has read this window's rows and scales
+#pragma unroll
+    for (int it = 0; it < kSlideItems; ++it) {
+      const int row = it * step + first, blk = row >> p.block_log2;
+      if (!(s[it] > 0.0f) || !moved[now_turn][blk]) continue;
+      const float now = __uint_as_float(most[now_turn][blk]);
+      if (now == s[it] && ((stays >> it) & 1u)) continue;
+      uint4 v = w[it];
+      if (now != s[it]) {
+        const float r = s[it] / now;
+        v.x = rescale_codes(v.x, r);
+        v.y = rescale_codes(v.y, r);
+        v.z = rescale_codes(v.z, r);
+        v.w = rescale_codes(v.w, r);
+      }
+      __stcs(reinterpret_cast<uint4 *>(x.dst + (r0 + row) * x.dst_n + c * 16), v);
+    }
+    if (rank == 0 && tid < (window >> p.block_log2) && moved[now_turn][tid])
+      x.scale_out[(r0 >> p.block_log2) + tid] = __uint_as_float(most[now_turn][tid]);
   }
 }
 
 }  // namespace
 
+template <int D>
+static cudaError_t launch_slide(const Compact8Params &p, cudaStream_t stream) {
+  const long long heads = static_cast<long long>(p.B) * p.Hkv * 2;
+  // some two CTAs an SM, where a window has rows for them
+  int lc = 0;
+  while ((16 << (lc + 1)) <= D && heads << (lc + 1) <= 304 && p.M > (kThreads * kSlideItems * 16 / D) << lc) ++lc;
+  const int window = (kThreads * kSlideItems * 16 / D) << lc;
+  const int windows = static_cast<int>((static_cast<long long>(p.M) + (p.base ? kWindow - 1 : 0) + window - 1) / window);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(heads << lc));  // (heads below 2^25)
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 1u << lc;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = lc ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, fa_compact_fp8_slide_kernel<D>, p, windows, lc);
+}
+
 cudaError_t launch_compact8(const Compact8Params &p, cudaStream_t stream) {
-  const long long heads = static_cast<long long>(p.B) * p.Hkv;
+  if (p.in_place) return p.d == 64 ? launch_slide<64>(p, stream) : launch_slide<128>(p, stream);
   // windows that M rows may touch (from a window's start without a base)
   const int windows = p.base ? (p.M - 1 + kWindow - 1) / kWindow + 1 : (p.M + kWindow - 1) / kWindow;
-  const unsigned grid = static_cast<unsigned>(p.in_place ? heads * 2 : heads * windows * 2);  // below 2^31: checked on entry
-  if (p.in_place) {
-    if (p.d == 64)
-      fa_compact_fp8_slide_kernel<64><<<grid, kThreads, 0, stream>>>(p, windows);
-    else
-      fa_compact_fp8_slide_kernel<128><<<grid, kThreads, 0, stream>>>(p, windows);
-  } else {
-    if (p.d == 64)
-      fa_compact_fp8_gather_kernel<64><<<grid, kThreads, 0, stream>>>(p, windows);
-    else
-      fa_compact_fp8_gather_kernel<128><<<grid, kThreads, 0, stream>>>(p, windows);
-  }
+  const unsigned grid = static_cast<unsigned>(static_cast<long long>(p.B) * p.Hkv * windows * 2);  // below 2^31: checked on entry
+  if (p.d == 64)
+    fa_compact_fp8_gather_kernel<64><<<grid, kThreads, 0, stream>>>(p, windows);
+  else
+    fa_compact_fp8_gather_kernel<128><<<grid, kThreads, 0, stream>>>(p, windows);
   return cudaGetLastError();
 }
 

@@ -70,6 +70,23 @@ def test_in_place(B, Hkv, Nk, M, d, block, layout):
     check(old[2], old[3], vc, vs, old[2], old[3], kept, [0] * B, block, "v")
 
 
+@pytest.mark.parametrize("B,Hkv,Nk,M,d,block,layout", [
+    (1, 2, 5000, 4000, 128, 16, "bhnd"), (1, 1, 6000, 3333, 64, 128, "bnhd"), (3, 7, 2100, 1500, 128, 32, "pitch"),
+    (2, 20, 1300, 1299, 128, 64, "bhnd"), (5, 40, 700, 600, 64, 64, "bnhd")])
+def test_long_lists_in_place(B, Hkv, Nk, M, d, block, layout):
+    """From one head shared by a cluster to heads of their own; lists from a base on, which may leave nothing to move."""
+    g = ref.gen(3150 + Nk)
+    for base in (None, [(37 * b) % 300 for b in range(B)]):
+        kc, ks = r8.cache(g, B, Hkv, Nk, d, block, layout, 5)
+        vc, vs = r8.cache(g, B, Hkv, Nk, d, block, layout, 5)
+        old = [t.clone() for t in (kc, ks, vc, vs)]
+        kept = lists(g, B, Hkv, Nk, M)
+        fa_cache_compact_fp8(kc, vc, ks, vs, kept, None if base is None else ref.ints(base), block)
+        base = base or [0] * B
+        check(old[0], old[1], kc, ks, old[0], old[1], kept, base, block, "k")
+        check(old[2], old[3], vc, vs, old[2], old[3], kept, base, block, "v")
+
+
 @pytest.mark.parametrize("d,block", [(64, 16), (128, 64), (64, 128), (128, 32)])
 def test_accepted_branch(d, block):
     """A drafted tree's branch behind rows that stay, from every place in a block; rows out of the cache are skipped."""
