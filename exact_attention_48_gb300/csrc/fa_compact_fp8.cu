@@ -5,11 +5,12 @@
 // codes that fall below e4m3's normal range); one whose scale it is is moved bit
 // by bit.
 //
-// HBM bounds both forms.  A CTA works on windows of whole blocks of destination rows
-// (128 rows out of place): it reads the rows' codes into registers and the scales of
-// the blocks they come from, finds each block's greatest, and writes.  Out of place
-// every window is a CTA of its own: B16 Hkv16 16384 to 8192 rows d128 (1.1 GB) 209 us,
-// 0.77 of the copy bandwidth.
+// HBM bounds both forms.  Out of place a warp moves 16 rows of K or V; it looks through
+// the list and the scales of its whole block by itself (up to 128 of each, which the
+// block's other warps look through as well), so that no warp waits for another and
+// 64 of them an SM keep loads in flight.  B16 Hkv16 16384 to 8192 rows d128 (1.1 GB) 164 us,
+// 0.98 of the copy bandwidth (blocks of 128 rows: 174); a CTA a window of 128 rows with
+// the blocks' greatest scales found in shared memory took 209, both tensors in a CTA 324.
 //
 // In place a destination row may be the source of an earlier destination only (kept
 // ascends and kept[i] >= i), so a head's windows of K or V go in order.  Columns do
@@ -23,12 +24,13 @@
 #include <cstdint>
 
 #include "fa_cache8.h"
+#include "ptx.cuh"
 
 namespace fa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWindow = 128;  // destination rows of a step, aligned: whole blocks
+constexpr int kWindow = 128;  // destination rows, aligned: whole blocks
 
 // One tensor of the two.
 struct Side {
@@ -51,98 +53,76 @@ __device__ __forceinline__ Side side_of(const Compact8Params &p, int tensor, int
   return x;
 }
 
-// What a thread holds of a window: a 16-byte piece of each of ITEMS rows.
+__device__ __forceinline__ uint4 rescale_piece(uint4 v, float r) {
+  return make_uint4(rescale_codes(v.x, r), rescale_codes(v.y, r), rescale_codes(v.z, r), rescale_codes(v.w, r));
+}
+
+// Out of place.  grid: x = (window of 128 rows of a head, K or V); a warp moves 16 rows,
+// and looks through the list and the scales of its whole block by itself (no exchange
+// between warps but where rows before base stay).
 template <int D>
-struct Window {
-  static constexpr int kPieces = D / 16, kPass = kThreads / kPieces, kItems = kWindow / kPass;
-  uint4 w[kItems];
-  float s[kItems];     // the row's scale before, 0: no row
-  bool stays[kItems];  // it is a row of the output that stays
-
-  // Window rows r0 + [0, 128): the rows that move there, and rows before `base`
-  // of a block that is written (they stay, and count).
-  __device__ __forceinline__ void read(const Compact8Params &p, const Side &x, const int *kept, long long base,
-                                       long long r0) {
-    const int c = threadIdx.x % kPieces;
-#pragma unroll
-    for (int it = 0; it < kItems; ++it) {
-      const long long dst = r0 + it * kPass + static_cast<int>(threadIdx.x) / kPieces, i = dst - base;
-      s[it] = 0.0f;
-      stays[it] = false;
-      if (dst < 0 || dst >= p.Nout) continue;
-      if (i < 0) {
-        // a row before base, in a block that rows from base on share
-        const long long first = base > 0 ? base : 0;
-        if ((dst >> p.block_log2) != (first >> p.block_log2)) continue;
-        s[it] = x.scale_out[dst >> p.block_log2];
-        stays[it] = true;
-        w[it] = *reinterpret_cast<const uint4 *>(x.dst + dst * x.dst_n + c * 16);
-        continue;
-      }
-      if (i >= p.M) continue;
-      const int from = kept[i];
-      const long long src = base + from;
-      if (from < 0 || src < 0 || src >= p.Nk) continue;
-      s[it] = x.scale[src >> p.block_log2];
-      w[it] = __ldcs(reinterpret_cast<const uint4 *>(x.src + src * x.src_n + c * 16));
-    }
-  }
-  // most, moved: [8] of the window's blocks, zero before.
-  __device__ __forceinline__ void count(const Compact8Params &p, uint32_t *most, uint32_t *moved, long long base,
-                                        long long r0) {
-#pragma unroll
-    for (int it = 0; it < kItems; ++it) {
-      const int row = it * kPass + static_cast<int>(threadIdx.x) / kPieces;
-      if (!(s[it] > 0.0f) || threadIdx.x % kPieces) continue;
-      atomicMax(&most[row >> p.block_log2], __float_as_uint(s[it]));
-      if (r0 + row >= base) moved[row >> p.block_log2] = 1u;
-    }
-  }
-  __device__ __forceinline__ void write(const Compact8Params &p, const Side &x, const uint32_t *most,
-                                        const uint32_t *moved, long long r0) {
-    const int c = threadIdx.x % kPieces;
-#pragma unroll
-    for (int it = 0; it < kItems; ++it) {
-      const int row = it * kPass + static_cast<int>(threadIdx.x) / kPieces, blk = row >> p.block_log2;
-      if (!(s[it] > 0.0f) || !moved[blk]) continue;
-      const float now = __uint_as_float(most[blk]);
-      if (now == s[it] && stays[it]) continue;
-      uint4 v = w[it];
-      if (now != s[it]) {
-        const float r = s[it] / now;
-        v.x = rescale_codes(v.x, r);
-        v.y = rescale_codes(v.y, r);
-        v.z = rescale_codes(v.z, r);
-        v.w = rescale_codes(v.w, r);
-      }
-      __stcs(reinterpret_cast<uint4 *>(x.dst + (r0 + row) * x.dst_n + c * 16), v);
-    }
-    const int blk = threadIdx.x;
-    if (blk < (kWindow >> p.block_log2) && moved[blk])
-      x.scale_out[(r0 >> p.block_log2) + blk] = __uint_as_float(most[blk]);
-  }
-};
-
-// The first window that rows from base on lie in.
-__device__ __forceinline__ long long first_window(long long base) { return base >> 7; }  // (arithmetic: floors)
-
-// (K and V of a window in one CTA, 108 registers and two CTAs an SM: B16 Hkv16
-// 16384 to 8192 rows d128 324 us.)
-template <int D>
-__global__ void __launch_bounds__(kThreads, 6) fa_compact_fp8_gather_kernel(const Compact8Params p, int windows) {
-  __shared__ uint32_t most[8], moved[8];
+__global__ void __launch_bounds__(kThreads, 8) fa_compact_fp8_gather_kernel(const Compact8Params p, int windows) {
+  constexpr int kPieces = D / 16, kPass = 32 / kPieces, kItems = 16 / kPass;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int x = blockIdx.x >> 1, bh = x / windows, b = bh / p.Hkv, h = bh - b * p.Hkv;
   const long long base = p.base ? p.base[b] : 0;
-  const long long r0 = (first_window(base) + (x - bh * windows)) * kWindow;
+  const long long w0 = ((base >> 7) + (x - bh * windows)) * kWindow;  // (arithmetic: floors)
+  const long long r0 = w0 + warp * 16, b0 = (r0 >> p.block_log2) << p.block_log2;
   const int *kept = p.kept + b * p.kept_b + h * p.kept_h;
-  if (threadIdx.x < 8) most[threadIdx.x] = moved[threadIdx.x] = 0u;
   const Side side = side_of(p, blockIdx.x & 1, b, h);
-  Window<D> w;
-  w.read(p, side, kept, base, r0);
-  __syncthreads();
-  w.count(p, most, moved, base, r0);
-  __syncthreads();
-  w.write(p, side, most, moved, r0);
+  // the block's rows, 32 at a time: the row that moves there (-1: none), its scale
+  const long long shared_blk = (base > 0 ? base : 0) >> p.block_log2;  // rows before base in it stay, and count
+  int from = -1;
+  float scale = 0.0f, most = 0.0f;
+  bool moved = false;
+  for (int u = 0; u < 1 << p.block_log2; u += 32) {
+    const long long dst = b0 + u + lane, i = dst - base;
+    int f = -1;
+    float s = 0.0f;
+    if (dst >= 0 && dst < p.Nout && lane < 1 << p.block_log2) {
+      if (i < 0) {
+        if ((dst >> p.block_log2) == shared_blk) {
+          f = static_cast<int>(dst);
+          s = side.scale_out[shared_blk];
+        }
+      } else if (i < p.M) {
+        const int k = kept[i];
+        const long long src = base + k;
+        if (k >= 0 && src >= 0 && src < p.Nk) {
+          f = static_cast<int>(src);
+          s = side.scale[src >> p.block_log2];
+          moved |= s > 0.0f;
+        }
+      }
+    }
+    most = fmaxf(most, s);
+    if (u == ((static_cast<int>(r0 - b0)) & ~31)) {  // this warp's own rows are among them
+      from = f;
+      scale = s;
+    }
+  }
+  const int c = lane % kPieces, own = static_cast<int>(r0 - b0) & 31;
+  uint4 w[kItems];
+#pragma unroll
+  for (int it = 0; it < kItems; ++it) {
+    const int row = it * kPass + lane / kPieces, f = __shfl_sync(0xffffffffu, from, own + row);
+    if (f < 0) continue;
+    const uint8_t *at = r0 + row < base ? side.dst + f * side.dst_n : side.src + f * side.src_n;
+    w[it] = __ldcs(reinterpret_cast<const uint4 *>(at + c * 16));
+  }
+  most = warp_max_f32(most);
+  moved = __any_sync(0xffffffffu, moved);
+  if (base > w0) __syncthreads();  // rows of the output and a scale of it that count have been read
+  if (!moved) return;
+#pragma unroll
+  for (int it = 0; it < kItems; ++it) {
+    const int row = it * kPass + lane / kPieces;
+    const float s = __shfl_sync(0xffffffffu, scale, own + row);
+    if (!(s > 0.0f)) continue;
+    __stcs(reinterpret_cast<uint4 *>(side.dst + (r0 + row) * side.dst_n + c * 16),
+           s == most ? w[it] : rescale_piece(w[it], s / most));
+  }
+  if (r0 == b0 && lane == 0) side.scale_out[r0 >> p.block_log2] = most;
 }
 
 __device__ __forceinline__ void meet(int log2_cluster) {
@@ -232,15 +212,8 @@ __global__ void __launch_bounds__(kThreads, 4) fa_compact_fp8_slide_kernel(const
       if (!(s[it] > 0.0f) || !moved[now_turn][blk]) continue;
       const float now = __uint_as_float(most[now_turn][blk]);
       if (now == s[it] && ((stays >> it) & 1u)) continue;
-      uint4 v = w[it];
-      if (now != s[it]) {
-        const float r = s[it] / now;
-        v.x = rescale_codes(v.x, r);
-        v.y = rescale_codes(v.y, r);
-        v.z = rescale_codes(v.z, r);
-        v.w = rescale_codes(v.w, r);
-      }
-      __stcs(reinterpret_cast<uint4 *>(x.dst + (r0 + row) * x.dst_n + c * 16), v);
+      __stcs(reinterpret_cast<uint4 *>(x.dst + (r0 + row) * x.dst_n + c * 16),
+             now == s[it] ? w[it] : rescale_piece(w[it], s[it] / now));
     }
     if (rank == 0 && tid < (window >> p.block_log2) && moved[now_turn][tid])
       x.scale_out[(r0 >> p.block_log2) + tid] = __uint_as_float(most[now_turn][tid]);
