@@ -56,30 +56,21 @@ namespace {
 constexpr float kMoveBy = 8.0f;   // a running maximum moves only when exceeded by more (log2 units)
 constexpr float kLift = 8.0f;     // weights reach 2^kLift
 constexpr float kLn2 = 0.69314718055994530942f;
-// The CTA's warps: kGroups warpgroups of softmax, then one that adds up O^T, then the
-// control warps.  A softmax warpgroup takes some 3000 cycles a tile, most of them
-// latency, so there are as many as the registers hold.  Registers: launched with
-// kLaunch a thread, split by setmaxnreg.
-template <int C>
-struct Roles;
-template <>
-struct Roles<16> {
-  static constexpr int kGroups = 4;
-  static constexpr uint32_t kLaunch = 80, kSoftmax = 88, kAdd = 72, kControl = 56;
-};
-template <>
-struct Roles<32> {
-  static constexpr int kGroups = 3;
-  static constexpr uint32_t kLaunch = 96, kSoftmax = 112, kAdd = 96, kControl = 48;
-};
+// The CTA's warps: four warpgroups of softmax, then one that adds up O^T, then the
+// control warps.  A softmax warpgroup takes 16 columns of a tile: with 32 columns two
+// share a tile (one with all 32 would need 112 registers, and code that does not stay in
+// the instruction cache: three of them took 1830 cycles a tile).  Registers: launched
+// with kLaunch a thread, split by setmaxnreg.
+constexpr int kGroups = 4, kSoftmaxWarps = 4 * kGroups, kThreads = 128 * (kGroups + 2);
+constexpr int kCols = 16;  // of a softmax warpgroup
+constexpr int kWarpAdd = kSoftmaxWarps, kWarpProducer = kWarpAdd + 4, kWarpS = kWarpProducer + 1;
+constexpr int kWarpO = kWarpProducer + 2, kWarpQ = kWarpProducer + 3;
+constexpr uint32_t kRegsLaunch = 80, kRegsSoftmax = 88, kRegsAdd = 80, kRegsControl = 48;
+static_assert(128 * (kGroups * kRegsSoftmax + kRegsAdd + kRegsControl) <= kThreads * kRegsLaunch, "register split");
+
 template <int D, int C>
 struct LayoutTc {
-  using R = Roles<C>;
-  static constexpr int kGroups = R::kGroups, kSoftmaxWarps = 4 * kGroups;
-  static constexpr int kThreads = 128 * (kGroups + 2);
-  static_assert(128 * (kGroups * R::kSoftmax + R::kAdd + R::kControl) <= kThreads * R::kLaunch, "register split");
-  static constexpr int kWarpAdd = kSoftmaxWarps, kWarpProducer = kWarpAdd + 4, kWarpS = kWarpProducer + 1;
-  static constexpr int kWarpO = kWarpProducer + 2, kWarpQ = kWarpProducer + 3;
+  static constexpr int kHalves = C / kCols, kSlots = kGroups / kHalves;  // warpgroups of a tile, tiles at work
   static constexpr uint32_t kTile = kKeys * D;         // a K or V tile
   // Slots of K and of V.  V tiles are asked for kLag tiles after their K: S^T runs about so far ahead of O^T, and a V
   // tile that came with its K would hold its slot meanwhile.
@@ -88,9 +79,10 @@ struct LayoutTc {
   static constexpr uint32_t kTmem = 2 * kBufs * 2 * C;
   static_assert(kTmem <= 512, "TMEM columns");
   // How many of what one role leaves to another are used in turn.
-  // A tile's maxima: tile x + 2 kGroups' are written by a warpgroup that saw tile x's sums done at its tile before.
+  // A tile's maxima: tile x + 8's are written by warpgroups that saw tile x + 4 - kSlots added up at their tile before,
+  // or a later one, so x; buffer x % kBufs of the weights is free when tile x - kBufs has been added up.
   static constexpr int kTiles = 8;
-  static_assert(kTiles >= 2 * kGroups, "tile x's maxima have been read by then");
+  static_assert(kBufs >= kSlots && kTiles >= kBufs + kSlots, "tile x's maxima have been read by then");
   // A segment's row factors: segment n + NB + 3's are written when S^T of segment n + NB + 1 is done, so that of a tile
   // beyond x + NB, x any of segment n's, and that takes tile x's scores read.
   static constexpr int kSegs = 8;
@@ -102,68 +94,49 @@ struct LayoutTc {
   static constexpr uint32_t kOffJump = kOffDead + 16;
   static constexpr uint32_t kOffRange = kOffJump + 128;
   static constexpr uint32_t kOffScan = kOffRange + 48;                    // warps' sums
-  static constexpr uint32_t kOffMost = kOffScan + 24 * 8;                 // [softmax warps][C] greatest e
-  static constexpr uint32_t kOffBase = kOffMost + kSoftmaxWarps * C * 4;  // [softmax warps][2][C]: 8 - m, l's factor
-  static constexpr uint32_t kOffTileM = kOffBase + kSoftmaxWarps * 2 * C * 4;  // [kTiles][C] m and the greatest vs
+  static constexpr uint32_t kOffMost = kOffScan + 24 * 8;                 // [2][softmax warps][16] greatest e, in turn
+  static constexpr uint32_t kOffBase = kOffMost + 2 * kSoftmaxWarps * kCols * 4;  // [softmax warps][2][16]: 8 - m, l's factor
+  static constexpr uint32_t kOffTileM = kOffBase + kSoftmaxWarps * 2 * kCols * 4;  // [kTiles][C] m and the greatest vs
   static constexpr uint32_t kOffAdd = kOffTileM + kTiles * (C + 4) * 4;   // [4 warps][C]: factors of O
-  static constexpr uint32_t kOffL = kOffAdd + 4 * C * 4;                  // [softmax warps][C] l, and [groups][C] its base
-  static constexpr uint32_t kOffLm = kOffL + kSoftmaxWarps * C * 4;
-  static constexpr uint32_t kOffRow = kOffLm + kGroups * C * 4;           // [kSegs][C] rows' factors
+  static constexpr uint32_t kOffL = kOffAdd + 4 * C * 4;                  // [softmax warps][16] l, and [groups][16] its base
+  static constexpr uint32_t kOffLm = kOffL + kSoftmaxWarps * kCols * 4;
+  static constexpr uint32_t kOffRow = kOffLm + kGroups * kCols * 4;           // [kSegs][C] rows' factors
   static constexpr uint32_t kOffBar = kOffRow + kSegs * C * 4;
-  // k_full[], k_empty[], v_full[], v_empty[], s_full[bufs], s_free[bufs], pv_done[bufs], o_empty[bufs], p_ready[groups], q_full[2], q_empty[2],
+  // k_full[], k_empty[], v_full[], v_empty[], s_full[bufs], s_free[bufs], pv_done[bufs], o_empty[bufs], p_ready[bufs], q_full[2], q_empty[2],
   // mask_full, mask_empty, l_full, l_empty, drain[2]
-  static constexpr int kNumBars = 2 * (kSlotsK + kSlotsV) + 4 * kBufs + kGroups + 10;
+  static constexpr int kNumBars = 2 * (kSlotsK + kSlotsV) + 5 * kBufs + 10;
   static constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;            // TMEM address, abort flag
   static constexpr uint32_t kSmall = (kOffMisc + 16 + 15) / 16 * 16;
   static constexpr uint32_t kRing = (kSlotsK + kSlotsV) * kTile;
-  static constexpr uint32_t kPTile = kKeys * 128, kP = kGroups * kPTile;  // weights: 128 bytes a key, 2 C used
+  static constexpr uint32_t kPTile = kKeys * 64, kP = kBufs * kPTile;  // weights: 64 bytes a key, 2 C used
   static constexpr uint32_t kRequest = kSmall + 1008 + kRing + kP + 2 * kQ;
   static_assert(kOffBar % 8 == 0 && kOffRange % 8 == 0 && kOffScan % 8 == 0 && kOffMost % 16 == 0, "alignment");
   static_assert(kRequest <= 232448, "shared memory budget");
 };
 
-// 32 lanes x 16 or 32 columns from each of two places.
-__device__ __forceinline__ void tmem_pair(uint32_t a, uint32_t b, uint32_t (&x)[16], uint32_t (&y)[16]) {
-  tmem_ld16(a, x);
-  tmem_ld16(b, y);
-  tmem_ld_wait16(x);
-  tmem_ld_wait16(y);
-}
-__device__ __forceinline__ void tmem_pair(uint32_t a, uint32_t b, uint32_t (&x)[32], uint32_t (&y)[32]) {
-  tmem_ld32(a, x);
-  tmem_ld32(b, y);
-  tmem_ld_wait(x);
-  tmem_ld_wait(y);
-}
-
-// Sums over the warp's lanes of N values each (N = 16, 32): lane l gets the sum of
-// value l % N, in a fixed order.
-template <int N>
-__device__ __forceinline__ float lane_sums(float (&v)[N]) {
+// Sums over the warp's lanes of 16 values each: lane l gets the sum of value l % 16,
+// in a fixed order.
+__device__ __forceinline__ float lane_sums(float (&v)[16]) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int o = N / 2; o; o >>= 1) {
+  for (int o = 8; o; o >>= 1) {
     const bool up = lane & o;
 #pragma unroll
-    for (int x = 0; x < N / 2; ++x) {
-      if (x >= o) break;
+    for (int x = 0; x < o; ++x) {
       const float keep = up ? v[x + o] : v[x], send = up ? v[x] : v[x + o];
       v[x] = keep + __shfl_xor_sync(0xffffffffu, send, o);
     }
   }
-  if (N == 16) v[0] += __shfl_xor_sync(0xffffffffu, v[0], 16);
-  return v[0];
+  return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 16);
 }
 
 template <int D, int C>
-__global__ void __launch_bounds__(LayoutTc<D, C>::kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     fa_tree_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                           const Tree8Params p) {
   using L = LayoutTc<D, C>;
-  using R = Roles<C>;
   constexpr int kAddWarps = D / 32;  // with columns of V
-  constexpr int SK = L::kSlotsK, SV = L::kSlotsV, NB = L::kBufs, W = L::kGroups, kLag = L::kLag;
-  constexpr int kWarpAdd = L::kWarpAdd, kWarpProducer = L::kWarpProducer, kWarpS = L::kWarpS, kWarpO = L::kWarpO;
+  constexpr int SK = L::kSlotsK, SV = L::kSlotsV, NB = L::kBufs, kLag = L::kLag;
   // (lane l of a warp looks after column l % C where a thing is done once a column)
   extern __shared__ uint8_t smem_raw[];
   uint8_t *small = smem_raw;
@@ -178,11 +151,11 @@ __global__ void __launch_bounds__(LayoutTc<D, C>::kThreads, 1)
   float *sum_l = floats(L::kOffL), *sum_m = floats(L::kOffLm);
   uint64_t *k_full = reinterpret_cast<uint64_t *>(small + L::kOffBar), *k_empty = k_full + SK;
   uint64_t *v_full = k_empty + SK, *v_empty = v_full + SV;
-  // Tile x of the run uses number x % NB of the buffers' barriers and p_ready number x % W.  No wait can find its
-  // barrier two phases on: tile x + NB's product waits for what tile x's readers arrive on.
+  // Tile x of the run uses number x % NB of the buffers' barriers.  No wait can find its barrier two phases on: tile
+  // x + NB's product waits for what tile x's readers arrive on, and its weights for tile x's sums.
   uint64_t *s_full = v_empty + SV, *s_free = s_full + NB, *pv_done = s_free + NB, *o_empty = pv_done + NB;
   uint64_t *p_ready = o_empty + NB;
-  uint64_t *q_full = p_ready + W, *q_empty = q_full + 2, *mask_full = q_empty + 2, *mask_empty = mask_full + 1;
+  uint64_t *q_full = p_ready + NB, *q_empty = q_full + 2, *mask_full = q_empty + 2, *mask_empty = mask_full + 1;
   uint64_t *l_full = mask_empty + 1, *l_empty = l_full + 1, *drain = l_empty + 1;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(small + L::kOffMisc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(small + L::kOffMisc + 4);
@@ -203,18 +176,18 @@ __global__ void __launch_bounds__(LayoutTc<D, C>::kThreads, 1)
     }
     for (int i = 0; i < NB; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_free[i], 4);
+      mbar_init(&s_free[i], 4 * L::kHalves);
+      mbar_init(&p_ready[i], 4 * L::kHalves);
       mbar_init(&pv_done[i], 1);
       mbar_init(&o_empty[i], kAddWarps);
     }
-    for (int i = 0; i < W; ++i) mbar_init(&p_ready[i], 4);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 1);
     }
     mbar_init(mask_full, 1);
-    mbar_init(mask_empty, L::kSoftmaxWarps + kAddWarps);
-    mbar_init(l_full, L::kSoftmaxWarps);
+    mbar_init(mask_empty, kSoftmaxWarps + kAddWarps);
+    mbar_init(l_full, kSoftmaxWarps);
     mbar_init(l_empty, kAddWarps);
     mbar_init(&drain[0], 1);
     mbar_init(&drain[1], 1);
@@ -230,7 +203,7 @@ __global__ void __launch_bounds__(LayoutTc<D, C>::kThreads, 1)
     tma_prefetch_desc(&tm_v);
   }
   tc_fence_before();
-  const bool has_run = find_run<L::kThreads>(p, c, run, reinterpret_cast<long long *>(small + L::kOffScan));
+  const bool has_run = find_run<kThreads>(p, c, run, reinterpret_cast<long long *>(small + L::kOffScan));
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   if (p.cuts && !p.cuts_by_unit && group == 0 && threadIdx.x == 0) p.cuts[c] = make_int4(-1, 0, 0, 0);
@@ -242,7 +215,7 @@ __global__ void __launch_bounds__(LayoutTc<D, C>::kThreads, 1)
   const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
 
   if (warp >= kWarpProducer) {
-    regs_decrease<R::kControl>();
+    regs_decrease<kRegsControl>();
     if (warp == kWarpProducer && lane == 0) {
       // ---------------------------------------------------------- producer
       const uint32_t total = static_cast<uint32_t>(wk.end - wk.t);
@@ -331,20 +304,19 @@ __global__ void __launch_bounds__(LayoutTc<D, C>::kThreads, 1)
       // ---------------------------------------------------------- O^T = V^T P^T
       // (at d = 64 rows 64.. of the product are what follows the tile in shared memory: nothing reads them)
       constexpr uint32_t kIdO = idesc_e4m3(128, 2 * C, true, true);
-      const uint64_t dT = sdesc_codes<D>(ring_v, L::kTile), dP = sdesc_sw128(smem_addr(sP), 16, 1024);
+      const uint64_t dT = sdesc_codes<D>(ring_v, L::kTile), dP = sdesc_codes<64>(sP);
       const uint32_t total = static_cast<uint32_t>(wk.end - wk.t);
       uint32_t sl = 0, sph = 0, bph = 1;  // V's slot and its phase, the buffer's
-      uint32_t wg = 0, wph = 0;           // the warpgroup and its weights' phase
       for (uint32_t y = 0; y < total; ++y) {
         const uint32_t buf = y % NB;
         if (!(mbar_wait(&v_full[sl], sph, ctl, kSiteVFull) && mbar_wait(&o_empty[buf], bph, ctl, kSiteDqEmpty) &&
-              mbar_wait(&p_ready[wg], wph, ctl, kSitePReady)))
+              mbar_wait(&p_ready[buf], bph ^ 1, ctl, kSitePReady)))
           break;
         tc_fence_after();
-        const uint64_t dv = desc_add(dT, sl * L::kTile), dp = desc_add(dP, wg * L::kPTile);
+        const uint64_t dv = desc_add(dT, sl * L::kTile), dp = desc_add(dP, buf * L::kPTile);
 #pragma unroll
         for (int kk = 0; kk < kKeys / 32; ++kk)
-          mma_ss_f8(tmem + (NB + buf) * 2 * C, desc_add(dv, kk * 32 * D), desc_add(dp, kk * 4096), kIdO, kk > 0 ? 1u : 0u);
+          mma_ss_f8(tmem + (NB + buf) * 2 * C, desc_add(dv, kk * 32 * D), desc_add(dp, kk * 2048), kIdO, kk > 0 ? 1u : 0u);
         tc_commit(&pv_done[buf]);
         tc_commit(&v_empty[sl]);
         if (++sl == SV) {
@@ -352,14 +324,10 @@ __global__ void __launch_bounds__(LayoutTc<D, C>::kThreads, 1)
           sph ^= 1;
         }
         if (buf == NB - 1) bph ^= 1;
-        if (++wg == W) {
-          wg = 0;
-          wph ^= 1;
-        }
       }
       tc_commit(&drain[1]);
       mbar_drain(&drain[1], 0);
-    } else if (warp == L::kWarpQ) {
+    } else if (warp == kWarpQ) {
       // ---------------------------------------------------------- q's parts, D / 16 lanes a row, and the tree's table
       constexpr int kLanes = D / 16;
       uint32_t n = 0, nmask = 0;
@@ -401,16 +369,10 @@ __global__ void __launch_bounds__(LayoutTc<D, C>::kThreads, 1)
     }
   } else if (warp >= kWarpAdd + kAddWarps) {
     // (the other warps of the warpgroup have no column of V)
-    if (R::kAdd > R::kLaunch)
-      regs_increase<R::kAdd>();
-    else
-      regs_decrease<R::kAdd>();
+    regs_increase<kRegsAdd>();
   } else if (warp >= kWarpAdd) {
     // ------------------------------------------------------------ O^T added up, a column of V per thread
-    if (R::kAdd > R::kLaunch)
-      regs_increase<R::kAdd>();
-    else
-      regs_decrease<R::kAdd>();
+    regs_increase<kRegsAdd>();
     const int col = (warp & 3) * 32 + lane, mine = lane & (C - 1);
     float *fac = floats(L::kOffAdd) + (warp - kWarpAdd) * C;
     uint32_t x = 0, seg = 0, nmask = 0;
@@ -468,9 +430,10 @@ __global__ void __launch_bounds__(LayoutTc<D, C>::kThreads, 1)
         const int row = first_row + mine;
         float l = 0.0f;
 #pragma unroll
-        for (int w = 0; w < L::kSoftmaxWarps; ++w) {
-          const float m = sum_m[(w >> 2) * C + mine];
-          l += m == -INFINITY ? sum_l[w * C + mine] : sum_l[w * C + mine] * ex2(m - M);
+        for (int w = 0; w < 4 * L::kSlots; ++w) {
+          const int wg = (w >> 2) * L::kHalves + mine / kCols, col = mine % kCols;
+          const float m = sum_m[wg * kCols + col], v = sum_l[(wg * 4 + (w & 3)) * kCols + col];
+          l += m == -INFINITY ? v : v * ex2(m - M);
         }
         const int row_node = row < unit_rows ? row % p.Nt : 0;
         const bool padding = wk.tail && ((dead[row_node >> 5] >> (row_node & 31)) & 1u);
@@ -513,20 +476,21 @@ __global__ void __launch_bounds__(LayoutTc<D, C>::kThreads, 1)
       ++seg;
     }
   } else {
-    // ------------------------------------------------------------ softmax, a key per thread
-    regs_increase<R::kSoftmax>();
-    const int wg = warp >> 2, key = threadIdx.x & 127, mine = lane & (C - 1);
-    float *most = floats(L::kOffMost) + wg * 4 * C;        // [4 warps][C]
-    float *base = floats(L::kOffBase) + warp * 2 * C;      // 8 - m, then l's factor
+    // ------------------------------------------------------------ softmax, a key per thread, 16 columns
+    regs_increase<kRegsSoftmax>();
+    constexpr int W = L::kSlots;
+    const int wg = warp >> 2, key = threadIdx.x & 127, mine = lane & (kCols - 1);
+    const int c0 = wg % L::kHalves * kCols;  // its first column
+        float *base = floats(L::kOffBase) + warp * 2 * kCols;  // 8 - m, then l's factor
     uint32_t x = 0, seg = 0, nmask = 0;  // tiles before the segment, segments, masked ones
-    uint32_t y0 = wg;                    // this warpgroup's next tile of the run
+    uint32_t y0 = wg / L::kHalves;       // this warpgroup's next tile of the run
     bool ok = true;
     while (wk.next()) {
       const int n = wk.k1 - wk.k0;
       const int from = wk.base();
-      float l[C], lm = -INFINITY;  // l of all columns, relative to lm, which a lane has of its own
+      float l[kCols], lm = -INFINITY;  // l of its columns, relative to lm, which a lane has of its own
 #pragma unroll
-      for (int r = 0; r < C; ++r) l[r] = 0.0f;
+      for (int r = 0; r < kCols; ++r) l[r] = 0.0f;
       bool have_mask = false;
       // this key's scale, and the value scale of 16-key slice lane % 8 (0: behind the end)
       const float *k_scale = p.k_scale + (static_cast<long long>(wk.b) * p.Hkv + wk.hk) * p.blocks;
@@ -539,7 +503,7 @@ __global__ void __launch_bounds__(LayoutTc<D, C>::kThreads, 1)
       };
       if (y0 < x + n) fetch(wk.k0 + static_cast<int>(y0 - x));
       // (written before the products of this segment were issued)
-      const float *rf = row_f + seg % L::kSegs * C;
+      const float *rf = row_f + seg % L::kSegs * C + c0;
       for (; y0 < x + n; y0 += W) {  // (a warp that gave up still meets the others)
         const int kt = wk.k0 + static_cast<int>(y0 - x);
         const uint32_t buf = y0 % NB;
@@ -558,13 +522,16 @@ __global__ void __launch_bounds__(LayoutTc<D, C>::kThreads, 1)
           continue;
         }
         tc_fence_after();
-        float s[C];
-        const uint32_t at = tmem + buf * 2 * C + lane_base;
+        float s[kCols];
+        const uint32_t at = tmem + buf * 2 * C + c0 + lane_base;
         {
-          uint32_t hi[C], lo[C];
-          tmem_pair(at, at + C, hi, lo);
+          uint32_t hi[kCols], lo[kCols];
+          tmem_ld16(at, hi);
+          tmem_ld16(at + C, lo);
+          tmem_ld_wait16(hi);
+          tmem_ld_wait16(lo);
 #pragma unroll
-          for (int y = 0; y < C; y += 2) {
+          for (int y = 0; y < kCols; y += 2) {
             const float2 f = *reinterpret_cast<const float2 *>(rf + y);
             const float2 e = ffma2(fadd2(make_float2(__uint_as_float(hi[y]), __uint_as_float(hi[y + 1])),
                                          make_float2(__uint_as_float(lo[y]), __uint_as_float(lo[y + 1]))),
@@ -581,70 +548,70 @@ __global__ void __launch_bounds__(LayoutTc<D, C>::kThreads, 1)
           // code that runs once a unit comes cold from memory.
           uint32_t rows = node < 0 ? ~0u : 0u;
           if (node >= 0 && node < p.Nt) {
-            int i = first_row % p.Nt;
+            int i = (first_row + c0) % p.Nt;
 #pragma unroll 1
-            for (int r = 0; r < C; ++r) {
+            for (int r = 0; r < kCols; ++r) {
               if ((i >> 5) >= (node >> 5) && ((bits[bit_row(i) + (node >> 5)] >> (node & 31)) & 1u)) rows |= 1u << r;
               if (++i == p.Nt) i = 0;
             }
           }
 #pragma unroll
-          for (int r = 0; r < C; ++r)
+          for (int r = 0; r < kCols; ++r)
             if (!((rows >> r) & 1u)) s[r] = -INFINITY;
         }
-        // the tile's maxima: over the warp's keys, then over the four warps
+        // the tile's maxima: over the warp's keys, then over the four warps, whose places are used in turn (one may be a
+        // tile ahead)
+        float *most = floats(L::kOffMost) + ((y0 / W & 1) * kSoftmaxWarps + wg * 4) * kCols;
 #pragma unroll
-        for (int r = 0; r < C; r += 4) {
+        for (int r = 0; r < kCols; r += 4) {
           const float4 v = make_float4(warp_max_f32(s[r]), warp_max_f32(s[r + 1]), warp_max_f32(s[r + 2]),
                                        warp_max_f32(s[r + 3]));
-          if (lane == 0) *reinterpret_cast<float4 *>(most + (warp & 3) * C + r) = v;
+          if (lane == 0) *reinterpret_cast<float4 *>(most + (warp & 3) * kCols + r) = v;
         }
         named_barrier(1 + wg, 128);
-        const float m = fmaxf(fmaxf(most[mine], most[C + mine]), fmaxf(most[2 * C + mine], most[3 * C + mine]));
+        const float m = fmaxf(fmaxf(most[mine], most[kCols + mine]), fmaxf(most[2 * kCols + mine], most[3 * kCols + mine]));
         const bool move = m > lm + kMoveBy;
         const float alpha = move ? ex2(lm - m) : 1.0f;
         if (move) lm = m;
         base[mine] = kLift - (m == -INFINITY ? 0.0f : m);
-        base[C + mine] = m == -INFINITY ? 0.0f : ex2(m - lm);
-        if ((warp & 3) == 0) tile_m[y0 % L::kTiles * (C + 4) + mine] = m;
+        base[kCols + mine] = m == -INFINITY ? 0.0f : ex2(m - lm);
+        if ((warp & 3) == 0) tile_m[y0 % L::kTiles * (C + 4) + c0 + mine] = m;
         if ((warp & 3) == 0 && lane == 0) tile_m[y0 % L::kTiles * (C + 4) + C] = vmax;
         __syncwarp();
         if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
-          for (int r = 0; r < C; ++r) l[r] *= __shfl_sync(0xffffffffu, alpha, r);
+          for (int r = 0; r < kCols; ++r) l[r] *= __shfl_sync(0xffffffffu, alpha, r);
         }
-        // the weights' buffer is free once tile y0 - W's product is done (and its sums, see kTiles)
-        if (y0 >= W &&
-            !(ok = __all_sync(0xffffffffu, mbar_wait(&o_empty[(y0 - W) % NB], ((y0 - W) / NB) & 1, ctl, kSiteDqEmpty))))
+        // the weights' buffer is free once tile y0 - NB's sums are done (see kTiles)
+        if (y0 >= NB && !(ok = __all_sync(0xffffffffu, mbar_wait(&o_empty[buf], ((y0 - NB) / NB) & 1, ctl, kSiteDqEmpty))))
           continue;
-        uint8_t *prow = sP + wg * L::kPTile + key * 128;
-#pragma unroll
-        for (int r = 0; r < C; r += 16) {
+        uint8_t *ptile = sP + buf * L::kPTile;
+        {
           uint32_t hi[4], lo[4];
 #pragma unroll
           for (int y = 0; y < 16; y += 4) {
-            const float4 b = *reinterpret_cast<const float4 *>(base + r + y);
-            const float4 g = *reinterpret_cast<const float4 *>(base + C + r + y);
-            const float2 e0 = fadd2(make_float2(s[r + y], s[r + y + 1]), make_float2(b.x, b.y));
-            const float2 e1 = fadd2(make_float2(s[r + y + 2], s[r + y + 3]), make_float2(b.z, b.w));
+            const float4 b = *reinterpret_cast<const float4 *>(base + y);
+            const float4 g = *reinterpret_cast<const float4 *>(base + kCols + y);
+            const float2 e0 = fadd2(make_float2(s[y], s[y + 1]), make_float2(b.x, b.y));
+            const float2 e1 = fadd2(make_float2(s[y + 2], s[y + 3]), make_float2(b.z, b.w));
             const float w0 = ex2(e0.x), w1 = ex2(e0.y), w2 = ex2(e1.x), w3 = ex2(e1.y);
             const float2 ii = make_float2(inv, inv);
-            const float2 n0 = ffma2(make_float2(w0, w1), fmul2(make_float2(g.x, g.y), ii), make_float2(l[r + y], l[r + y + 1]));
+            const float2 n0 = ffma2(make_float2(w0, w1), fmul2(make_float2(g.x, g.y), ii), make_float2(l[y], l[y + 1]));
             const float2 n1 =
-                ffma2(make_float2(w2, w3), fmul2(make_float2(g.z, g.w), ii), make_float2(l[r + y + 2], l[r + y + 3]));
-            l[r + y] = n0.x;
-            l[r + y + 1] = n0.y;
-            l[r + y + 2] = n1.x;
-            l[r + y + 3] = n1.y;
+                ffma2(make_float2(w2, w3), fmul2(make_float2(g.z, g.w), ii), make_float2(l[y + 2], l[y + 3]));
+            l[y] = n0.x;
+            l[y + 1] = n0.y;
+            l[y + 2] = n1.x;
+            l[y + 3] = n1.y;
             parts_of(w0, w1, w2, w3, &hi[y / 4], &lo[y / 4]);
           }
-          *reinterpret_cast<uint4 *>(prow + (((r / 16) ^ (key & 7)) * 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4 *>(prow + (((r / 16 + C / 16) ^ (key & 7)) * 16)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          *reinterpret_cast<uint4 *>(ptile + piece_at<64>(key, c0 / 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4 *>(ptile + piece_at<64>(key, (c0 + C) / 16)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
         if (masked) {
           // V rows that no query row sees become zeros (0 * NaN is NaN)
           if (!(ok = __all_sync(0xffffffffu, mbar_wait(&v_full[y0 % SV], (y0 / SV) & 1, ctl, kSiteVFull)))) continue;
-          if (node >= p.Nt || (node >= 0 && ((dead[node >> 5] >> (node & 31)) & 1u))) {
+          if (c0 == 0 && (node >= p.Nt || (node >= 0 && ((dead[node >> 5] >> (node & 31)) & 1u)))) {
             uint4 *v = reinterpret_cast<uint4 *>(ring_v + (y0 % SV) * L::kTile + key * D);
 #pragma unroll
             for (int y = 0; y < D / 16; ++y) v[y] = make_uint4(0u, 0u, 0u, 0u);
@@ -652,7 +619,7 @@ __global__ void __launch_bounds__(LayoutTc<D, C>::kThreads, 1)
         }
         fence_proxy_async_smem();
         tc_fence_before();
-        warp_arrive(&p_ready[wg]);
+        warp_arrive(&p_ready[buf]);
       }
       x += n;
       if (ok && wk.masked() && !have_mask)
@@ -660,10 +627,10 @@ __global__ void __launch_bounds__(LayoutTc<D, C>::kThreads, 1)
       // ---- l over the warp's keys
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(l_empty, (seg & 1) ^ 1, ctl, kSiteLseEmpty));
       if (ok) {
-        const float sum = lane_sums<C>(l);
-        if (lane < C) {
-          sum_l[warp * C + lane] = sum;
-          if ((warp & 3) == 0) sum_m[wg * C + lane] = lm;
+        const float sum = lane_sums(l);
+        if (lane < kCols) {
+          sum_l[warp * kCols + lane] = sum;
+          if ((warp & 3) == 0) sum_m[wg * kCols + lane] = lm;
         }
       }
       warp_arrive(l_full);
@@ -689,7 +656,7 @@ cudaError_t launch_tc(const CUtensorMap &tk, const CUtensorMap &tv, const Tree8P
   auto kern = fa_tree_fp8_tc_kernel<D, C>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kRequest);
   if (e != cudaSuccess) return e;
-  kern<<<static_cast<unsigned>(p.ranges) * p.groups, L::kThreads, L::kRequest, stream>>>(tk, tv, p);
+  kern<<<static_cast<unsigned>(p.ranges) * p.groups, kThreads, L::kRequest, stream>>>(tk, tv, p);
   return cudaGetLastError();
 }
 
