@@ -17,7 +17,7 @@
 // the CTA.  B4 H32 Hkv8 N4001 d128 (360 MB, 53 us at the copy rate): one head ahead in
 // registers 104 us, three in shared memory 92 (issue slots: 380 instructions a piece,
 // many of them addresses); one of the three tensors a CTA, addresses stepped from
-// head to head and infinities looked for by the greatest value alone 76, 0.70 of that rate.
+// head to head and infinities looked for by the greatest value alone 75, 0.71 of that rate.
 
 #include <cfloat>
 #include <cstdint>

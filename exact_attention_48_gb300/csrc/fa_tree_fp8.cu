@@ -122,12 +122,12 @@ constexpr int kWholeTiles = 8;
 // however many are used.  Both forms on the same calls, us:
 //                                       columns   rows
 //   B16 H16 T1 Nk16384, d = 128             169    254
-//                       d = 64              133    224
-//   B2 H32 Hkv8 T5 Nk100001, d = 128        101    114
-//                            d = 64          86     96
-//   B16 H16 T32 Nk16384, d = 128            231    264
-//                        d = 64             201    224
-//   B2 H32 Hkv8 T64 Nk65536, d = 128        405    157
+//                       d = 64              135    224
+//   B2 H32 Hkv8 T5 Nk100001, d = 128         94    114
+//                            d = 64          83     96
+//   B16 H16 T32 Nk16384, d = 128            216    264
+//                        d = 64             190    224
+//   B2 H32 Hkv8 T64 Nk65536, d = 128        405    157   (64 columns a CTA)
 Tree8Plan plan_tree8(int B, int H, int Hkv, int Nt, int Nk, int d) {
   Tree8Plan pl{};
   const int rows = H / Hkv * Nt;  // (below 2^31: H < 2^24, Nt <= 128)

@@ -25,19 +25,19 @@
 // 2^-10 with its tile's greatest at 2^8.  Scores, maxima, sums and O are fp32.
 //
 // What bounds it.  HBM, 2 d bytes a key: a 128-key tile takes an SM 1400 cycles of its
-// share of the traffic, its products some 560 (a tcgen05 instruction takes 60 or more
-// whatever its N) and its softmax about 10 issue slots a row and warp.  16 rows:
-// B16 H16 T1 Nk16384 (1.1 GB) 169 us, 0.97 of the copy bandwidth; B2 H32 Hkv8 T5
-// Nk100001 (0.4 GB) 104 us, where a run of 22 tiles has a start, an end and a second
-// launch to pay for.  32 rows: B16 H16 T32 Nk16384 (lengths of half on average, 0.8 GB)
-// 205 us, and the latency of a tile's way through the softmax (1950 cycles a tile with
-// three warpgroups, all that the registers hold) bounds it.  Converting codes to f16 for
-// mma.sync took 210, 170 and 470 us.  d = 64: a tile has half the bytes and takes the same
-// steps, 133 us for the first (0.54 GB, 0.61 of the copy bandwidth; 160 by mma.sync).
+// share of the traffic at d = 128, its products some 560 (a tcgen05 instruction takes 60 or
+// more whatever its N) and its softmax about 10 issue slots a row and warp.  16 rows:
+// B16 H16 T1 Nk16384 (1.1 GB) 169 us, 0.94 of the copy bandwidth.  32 rows: B16 H16 T32
+// Nk16384 (lengths of three quarters on average, 0.8 GB) 183 us, 0.67, and B2 H32 Hkv8 T5
+// Nk100001 (0.4 GB) 97 us, 0.62, where a run of 82 tiles has a start, an end and a second
+// launch to pay for: 59 % of the issue slots, and the way of a tile through its softmax
+// (1750 to 1950 cycles a tile).  d = 64: a tile has half the bytes and takes the same
+// steps, 135 us for the first (0.54 GB), 190 for the second's shape with full caches.
+// Codes converted to f16 for mma.sync took 210, 470 and 170 us, 160 and 253 at d = 64.
 //
-// CTA: three or four warpgroups of softmax, a key per thread, which take the tiles in
-// turn; one that adds up O^T, a column of V per thread; then the TMA producer, a
-// warp that issues S^T and owns TMEM, one that issues O^T (one thread
+// CTA: four warpgroups of softmax, a key per thread, which take the tiles in turn (32
+// rows: two a tile, 16 columns each); one that adds up O^T, a column of V per thread; then
+// the TMA producer, a warp that issues S^T and owns TMEM, one that issues O^T (one thread
 // for both took 1950 cycles a tile, most of them in the instructions themselves), and
 // one for q's parts and the tree's table.  TMEM: four S^T and four O^T of 2 C columns.
 // The tiles of all units form one list that is cut into equal runs (fa_runs.cuh), and a
