@@ -131,7 +131,7 @@ constexpr int kWholeTiles = 8;
 Tree8Plan plan_tree8(int B, int H, int Hkv, int Nt, int Nk, int d) {
   Tree8Plan pl{};
   const int rows = H / Hkv * Nt;  // (below 2^31: H < 2^24, Nt <= 128)
-  pl.rows = rows <= 16 ? 16 : (rows <= 32 ? 32 : 128);
+  pl.rows = rows <= 8 ? 8 : (rows <= 16 ? 16 : (rows <= 32 ? 32 : 128));
   pl.groups = (rows + pl.rows - 1) / pl.rows;
   const int per_unit = (Nk + kKeys - 1) / kKeys;
   const long long units = static_cast<long long>(B) * Hkv;

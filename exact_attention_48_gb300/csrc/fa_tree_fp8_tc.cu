@@ -62,7 +62,6 @@ constexpr float kLn2 = 0.69314718055994530942f;
 // the instruction cache: three of them took 1830 cycles a tile).  Registers: launched
 // with kLaunch a thread, split by setmaxnreg.
 constexpr int kGroups = 4, kSoftmaxWarps = 4 * kGroups, kThreads = 128 * (kGroups + 2);
-constexpr int kCols = 16;  // of a softmax warpgroup
 constexpr int kWarpAdd = kSoftmaxWarps, kWarpProducer = kWarpAdd + 4, kWarpS = kWarpProducer + 1;
 constexpr int kWarpO = kWarpProducer + 2, kWarpQ = kWarpProducer + 3;
 constexpr uint32_t kRegsLaunch = 80, kRegsSoftmax = 88, kRegsAdd = 80, kRegsControl = 48;
@@ -70,6 +69,7 @@ static_assert(128 * (kGroups * kRegsSoftmax + kRegsAdd + kRegsControl) <= kThrea
 
 template <int D, int C>
 struct LayoutTc {
+  static constexpr int kCols = C < 16 ? C : 16;           // of a softmax warpgroup
   static constexpr int kHalves = C / kCols, kSlots = kGroups / kHalves;  // warpgroups of a tile, tiles at work
   static constexpr uint32_t kTile = kKeys * D;         // a K or V tile
   // Slots of K and of V.  V tiles are asked for kLag tiles after their K: S^T runs about so far ahead of O^T, and a V
@@ -94,11 +94,11 @@ struct LayoutTc {
   static constexpr uint32_t kOffJump = kOffDead + 16;
   static constexpr uint32_t kOffRange = kOffJump + 128;
   static constexpr uint32_t kOffScan = kOffRange + 48;                    // warps' sums
-  static constexpr uint32_t kOffMost = kOffScan + 24 * 8;                 // [2][softmax warps][16] greatest e, in turn
-  static constexpr uint32_t kOffBase = kOffMost + 2 * kSoftmaxWarps * kCols * 4;  // [softmax warps][2][16]: 8 - m, l's factor
+  static constexpr uint32_t kOffMost = kOffScan + 24 * 8;                 // [2][softmax warps][kCols] greatest e, in turn
+  static constexpr uint32_t kOffBase = kOffMost + 2 * kSoftmaxWarps * kCols * 4;  // [softmax warps][2][kCols]: 8 - m, l's factor
   static constexpr uint32_t kOffTileM = kOffBase + kSoftmaxWarps * 2 * kCols * 4;  // [kTiles][C] m and the greatest vs
   static constexpr uint32_t kOffAdd = kOffTileM + kTiles * (C + 4) * 4;   // [4 warps][C]: factors of O
-  static constexpr uint32_t kOffL = kOffAdd + 4 * C * 4;                  // [softmax warps][16] l, and [groups][16] its base
+  static constexpr uint32_t kOffL = kOffAdd + 4 * C * 4;                  // [softmax warps][kCols] l, and [groups][kCols] its base
   static constexpr uint32_t kOffLm = kOffL + kSoftmaxWarps * kCols * 4;
   static constexpr uint32_t kOffRow = kOffLm + kGroups * kCols * 4;           // [kSegs][C] rows' factors
   static constexpr uint32_t kOffBar = kOffRow + kSegs * C * 4;
@@ -114,12 +114,13 @@ struct LayoutTc {
   static_assert(kRequest <= 232448, "shared memory budget");
 };
 
-// Sums over the warp's lanes of 16 values each: lane l gets the sum of value l % 16,
-// in a fixed order.
-__device__ __forceinline__ float lane_sums(float (&v)[16]) {
+// Sums over the warp's lanes of N values each: lane l gets the sum of value l % N, in a
+// fixed order.
+template <int N>
+__device__ __forceinline__ float lane_sums(float (&v)[N]) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int o = 8; o; o >>= 1) {
+  for (int o = N / 2; o; o >>= 1) {
     const bool up = lane & o;
 #pragma unroll
     for (int x = 0; x < o; ++x) {
@@ -127,7 +128,27 @@ __device__ __forceinline__ float lane_sums(float (&v)[16]) {
       v[x] = keep + __shfl_xor_sync(0xffffffffu, send, o);
     }
   }
-  return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 16);
+#pragma unroll
+  for (int o = N; o < 32; o <<= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+  return v[0];
+}
+
+// N columns' two parts, of this thread's lane: hi at `at`, lo C columns on.
+template <int C, int N>
+__device__ __forceinline__ void tmem_parts(uint32_t at, uint32_t (&hi)[N], uint32_t (&lo)[N]) {
+  if constexpr (N == 16) {
+    tmem_ld16(at, hi);
+    tmem_ld16(at + C, lo);
+    tmem_ld_wait16(hi);
+    tmem_ld_wait16(lo);
+  } else {
+    static_assert(N == 8 && C == 8, "side by side");
+    uint32_t w[16];
+    tmem_ld16(at, w);
+    tmem_ld_wait16(w);
+#pragma unroll
+    for (int y = 0; y < 8; ++y) hi[y] = w[y], lo[y] = w[8 + y];
+  }
 }
 
 template <int D, int C>
@@ -135,6 +156,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fa_tree_fp8_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                           const Tree8Params p) {
   using L = LayoutTc<D, C>;
+  constexpr int kCols = L::kCols;
   constexpr int kAddWarps = D / 32;  // with columns of V
   constexpr int SK = L::kSlotsK, SV = L::kSlotsV, NB = L::kBufs, kLag = L::kLag;
   // (lane l of a warp looks after column l % C where a thing is done once a column)
@@ -403,14 +425,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const uint32_t at = tmem + (NB + buf) * 2 * C + lane_base;
 #pragma unroll
-        for (int r = 0; r < C; r += 16) {
-          uint32_t hi[16], lo[16];
-          tmem_ld16(at + r, hi);
-          tmem_ld16(at + C + r, lo);
-          tmem_ld_wait16(hi);
-          tmem_ld_wait16(lo);
+        for (int r = 0; r < C; r += kCols) {
+          uint32_t hi[kCols], lo[kCols];
+          tmem_parts<C>(at + r, hi, lo);
 #pragma unroll
-          for (int y = 0; y < 16; y += 4) {
+          for (int y = 0; y < kCols; y += 4) {
             const float4 f = *reinterpret_cast<const float4 *>(fac + r + y);
             o[r + y] = fmaf(__uint_as_float(hi[y]) + __uint_as_float(lo[y]), f.x, o[r + y]);
             o[r + y + 1] = fmaf(__uint_as_float(hi[y + 1]) + __uint_as_float(lo[y + 1]), f.y, o[r + y + 1]);
@@ -526,10 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t at = tmem + buf * 2 * C + c0 + lane_base;
         {
           uint32_t hi[kCols], lo[kCols];
-          tmem_ld16(at, hi);
-          tmem_ld16(at + C, lo);
-          tmem_ld_wait16(hi);
-          tmem_ld_wait16(lo);
+          tmem_parts<C>(at, hi, lo);
 #pragma unroll
           for (int y = 0; y < kCols; y += 2) {
             const float2 f = *reinterpret_cast<const float2 *>(rf + y);
@@ -587,9 +603,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           continue;
         uint8_t *ptile = sP + buf * L::kPTile;
         {
-          uint32_t hi[4], lo[4];
+          uint32_t hi[kCols / 4], lo[kCols / 4];
 #pragma unroll
-          for (int y = 0; y < 16; y += 4) {
+          for (int y = 0; y < kCols; y += 4) {
             const float4 b = *reinterpret_cast<const float4 *>(base + y);
             const float4 g = *reinterpret_cast<const float4 *>(base + kCols + y);
             const float2 e0 = fadd2(make_float2(s[y], s[y + 1]), make_float2(b.x, b.y));
@@ -605,8 +621,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             l[y + 3] = n1.y;
             parts_of(w0, w1, w2, w3, &hi[y / 4], &lo[y / 4]);
           }
-          *reinterpret_cast<uint4 *>(ptile + piece_at<64>(key, c0 / 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4 *>(ptile + piece_at<64>(key, (c0 + C) / 16)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          if constexpr (kCols == 16) {
+            *reinterpret_cast<uint4 *>(ptile + piece_at<64>(key, c0 / 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4 *>(ptile + piece_at<64>(key, (c0 + C) / 16)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          } else {
+            *reinterpret_cast<uint4 *>(ptile + piece_at<64>(key, 0)) = make_uint4(hi[0], hi[1], lo[0], lo[1]);
+          }
         }
         if (masked) {
           // V rows that no query row sees become zeros (0 * NaN is NaN)
@@ -663,8 +683,12 @@ cudaError_t launch_tc(const CUtensorMap &tk, const CUtensorMap &tv, const Tree8P
 }  // namespace
 
 cudaError_t launch_tree8_tc(const CUtensorMap &tk, const CUtensorMap &tv, const Tree8Params &p, cudaStream_t stream) {
-  if (p.d == 64) return p.rows == 16 ? launch_tc<64, 16>(tk, tv, p, stream) : launch_tc<64, 32>(tk, tv, p, stream);
-  return p.rows == 16 ? launch_tc<128, 16>(tk, tv, p, stream) : launch_tc<128, 32>(tk, tv, p, stream);
+  const bool d64 = p.d == 64;
+  switch (p.rows) {
+    case 8: return d64 ? launch_tc<64, 8>(tk, tv, p, stream) : launch_tc<128, 8>(tk, tv, p, stream);
+    case 16: return d64 ? launch_tc<64, 16>(tk, tv, p, stream) : launch_tc<128, 16>(tk, tv, p, stream);
+    default: return d64 ? launch_tc<64, 32>(tk, tv, p, stream) : launch_tc<128, 32>(tk, tv, p, stream);
+  }
 }
 
 }  // namespace fa
