@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++seg;
         const uint64_t dq = desc_add(dQ, qb * L::kQ);
         for (int j = wk.k0; j < wk.k1; ++j) {
-          if (!(ok = mbar_wait(&s_free[buf], bph, ctl, kSiteSFree) && mbar_wait(&k_full[sl], sph, ctl, kSiteKFull))) break;
+          if (!(ok = mbar_wait_both(&s_free[buf], bph, kSiteSFree, &k_full[sl], sph, kSiteKFull, ctl))) break;
           tc_fence_after();
           const uint64_t dk = desc_add(dT, sl * L::kTile);
 #pragma unroll
@@ -253,8 +253,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t total = static_cast<uint32_t>(wk.end - wk.t);
       uint32_t sl = 0, sph = 0, buf = 0, bph = 0;  // V's slot and its phase, the weights' buffer and its phase
       for (uint32_t y = 0; y < total; ++y) {
-        if (!(mbar_wait(&v_full[sl], sph, ctl, kSiteVFull) && mbar_wait(o_empty, (y & 1) ^ 1, ctl, kSiteDqEmpty) &&
-              mbar_wait(&p_ready[buf], bph, ctl, kSitePReady)))
+        if (!(mbar_wait_both(&v_full[sl], sph, kSiteVFull, &p_ready[buf], bph, kSitePReady, ctl) &&
+              mbar_wait(o_empty, (y & 1) ^ 1, ctl, kSiteDqEmpty)))
           break;
         tc_fence_after();
         const uint64_t dv = desc_add(dT, sl * L::kTile);

@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t dq = desc_add(dQ, qb * L::kQ);
         for (int j = wk.k0; j < wk.k1; ++j, ++i) {
           const uint32_t buf = i % NB;
-          if (!(ok = mbar_wait(&s_free[buf], bph, ctl, kSiteSFree) && mbar_wait(&k_full[sl], sph, ctl, kSiteKFull))) break;
+          if (!(ok = mbar_wait_both(&s_free[buf], bph, kSiteSFree, &k_full[sl], sph, kSiteKFull, ctl))) break;
           tc_fence_after();
           const uint64_t dk = desc_add(dT, sl * L::kTile);
 #pragma unroll
@@ -328,12 +328,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t kIdO = idesc_e4m3(128, 2 * C, true, true);
       const uint64_t dT = sdesc_codes<D>(ring_v, L::kTile), dP = sdesc_codes<64>(sP);
       const uint32_t total = static_cast<uint32_t>(wk.end - wk.t);
-      uint32_t sl = 0, sph = 0, bph = 1;  // V's slot and its phase, the buffer's
+      uint32_t sl = 0, sph = 0, bph = 0;  // V's slot and its phase, the buffer's
       for (uint32_t y = 0; y < total; ++y) {
         const uint32_t buf = y % NB;
-        if (!(mbar_wait(&v_full[sl], sph, ctl, kSiteVFull) && mbar_wait(&o_empty[buf], bph, ctl, kSiteDqEmpty) &&
-              mbar_wait(&p_ready[buf], bph ^ 1, ctl, kSitePReady)))
-          break;
+        // (O^T's buffer is free as well: its weights were written when tile y - NB had been added up)
+        if (!mbar_wait_both(&v_full[sl], sph, kSiteVFull, &p_ready[buf], bph, kSitePReady, ctl)) break;
         tc_fence_after();
         const uint64_t dv = desc_add(dT, sl * L::kTile), dp = desc_add(dP, buf * L::kPTile);
 #pragma unroll

@@ -171,6 +171,14 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, const 
   }
 }
 
+// Waits for two barriers, looked at together: a wait that finds its barrier done takes
+// some 140 cycles, most of them latency.
+__device__ __forceinline__ bool mbar_wait_both(uint64_t *a, uint32_t parity_a, int site_a, uint64_t *b, uint32_t parity_b,
+                                               int site_b, const WaitCtl &ctl) {
+  const bool x = mbar_try_wait(a, parity_a), y = mbar_try_wait(b, parity_b);
+  return (x || mbar_wait(a, parity_a, ctl, site_a)) && (y || mbar_wait(b, parity_b, ctl, site_b));
+}
+
 // acc.x += the low bf16 of b, acc.y += the high bf16 of b: mixed-precision
 // adds (sm_100+), the bf16 -> f32 widening is exact and each add rounds once.
 __device__ __forceinline__ float2 add_bf16x2_f32(float2 acc, uint32_t b) {
