@@ -43,14 +43,14 @@ constexpr float kLn2 = 0.69314718055994530942f;
 // Register split: 640 threads launched with 96 each.
 constexpr uint32_t kRegsSoftmax = 104, kRegsAdd = 104, kRegsControl = 64;
 static_assert(256 * kRegsSoftmax + 256 * kRegsAdd + 128 * kRegsControl <= kThreads * 96, "register split");
+static_assert(kRegsSoftmax >= 96 && kRegsAdd >= 96 && kRegsControl <= 96, "setmaxnreg goes up or down only");
 
 template <int D>
 struct LayoutRows {
   static constexpr uint32_t kTile = kKeys * D;         // a K or V tile, or one part of q
-  static constexpr int kSlotsK = D == 128 ? 4 : 8, kSlotsV = kSlotsK + 1;
   // V tiles are asked for kLag tiles after their K (S runs about so far ahead of O).
   static constexpr int kLag = 2;
-  static constexpr int kBufs = 3;                      // of S
+  static constexpr int kBufs = 3;                      // of S, and slots of K and of V
   static constexpr uint32_t kTmem = 512, kO = kBufs * 128;
   static constexpr uint32_t kQ = 2 * kTile;            // both parts; two segments' in turn
   // first the small things, then (1 KB aligned) the ring and q
@@ -65,12 +65,12 @@ struct LayoutRows {
   static constexpr uint32_t kOffL = kOffTileV + 16;                // [2][128] l, [2][128] its base
   static constexpr uint32_t kOffRow = kOffL + 4 * kRows * 4;       // [3 segments][128] rows' factors
   static constexpr uint32_t kOffBar = kOffRow + 3 * kRows * 4;
-  // k_full[], k_empty[], v_full[], v_empty[], s_full[3], s_free[3], p_ready[3], q_full[2], pv_done, o_empty, mask_full,
-  // mask_empty, l_full, l_empty, drain[2]
-  static constexpr int kNumBars = 2 * (kSlotsK + kSlotsV) + 3 * kBufs + 2 + 8;
+  // k_full[3], v_full[3], s_full[3], p_ready[3], pv_done[3], q_full[2], o_empty, mask_full, mask_empty, l_full, l_empty,
+  // drain[2]
+  static constexpr int kNumBars = 5 * kBufs + 2 + 7;
   static constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;     // TMEM address, abort flag
   static constexpr uint32_t kSmall = (kOffMisc + 16 + 15) / 16 * 16;
-  static constexpr uint32_t kRing = (kSlotsK + kSlotsV) * kTile;
+  static constexpr uint32_t kRing = 2 * kBufs * kTile;
   static constexpr uint32_t kRequest = kSmall + 1008 + kRing + 2 * kQ;
   static_assert(kOffBar % 8 == 0 && kOffRange % 8 == 0 && kOffScan % 8 == 0 && kOffScale % 16 == 0, "alignment");
   static_assert(kRequest <= 232448, "shared memory budget");
@@ -81,25 +81,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     fa_tree_fp8_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                             const Tree8Params p) {
   using L = LayoutRows<D>;
-  constexpr int SK = L::kSlotsK, SV = L::kSlotsV, NB = L::kBufs, kLag = L::kLag;
+  constexpr int NB = L::kBufs, kLag = L::kLag;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *small = smem_raw;
   uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + L::kSmall + 1023) &
                                               ~uintptr_t(1023));
-  uint8_t *ring_v = ring + SK * L::kTile, *sQ = ring + L::kRing;
+  uint8_t *ring_v = ring + NB * L::kTile, *sQ = ring + L::kRing;
   uint32_t *bits = reinterpret_cast<uint32_t *>(small + L::kOffBits);
   uint32_t *dead = reinterpret_cast<uint32_t *>(small + L::kOffDead);
   RunStart *run = reinterpret_cast<RunStart *>(small + L::kOffRange);
   auto floats = [&](uint32_t off) { return reinterpret_cast<float *>(small + off); };
   float *tile_m = floats(L::kOffTileM), *tile_v = floats(L::kOffTileV), *row_f = floats(L::kOffRow);
   float *sum_l = floats(L::kOffL), *sum_m = sum_l + 2 * kRows;
-  uint64_t *k_full = reinterpret_cast<uint64_t *>(small + L::kOffBar), *k_empty = k_full + SK;
-  uint64_t *v_full = k_empty + SK, *v_empty = v_full + SV;
-  // Tile x of the run uses s_full, s_free and p_ready number x % 3 (a p_ready for each warpgroup would not do: a
-  // warpgroup may be through with its next tile before the issuer has looked).  No wait can find its barrier two
-  // phases on: what would complete the next phase waits for what the waiter does after this one.
-  uint64_t *s_full = v_empty + SV, *s_free = s_full + NB, *p_ready = s_free + NB, *q_full = p_ready + NB;
-  uint64_t *pv_done = q_full + 2, *o_empty = pv_done + 1, *mask_full = o_empty + 1, *mask_empty = mask_full + 1;
+  uint64_t *k_full = reinterpret_cast<uint64_t *>(small + L::kOffBar), *v_full = k_full + NB;
+  // Tile x of the run uses slot, buffer and barrier number x % 3 of each kind (a p_ready for each warpgroup would not do:
+  // a warpgroup may be through with its next tile before the issuer has looked); s_full tells that K's slot is free as
+  // well, pv_done that V's and S's are.  No wait can find its barrier two phases on: what would complete the next phase
+  // waits for what the waiter does after this one.
+  uint64_t *s_full = v_full + NB, *p_ready = s_full + NB, *pv_done = p_ready + NB, *q_full = pv_done + NB;
+  uint64_t *o_empty = q_full + 2, *mask_full = o_empty + 1, *mask_empty = mask_full + 1;
   uint64_t *l_full = mask_empty + 1, *l_empty = l_full + 1, *drain = l_empty + 1;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(small + L::kOffMisc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(small + L::kOffMisc + 4);
@@ -111,24 +111,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int rows = min(kRows, unit_rows - first_row), warps = (rows + 31) / 32;  // of a warpgroup, with rows
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < SK; ++i) {
-      mbar_init(&k_full[i], 1);
-      mbar_init(&k_empty[i], 1);
-    }
-    for (int i = 0; i < SV; ++i) {
-      mbar_init(&v_full[i], 1);
-      mbar_init(&v_empty[i], 1);
-    }
     for (int i = 0; i < NB; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&v_full[i], 1);
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_free[i], 1);
+      mbar_init(&pv_done[i], 1);
       mbar_init(&p_ready[i], warps);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], warps);
       mbar_init(&drain[i], 1);
     }
-    mbar_init(pv_done, 1);
     mbar_init(o_empty, 2 * warps);
     mbar_init(mask_full, 1);
     mbar_init(mask_empty, 4 * warps);
@@ -179,11 +172,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             left = wk.k1 - wk.k0;
             row = wk.k0 * kKeys;
           }
-          if (!(ok = mbar_wait(&k_empty[ks], kph, ctl, kSiteKEmpty))) break;
+          if (!(ok = mbar_wait(&s_full[ks], kph, ctl, kSiteKEmpty))) break;
           mbar_arrive_expect_tx(&k_full[ks], L::kTile);
           tma_load_4d(ring + ks * L::kTile, &tm_k, &k_full[ks], 0, row, wk.hk, wk.b);
           ++nk;
-          if (++ks == SK) {
+          if (++ks == NB) {
             ks = 0;
             kph ^= 1;
           }
@@ -192,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           --left;
         }
         if (y >= kLag) {
-          if (!(ok = mbar_wait(&v_empty[vs], vph, ctl, kSiteVEmpty))) break;
+          if (!(ok = mbar_wait(&pv_done[vs], vph, ctl, kSiteVEmpty))) break;
 #ifdef FA_TEST_SKIP_FIRST_V_LOAD
           // Test builds only: the run's first V tile is never loaded, so the wait
           // for it runs out and the bounded-wait path is taken.
@@ -203,21 +196,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_4d(ring_v + vs * L::kTile, &tm_v, &v_full[vs], 0, v.x, v.y, v.z);
           }
           ++nv;
-          if (++vs == SV) {
+          if (++vs == NB) {
             vs = 0;
             vph ^= 1;
           }
         }
       }
       // every copy issued lands before this thread leaves (bounded waits)
-      for (uint32_t i = nk > SK ? nk - SK : 0; i < nk; ++i) mbar_drain(&k_full[i % SK], (i / SK) & 1);
-      for (uint32_t i = nv > SV ? nv - SV : 0; i < nv; ++i) mbar_drain(&v_full[i % SV], (i / SV) & 1);
+      for (uint32_t i = nk > NB ? nk - NB : 0; i < nk; ++i) mbar_drain(&k_full[i % NB], (i / NB) & 1);
+      for (uint32_t i = nv > NB ? nv - NB : 0; i < nv; ++i) mbar_drain(&v_full[i % NB], (i / NB) & 1);
     } else if (warp == kWarpS && lane == 0) {
       // ---------------------------------------------------------- S = Q K^T
       constexpr uint32_t kIdS = idesc_e4m3(kRows, kKeys, false, false);
       constexpr int kSteps = D / 32;
       const uint64_t dQ = sdesc_codes<D>(sQ), dT = sdesc_codes<D>(ring);
-      uint32_t seg = 0, sl = 0, sph = 0, buf = 0, bph = 1;  // segment, K's slot and its phase, S's buffer and its phase
+      uint32_t seg = 0, buf = 0, ph = 0;  // segment, buffer and slot, their phase
       bool ok = true;
       while (ok && wk.next()) {
         const uint32_t qb = seg & 1;
@@ -225,22 +218,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++seg;
         const uint64_t dq = desc_add(dQ, qb * L::kQ);
         for (int j = wk.k0; j < wk.k1; ++j) {
-          if (!(ok = mbar_wait_both(&s_free[buf], bph, kSiteSFree, &k_full[sl], sph, kSiteKFull, ctl))) break;
+          if (!(ok = mbar_wait_both(&pv_done[buf], ph ^ 1, kSiteSFree, &k_full[buf], ph, kSiteKFull, ctl))) break;
           tc_fence_after();
-          const uint64_t dk = desc_add(dT, sl * L::kTile);
+          const uint64_t dk = desc_add(dT, buf * L::kTile);
 #pragma unroll
           for (int kk = 0; kk < 2 * kSteps; ++kk)  // both parts of q, one after the other
             mma_ss_f8(tmem + buf * 128, desc_add(dq, kk / kSteps * L::kTile + kk % kSteps * 32),
                       desc_add(dk, kk % kSteps * 32), kIdS, kk > 0 ? 1u : 0u);
           tc_commit(&s_full[buf]);
-          tc_commit(&k_empty[sl]);
-          if (++sl == SK) {
-            sl = 0;
-            sph ^= 1;
-          }
           if (++buf == NB) {
             buf = 0;
-            bph ^= 1;
+            ph ^= 1;
           }
         }
       }
@@ -251,29 +239,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t kIdO = idesc_e4m3(kRows, D, false, true);
       const uint64_t dT = sdesc_codes<D>(ring_v);
       const uint32_t total = static_cast<uint32_t>(wk.end - wk.t);
-      uint32_t sl = 0, sph = 0, buf = 0, bph = 0;  // V's slot and its phase, the weights' buffer and its phase
+      uint32_t buf = 0, ph = 0;  // buffer and slot, their phase
       for (uint32_t y = 0; y < total; ++y) {
-        if (!(mbar_wait_both(&v_full[sl], sph, kSiteVFull, &p_ready[buf], bph, kSitePReady, ctl) &&
+        if (!(mbar_wait_both(&v_full[buf], ph, kSiteVFull, &p_ready[buf], ph, kSitePReady, ctl) &&
               mbar_wait(o_empty, (y & 1) ^ 1, ctl, kSiteDqEmpty)))
           break;
         tc_fence_after();
-        const uint64_t dv = desc_add(dT, sl * L::kTile);
+        const uint64_t dv = desc_add(dT, buf * L::kTile);
         const uint32_t tp = tmem + buf * 128;
 #pragma unroll
         for (int kk = 0; kk < kKeys / 32; ++kk) {
           mma_ts_f8(tmem + L::kO, tp + kk * 16, desc_add(dv, kk * 32 * D), kIdO, kk > 0 ? 1u : 0u);
           mma_ts_f8(tmem + L::kO, tp + kk * 16 + 8, desc_add(dv, kk * 32 * D), kIdO, 1u);
         }
-        tc_commit(pv_done);
-        tc_commit(&s_free[buf]);
-        tc_commit(&v_empty[sl]);
-        if (++sl == SV) {
-          sl = 0;
-          sph ^= 1;
-        }
+        tc_commit(&pv_done[buf]);
         if (++buf == NB) {
           buf = 0;
-          bph ^= 1;
+          ph ^= 1;
         }
       }
       tc_commit(&drain[1]);
@@ -337,6 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool more = first && wn.next();
     if (first) load_q(wn, 0);
     uint32_t x = 0, seg = 0, nmask = 0;
+    uint32_t buf = 0, ph = 0;  // tile x's, and its phase
     bool ok = true;
     while (wk.next()) {
       if (threadIdx.x == kWarpAdd * 32 && group == 0 && p.cuts && wk.k0 == 0 && (!wk.tail || p.cuts_by_unit))
@@ -349,7 +332,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int y = 0; y < D / 2; ++y) o[y] = 0.0f;
       float M = -INFINITY;
       for (int kt = wk.k0; ok && kt < wk.k1; ++kt, ++x) {
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(pv_done, x & 1, ctl, kSitePvDone)))) break;
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[buf], ph, ctl, kSitePvDone)))) break;
+        if (++buf == NB) {
+          buf = 0;
+          ph ^= 1;
+        }
         tc_fence_after();
         const float m = tile_m[(x & 3) * kRows + r], vs = tile_v[x & 3];
         const bool move = m > M + kMoveBy;
@@ -566,11 +553,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (r == 0) tile_v[y0 & 3] = vmax;
         if (masked) {
           // V rows that no query row sees become zeros (0 * NaN is NaN)
-          if (!(ok = __all_sync(0xffffffffu, mbar_wait(&v_full[y0 % SV], (y0 / SV) & 1, ctl, kSiteVFull)))) break;
+          if (!(ok = __all_sync(0xffffffffu, mbar_wait(&v_full[buf], bph, ctl, kSiteVFull)))) break;
           for (int key = r; key < kKeys; key += warps * 32) {
             const int i = n0 + key;
             if (i < p.Nt && (i < 0 || !((dead[i >> 5] >> (i & 31)) & 1u))) continue;
-            uint4 *v = reinterpret_cast<uint4 *>(ring_v + (y0 % SV) * L::kTile + key * D);
+            uint4 *v = reinterpret_cast<uint4 *>(ring_v + buf * L::kTile + key * D);
 #pragma unroll
             for (int y = 0; y < D / 16; ++y) v[y] = make_uint4(0u, 0u, 0u, 0u);
           }

@@ -60,29 +60,32 @@ constexpr float kLn2 = 0.69314718055994530942f;
 // control warps.  A softmax warpgroup takes 16 columns of a tile: with 32 columns two
 // share a tile (one with all 32 would need 112 registers, and code that does not stay in
 // the instruction cache: three of them took 1830 cycles a tile).  Registers: launched
-// with kLaunch a thread, split by setmaxnreg.
+// with kRegsLaunch a thread, split by setmaxnreg.
 constexpr int kGroups = 4, kSoftmaxWarps = 4 * kGroups, kThreads = 128 * (kGroups + 2);
 constexpr int kWarpAdd = kSoftmaxWarps, kWarpProducer = kWarpAdd + 4, kWarpS = kWarpProducer + 1;
 constexpr int kWarpO = kWarpProducer + 2, kWarpQ = kWarpProducer + 3;
 constexpr uint32_t kRegsLaunch = 80, kRegsSoftmax = 88, kRegsAdd = 80, kRegsControl = 48;
 static_assert(128 * (kGroups * kRegsSoftmax + kRegsAdd + kRegsControl) <= kThreads * kRegsLaunch, "register split");
+static_assert(kRegsSoftmax >= kRegsLaunch && kRegsAdd >= kRegsLaunch && kRegsControl <= kRegsLaunch,
+              "setmaxnreg goes up or down only");
 
 template <int D, int C>
 struct LayoutTc {
   static constexpr int kCols = C < 16 ? C : 16;           // of a softmax warpgroup
-  static constexpr int kHalves = C / kCols, kSlots = kGroups / kHalves;  // warpgroups of a tile, tiles at work
+  static constexpr int kHalves = C / kCols, kAtWork = kGroups / kHalves;  // warpgroups of a tile, tiles at work
   static constexpr uint32_t kTile = kKeys * D;         // a K or V tile
-  // Slots of K and of V.  V tiles are asked for kLag tiles after their K: S^T runs about so far ahead of O^T, and a V
+  // Slots of K and of V: as many as buffers, so that the barrier of a product tells of its operand's slot as well (a
+  // commit of its own for it costs the issuers: B16 H16 T32 Nk16384 203 us for 215, five slots of V and all).  V tiles are asked for kLag tiles after their K: S^T runs about so far ahead of O^T, and a V
   // tile that came with its K would hold its slot meanwhile.
-  static constexpr int kSlotsK = D == 128 ? 4 : 8, kSlotsV = kSlotsK + 1, kLag = 3;
   static constexpr int kBufs = 4;                      // of S^T, and of O^T
+  static constexpr int kSlots = kBufs, kLag = 3;
   static constexpr uint32_t kTmem = 2 * kBufs * 2 * C;
   static_assert(kTmem <= 512, "TMEM columns");
   // How many of what one role leaves to another are used in turn.
-  // A tile's maxima: tile x + 8's are written by warpgroups that saw tile x + 4 - kSlots added up at their tile before,
+  // A tile's maxima: tile x + 8's are written by warpgroups that saw tile x + 4 - kAtWork added up at their tile before,
   // or a later one, so x; buffer x % kBufs of the weights is free when tile x - kBufs has been added up.
   static constexpr int kTiles = 8;
-  static_assert(kBufs >= kSlots && kTiles >= kBufs + kSlots, "tile x's maxima have been read by then");
+  static_assert(kBufs >= kAtWork && kTiles >= kBufs + kAtWork, "tile x's maxima have been read by then");
   // A segment's row factors: segment n + NB + 3's are written when S^T of segment n + NB + 1 is done, so that of a tile
   // beyond x + NB, x any of segment n's, and that takes tile x's scores read.
   static constexpr int kSegs = 8;
@@ -102,12 +105,12 @@ struct LayoutTc {
   static constexpr uint32_t kOffLm = kOffL + kSoftmaxWarps * kCols * 4;
   static constexpr uint32_t kOffRow = kOffLm + kGroups * kCols * 4;           // [kSegs][C] rows' factors
   static constexpr uint32_t kOffBar = kOffRow + kSegs * C * 4;
-  // k_full[], k_empty[], v_full[], v_empty[], s_full[bufs], s_free[bufs], pv_done[bufs], o_empty[bufs], p_ready[bufs], q_full[2], q_empty[2],
+  // k_full[slots], v_full[slots], s_full[bufs], s_free[bufs], pv_done[bufs], o_empty[bufs], p_ready[bufs], q_full[2], q_empty[2],
   // mask_full, mask_empty, l_full, l_empty, drain[2]
-  static constexpr int kNumBars = 2 * (kSlotsK + kSlotsV) + 5 * kBufs + 10;
+  static constexpr int kNumBars = 2 * kSlots + 5 * kBufs + 10;
   static constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;            // TMEM address, abort flag
   static constexpr uint32_t kSmall = (kOffMisc + 16 + 15) / 16 * 16;
-  static constexpr uint32_t kRing = (kSlotsK + kSlotsV) * kTile;
+  static constexpr uint32_t kRing = 2 * kSlots * kTile;
   static constexpr uint32_t kPTile = kKeys * 64, kP = kBufs * kPTile;  // weights: 64 bytes a key, 2 C used
   static constexpr uint32_t kRequest = kSmall + 1008 + kRing + kP + 2 * kQ;
   static_assert(kOffBar % 8 == 0 && kOffRange % 8 == 0 && kOffScan % 8 == 0 && kOffMost % 16 == 0, "alignment");
@@ -158,24 +161,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   using L = LayoutTc<D, C>;
   constexpr int kCols = L::kCols;
   constexpr int kAddWarps = D / 32;  // with columns of V
-  constexpr int SK = L::kSlotsK, SV = L::kSlotsV, NB = L::kBufs, kLag = L::kLag;
+  constexpr int NB = L::kBufs, kLag = L::kLag;
   // (lane l of a warp looks after column l % C where a thing is done once a column)
   extern __shared__ uint8_t smem_raw[];
   uint8_t *small = smem_raw;
   uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + L::kSmall + 1023) &
                                               ~uintptr_t(1023));
-  uint8_t *ring_v = ring + SK * L::kTile, *sP = ring + L::kRing, *sQ = sP + L::kP;
+  uint8_t *ring_v = ring + NB * L::kTile, *sP = ring + L::kRing, *sQ = sP + L::kP;
   uint32_t *bits = reinterpret_cast<uint32_t *>(small + L::kOffBits);
   uint32_t *dead = reinterpret_cast<uint32_t *>(small + L::kOffDead);
   RunStart *run = reinterpret_cast<RunStart *>(small + L::kOffRange);
   auto floats = [&](uint32_t off) { return reinterpret_cast<float *>(small + off); };
   float *tile_m = floats(L::kOffTileM), *row_f = floats(L::kOffRow);
   float *sum_l = floats(L::kOffL), *sum_m = floats(L::kOffLm);
-  uint64_t *k_full = reinterpret_cast<uint64_t *>(small + L::kOffBar), *k_empty = k_full + SK;
-  uint64_t *v_full = k_empty + SK, *v_empty = v_full + SV;
+  uint64_t *k_full = reinterpret_cast<uint64_t *>(small + L::kOffBar), *v_full = k_full + NB;
   // Tile x of the run uses number x % NB of the buffers' barriers.  No wait can find its barrier two phases on: tile
   // x + NB's product waits for what tile x's readers arrive on, and its weights for tile x's sums.
-  uint64_t *s_full = v_empty + SV, *s_free = s_full + NB, *pv_done = s_free + NB, *o_empty = pv_done + NB;
+  uint64_t *s_full = v_full + NB, *s_free = s_full + NB, *pv_done = s_free + NB, *o_empty = pv_done + NB;
   uint64_t *p_ready = o_empty + NB;
   uint64_t *q_full = p_ready + NB, *q_empty = q_full + 2, *mask_full = q_empty + 2, *mask_empty = mask_full + 1;
   uint64_t *l_full = mask_empty + 1, *l_empty = l_full + 1, *drain = l_empty + 1;
@@ -188,15 +190,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int first_row = group * C, unit_rows = p.G * p.Nt;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < SK; ++i) {
-      mbar_init(&k_full[i], 1);
-      mbar_init(&k_empty[i], 1);
-    }
-    for (int i = 0; i < SV; ++i) {
-      mbar_init(&v_full[i], 1);
-      mbar_init(&v_empty[i], 1);
-    }
     for (int i = 0; i < NB; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&v_full[i], 1);
       mbar_init(&s_full[i], 1);
       mbar_init(&s_free[i], 4 * L::kHalves);
       mbar_init(&p_ready[i], 4 * L::kHalves);
@@ -258,11 +254,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             left = wk.k1 - wk.k0;
             row = wk.k0 * kKeys;
           }
-          if (!(ok = mbar_wait(&k_empty[ks], kph, ctl, kSiteKEmpty))) break;
+          // (the slot's last tile has been multiplied)
+          if (!(ok = mbar_wait(&s_full[ks], kph, ctl, kSiteKEmpty))) break;
           mbar_arrive_expect_tx(&k_full[ks], L::kTile);
           tma_load_4d(ring + ks * L::kTile, &tm_k, &k_full[ks], 0, row, wk.hk, wk.b);
           ++nk;
-          if (++ks == SK) {
+          if (++ks == NB) {
             ks = 0;
             kph ^= 1;
           }
@@ -271,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           --left;
         }
         if (y >= kLag) {
-          if (!(ok = mbar_wait(&v_empty[vs], vph, ctl, kSiteVEmpty))) break;
+          if (!(ok = mbar_wait(&pv_done[vs], vph, ctl, kSiteVEmpty))) break;
 #ifdef FA_TEST_SKIP_FIRST_V_LOAD
           // Test builds only: the run's first V tile is never loaded, so the wait
           // for it runs out and the bounded-wait path is taken.
@@ -282,41 +279,38 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_4d(ring_v + vs * L::kTile, &tm_v, &v_full[vs], 0, v.x, v.y, v.z);
           }
           ++nv;
-          if (++vs == SV) {
+          if (++vs == NB) {
             vs = 0;
             vph ^= 1;
           }
         }
       }
       // every copy issued lands before this thread leaves (bounded waits)
-      for (uint32_t i = nk > SK ? nk - SK : 0; i < nk; ++i) mbar_drain(&k_full[i % SK], (i / SK) & 1);
-      for (uint32_t i = nv > SV ? nv - SV : 0; i < nv; ++i) mbar_drain(&v_full[i % SV], (i / SV) & 1);
+      for (uint32_t i = nk > NB ? nk - NB : 0; i < nk; ++i) mbar_drain(&k_full[i % NB], (i / NB) & 1);
+      for (uint32_t i = nv > NB ? nv - NB : 0; i < nv; ++i) mbar_drain(&v_full[i % NB], (i / NB) & 1);
     } else if (warp == kWarpS && lane == 0) {
       // ---------------------------------------------------------- S^T = K Q^T
       constexpr uint32_t kIdS = idesc_e4m3(kKeys, 2 * C, false, false);
       const uint64_t dQ = sdesc_codes<D>(sQ), dT = sdesc_codes<D>(ring);
-      uint32_t i = 0, seg = 0, sl = 0, sph = 0, bph = 1;  // tile, segment, K's slot and its phase, the buffer's
+      uint32_t seg = 0, buf = 0, ph = 0;  // segment, buffer and slot, their phase
       bool ok = true;
       while (ok && wk.next()) {
         const uint32_t qb = seg & 1;
         if (!(ok = mbar_wait(&q_full[qb], (seg >> 1) & 1, ctl, kSiteQFull))) break;
         ++seg;
         const uint64_t dq = desc_add(dQ, qb * L::kQ);
-        for (int j = wk.k0; j < wk.k1; ++j, ++i) {
-          const uint32_t buf = i % NB;
-          if (!(ok = mbar_wait_both(&s_free[buf], bph, kSiteSFree, &k_full[sl], sph, kSiteKFull, ctl))) break;
+        for (int j = wk.k0; j < wk.k1; ++j) {
+          if (!(ok = mbar_wait_both(&s_free[buf], ph ^ 1, kSiteSFree, &k_full[buf], ph, kSiteKFull, ctl))) break;
           tc_fence_after();
-          const uint64_t dk = desc_add(dT, sl * L::kTile);
+          const uint64_t dk = desc_add(dT, buf * L::kTile);
 #pragma unroll
           for (int kk = 0; kk < D / 32; ++kk)
             mma_ss_f8(tmem + buf * 2 * C, desc_add(dk, kk * 32), desc_add(dq, kk * 32), kIdS, kk > 0 ? 1u : 0u);
           tc_commit(&s_full[buf]);
-          tc_commit(&k_empty[sl]);
-          if (++sl == SK) {
-            sl = 0;
-            sph ^= 1;
+          if (++buf == NB) {
+            buf = 0;
+            ph ^= 1;
           }
-          if (buf == NB - 1) bph ^= 1;
         }
         tc_commit(&q_empty[qb]);
       }
@@ -328,23 +322,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t kIdO = idesc_e4m3(128, 2 * C, true, true);
       const uint64_t dT = sdesc_codes<D>(ring_v, L::kTile), dP = sdesc_codes<64>(sP);
       const uint32_t total = static_cast<uint32_t>(wk.end - wk.t);
-      uint32_t sl = 0, sph = 0, bph = 0;  // V's slot and its phase, the buffer's
+      uint32_t buf = 0, ph = 0;  // buffer and slot, their phase
       for (uint32_t y = 0; y < total; ++y) {
-        const uint32_t buf = y % NB;
         // (O^T's buffer is free as well: its weights were written when tile y - NB had been added up)
-        if (!mbar_wait_both(&v_full[sl], sph, kSiteVFull, &p_ready[buf], bph, kSitePReady, ctl)) break;
+        if (!mbar_wait_both(&v_full[buf], ph, kSiteVFull, &p_ready[buf], ph, kSitePReady, ctl)) break;
         tc_fence_after();
-        const uint64_t dv = desc_add(dT, sl * L::kTile), dp = desc_add(dP, buf * L::kPTile);
+        const uint64_t dv = desc_add(dT, buf * L::kTile), dp = desc_add(dP, buf * L::kPTile);
 #pragma unroll
         for (int kk = 0; kk < kKeys / 32; ++kk)
           mma_ss_f8(tmem + (NB + buf) * 2 * C, desc_add(dv, kk * 32 * D), desc_add(dp, kk * 2048), kIdO, kk > 0 ? 1u : 0u);
         tc_commit(&pv_done[buf]);
-        tc_commit(&v_empty[sl]);
-        if (++sl == SV) {
-          sl = 0;
-          sph ^= 1;
+        if (++buf == NB) {
+          buf = 0;
+          ph ^= 1;
         }
-        if (buf == NB - 1) bph ^= 1;
       }
       tc_commit(&drain[1]);
       mbar_drain(&drain[1], 0);
@@ -448,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int row = first_row + mine;
         float l = 0.0f;
 #pragma unroll
-        for (int w = 0; w < 4 * L::kSlots; ++w) {
+        for (int w = 0; w < 4 * L::kAtWork; ++w) {
           const int wg = (w >> 2) * L::kHalves + mine / kCols, col = mine % kCols;
           const float m = sum_m[wg * kCols + col], v = sum_l[(wg * 4 + (w & 3)) * kCols + col];
           l += m == -INFINITY ? v : v * ex2(m - M);
@@ -496,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ------------------------------------------------------------ softmax, a key per thread, 16 columns
     regs_increase<kRegsSoftmax>();
-    constexpr int W = L::kSlots;
+    constexpr int W = L::kAtWork;
     const int wg = warp >> 2, key = threadIdx.x & 127, mine = lane & (kCols - 1);
     const int c0 = wg % L::kHalves * kCols;  // its first column
         float *base = floats(L::kOffBase) + warp * 2 * kCols;  // 8 - m, then l's factor
@@ -628,10 +619,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (masked) {
-          // V rows that no query row sees become zeros (0 * NaN is NaN)
-          if (!(ok = __all_sync(0xffffffffu, mbar_wait(&v_full[y0 % SV], (y0 / SV) & 1, ctl, kSiteVFull)))) continue;
+          // V rows that no query row sees become zeros (0 * NaN is NaN).  (The buffer's number is worked out anew here: one
+          // more register for it above is spilled, 215 us for 203.)
+          if (!(ok = __all_sync(0xffffffffu, mbar_wait(&v_full[y0 % NB], (y0 / NB) & 1, ctl, kSiteVFull)))) continue;
           if (c0 == 0 && (node >= p.Nt || (node >= 0 && ((dead[node >> 5] >> (node & 31)) & 1u)))) {
-            uint4 *v = reinterpret_cast<uint4 *>(ring_v + (y0 % SV) * L::kTile + key * D);
+            uint4 *v = reinterpret_cast<uint4 *>(ring_v + (y0 % NB) * L::kTile + key * D);
 #pragma unroll
             for (int y = 0; y < D / 16; ++y) v[y] = make_uint4(0u, 0u, 0u, 0u);
           }
