@@ -44,7 +44,7 @@ Tree8Plan plan_tree8(int B, int H, int Hkv, int Nt, int Nk, int d);
 // tk, tv: maps of encode_map_rows8 with boxes of 128 rows.
 cudaError_t launch_tree8(const CUtensorMap &tk, const CUtensorMap &tv, const Tree8Params &p, bool merge,
                          cudaStream_t stream);
-// Its main kernels at d = 128: 16 rows, 128 rows.
+// Its main kernels: groups of 8, 16 or 32 rows, and of 128.
 cudaError_t launch_tree8_tc(const CUtensorMap &tk, const CUtensorMap &tv, const Tree8Params &p, cudaStream_t stream);
 cudaError_t launch_tree8_rows(const CUtensorMap &tk, const CUtensorMap &tv, const Tree8Params &p, cudaStream_t stream);
 

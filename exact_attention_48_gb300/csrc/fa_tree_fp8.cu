@@ -117,17 +117,19 @@ cudaError_t launch_merge8(const Tree8Params &p, cudaStream_t stream) {
 // Short caches are not cut inside a unit: see plan_tree.
 constexpr int kWholeTiles = 8;
 
-// Rows of a group (a CTA's): 16 or 32 as columns of the transposed products
+// Rows of a group (a CTA's): 8, 16 or 32 as columns of the transposed products
 // (fa_tree_fp8_tc.cu), or 128 as lanes (fa_tree_fp8_rows.cu), which cost the same
-// however many are used.  Both forms on the same calls, us:
-//                                       columns   rows
-//   B16 H16 T1 Nk16384, d = 128             169    254
-//                       d = 64              135    224
-//   B2 H32 Hkv8 T5 Nk100001, d = 128         94    114
-//                            d = 64          83     96
-//   B16 H16 T32 Nk16384, d = 128            216    264
-//                        d = 64             190    224
-//   B2 H32 Hkv8 T64 Nk65536, d = 128        405    157   (64 columns a CTA)
+// however many are used.  The forms on the same calls, us:
+//                                       columns         lanes
+//   B16 H16 T1 Nk16384, d = 128             162 (8)     254
+//                                           168 (16)
+//                       d = 64              110 (8)     224
+//                                           135 (16)
+//   B2 H32 Hkv8 T5 Nk100001, d = 128         87 (32)    114
+//                            d = 64          82 (32)     96
+//   B16 H16 T32 Nk16384, d = 128            203 (32)    264
+//                        d = 64             187 (32)    224
+//   B2 H32 Hkv8 T64 Nk65536, d = 128        405 (64)    157
 Tree8Plan plan_tree8(int B, int H, int Hkv, int Nt, int Nk, int d) {
   Tree8Plan pl{};
   const int rows = H / Hkv * Nt;  // (below 2^31: H < 2^24, Nt <= 128)

@@ -26,13 +26,13 @@
 //
 // What bounds it.  HBM, 2 d bytes a key: a 128-key tile takes an SM 1400 cycles of its
 // share of the traffic at d = 128, its products some 560 (a tcgen05 instruction takes 60 or
-// more whatever its N) and its softmax about 10 issue slots a row and warp.  16 rows:
-// B16 H16 T1 Nk16384 (1.1 GB) 169 us, 0.94 of the copy bandwidth.  32 rows: B16 H16 T32
-// Nk16384 (lengths of three quarters on average, 0.8 GB) 183 us, 0.67, and B2 H32 Hkv8 T5
-// Nk100001 (0.4 GB) 97 us, 0.62, where a run of 82 tiles has a start, an end and a second
-// launch to pay for: 59 % of the issue slots, and the way of a tile through its softmax
-// (1750 to 1950 cycles a tile).  d = 64: a tile has half the bytes and takes the same
-// steps, 135 us for the first (0.54 GB), 190 for the second's shape with full caches.
+// more whatever its N) and its softmax about 10 issue slots a row and warp.  Up to 8
+// rows: B16 H16 T1 Nk16384 (1.1 GB) 162 us, 0.98 of the copy bandwidth.  32 rows: B16 H16
+// T32 Nk16384 (lengths of three quarters on average, 0.8 GB) 171 us, 0.72, and B2 H32 Hkv8
+// T5 Nk100001 (0.4 GB) 89 us, 0.68, where a run of 82 tiles has a start, an end and a
+// second launch to pay for: 63 % of the issue slots, and the way of a tile through
+// its softmax (1750 cycles a tile).  d = 64: a tile has half the bytes and takes the same
+// steps, 110 us for the first (0.54 GB), 187 for the second's shape with full caches.
 // Codes converted to f16 for mma.sync took 210, 470 and 170 us, 160 and 253 at d = 64.
 //
 // CTA: four warpgroups of softmax, a key per thread, which take the tiles in turn (32

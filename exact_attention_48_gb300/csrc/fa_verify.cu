@@ -159,6 +159,8 @@ __global__ void __launch_bounds__(kThreads, 2) fa_verify_kernel(const VerifyPara
   cg::cluster_group cluster = cg::this_cluster();
   const int ranks = p.ranks, rank = blockIdx.x % ranks, b = blockIdx.x / ranks;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // (all of the cluster's CTAs have to have started before one writes to another's shared memory: waited for below)
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;");
   const bool drafted = p.draft != nullptr;
   // this CTA's share of a row, and the warps' tiles in it
   const int share = (p.V + ranks - 1) / ranks;
@@ -184,6 +186,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_verify_kernel(const VerifyPara
   }
   if (tid == 0) s.sums[0] = Pair{1.0f, 0.0f};
   __syncthreads();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   if (s.parent[0] != -1) {  // (the same for the whole cluster)
     if (rank == 0) {
       for (int i = tid; i < p.Nt; i += kThreads) accepted[i] = -1;
