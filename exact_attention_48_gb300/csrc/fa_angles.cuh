@@ -45,11 +45,15 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// The cosine and sine of the angle that a position makes with a frequency.
-__device__ __forceinline__ void angle_of(long long pos, float f, float *cs, float *sn) {
-  const uint64_t a = static_cast<uint64_t>(pos) * turn_fraction(f);
+// The cosine and sine of the angle that a position makes with a frequency, or with its
+// fraction of a turn.
+__device__ __forceinline__ void angle_of(long long pos, uint64_t turns, float *cs, float *sn) {
+  const uint64_t a = static_cast<uint64_t>(pos) * turns;
   const float half_turns = static_cast<float>(static_cast<int32_t>(a >> 32)) * 4.656612873077393e-10f;  // 2^-31
   sincospif(half_turns, sn, cs);
+}
+__device__ __forceinline__ void angle_of(long long pos, float f, float *cs, float *sn) {
+  angle_of(pos, turn_fraction(f), cs, sn);
 }
 
 // A thread's two 16-byte pieces of a row.  Neighbouring threads take

@@ -17,7 +17,9 @@
 // the CTA.  B4 H32 Hkv8 N4001 d128 (360 MB, 53 us at the copy rate): one head ahead in
 // registers 104 us, three in shared memory 92 (issue slots: 380 instructions a piece,
 // many of them addresses); one of the three tensors a CTA, addresses stepped from
-// head to head and infinities looked for by the greatest value alone 75, 0.71 of that rate.
+// head to head and infinities looked for by the greatest value alone 76, 0.70 of that rate.  A CTA
+// works out its tokens' angles itself (some 50 instructions each): with as few CTAs as
+// fill the SMs B16 H16 Hkv1 N1500 d64 takes 23 us, with four times as many 29.
 
 #include <cfloat>
 #include <cstdint>
@@ -41,6 +43,7 @@ __device__ __forceinline__ void copy16(void *dst, const void *src) {
 template <bool INTERLEAVED, int kThreads>
 __global__ void __launch_bounds__(kThreads, 1024 / kThreads) fa_append_fp8_kernel(const Append8Params p) {
   extern __shared__ float4 shared[];  // rows on their way [kAhead][2][threads]
+  __shared__ uint64_t turns[64];              // the pairs' fractions of a turn
   __shared__ uint32_t most[3][kThreads / 4];  // greatest values of the heads at work, used in turn
   const int per_row = p.d >> 4, tid = threadIdx.x;
   const int lanes = per_row * p.slots;
@@ -84,7 +87,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) fa_append_fp8_kerne
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) ask(i);
 
+  if (!is_v && tid < p.rot / 2) turns[tid] = turn_fraction(p.inv_freq[tid]);
   for (int i = tid; i < 3 * (kThreads / 4); i += kThreads) most[i / (kThreads / 4)][i % (kThreads / 4)] = 0u;
+  __syncthreads();
   // the angles of this thread's pairs (threads of other heads and of other CTAs compute the same ones: cheaper than
   // to share them where a thread keeps them for all of its heads)
   float cs[8], sn[8];
@@ -95,12 +100,11 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) fa_append_fp8_kerne
       cs[i] = 1.0f;
       sn[i] = 0.0f;
       if (!(i < 4 ? x.t0 : x.t1)) continue;
-      angle_of(pos, p.inv_freq[i < 4 ? x.p0 + i : x.p1 + i - 4], &cs[i], &sn[i]);
+      angle_of(pos, turns[i < 4 ? x.p0 + i : x.p1 + i - 4], &cs[i], &sn[i]);
       cs[i] *= p.factor;
       sn[i] *= p.factor;
     }
   }
-  __syncthreads();
 
   const long long row = from + slot;
   uint8_t *head8 = is_v ? p.vc + b * p.svc.b + first * p.svc.h : p.kc + b * p.skc.b + first * p.skc.h;
@@ -239,9 +243,9 @@ cudaError_t launch_append8(bool interleaved, const Append8Params &in, cudaStream
   p.per_b = (p.N - 1 + block - 1) / block + 1;
   p.slots = 1;
   while (p.slots < p.N && p.slots < block) p.slots *= 2;
-  // Groups of heads: some four CTAs an SM in all, in proportion to the heads, while each has heads for them
+  // Groups of heads, in proportion to the heads: a CTA an SM in all (each one works out its tokens' angles)
   const int at_once = threads_of(p) / (p.slots * (p.d / 16));
-  const long long blocks = static_cast<long long>(p.B) * p.per_b, want = (4 * 152 + blocks - 1) / blocks;
+  const long long blocks = static_cast<long long>(p.B) * p.per_b, want = (152 + blocks - 1) / blocks;
   auto groups = [&](int heads) {
     const long long most = (heads + at_once - 1) / at_once, share = (want * heads + p.H + 2 * p.Hkv - 1) / (p.H + 2 * p.Hkv);
     const long long g = share < most ? share : most;
