@@ -98,12 +98,12 @@ def run(g, B, H, Hkv, Nt, Nk, d, block, layout="bhnd", lens=None, parents=None, 
     (1, 8, 1, 1, 5000, 128, 16, "pitch"),
     (1, 8, 1, 1, 5000, 64, 128, "pitch"),
     (3, 6, 6, 3, 700, 64, 64, "bhnd"),
-    (2, 16, 2, 2, 3001, 128, 32, "bnhd"),      # 16 rows: one row tile
-    (2, 17, 1, 1, 2100, 128, 64, "bhnd"),      # 17: two
+    (2, 16, 2, 2, 3001, 128, 32, "bnhd"),      # 16 rows a cache head
+    (2, 17, 1, 1, 2100, 128, 64, "bhnd"),      # 17
     (1, 8, 2, 8, 2500, 64, 64, "bhnd"),        # 32
-    (1, 4, 1, 9, 2500, 128, 64, "bhnd"),       # 36: four, one of them empty
+    (1, 4, 1, 9, 2500, 128, 64, "bhnd"),       # 36
     (1, 8, 1, 8, 1500, 64, 16, "bnhd"),        # 64
-    (1, 4, 2, 33, 3000, 128, 128, "bhnd"),     # 66: eight, three of them empty
+    (1, 4, 2, 33, 3000, 128, 128, "bhnd"),     # 66
     (1, 2, 2, 128, 2000, 64, 64, "bhnd"),      # 128
     (1, 3, 1, 64, 1100, 128, 32, "bhnd"),      # 192 rows: two groups
     (1, 16, 1, 128, 1300, 64, 64, "bhnd"),     # 2048 rows: 16 groups
@@ -124,9 +124,9 @@ def test_long_and_many_units():
 
 
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("G,Nt", [(4, 4), (17, 1), (2, 16), (1, 33), (4, 16), (5, 13), (2, 64), (43, 3), (8, 40)])
+@pytest.mark.parametrize("G,Nt", [(8, 1), (3, 3), (1, 7), (4, 4), (17, 1), (2, 16), (1, 33), (4, 16), (5, 13), (2, 64), (43, 3), (8, 40)])
 def test_rows_of_a_group(G, Nt, d):
-    """Query rows of a cache head around the kernels' 16, 32 and 128, over caches whose units are cut by the runs' ends,
+    """Query rows of a cache head around the kernels' 8, 16, 32 and 128, over caches whose units are cut by the runs' ends,
     and of which a run holds several."""
     g = ref.gen(2020 + G + Nt)
     run(g, 3, 5 * G, 5, Nt, 2900, d, 64, "bnhd", [2900, 2000, 1300], tree_of(g, 3, Nt), heads=[(0, 0), (0, 4), (1, 2), (2, 0)])
