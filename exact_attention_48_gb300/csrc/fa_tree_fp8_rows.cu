@@ -12,17 +12,17 @@
 // What bounds it.  The products at d = 128: 16 instructions of 128 x 128 x 32 a tile, 90
 // cycles each, 1440 cycles of a tile of 128 keys and 128 rows, as many as its share of
 // the HBM traffic takes (1400).  A softmax takes a warp some 700 instructions.
-// B2 H32 Hkv8 Nt64 Nk65536 (two CTAs a tile of 128 rows each): 157 us, 2100 cycles a
-// tile, the way from a tile's O to the next one's start.  d = 64: 130 us.
+// B2 H32 Hkv8 Nt64 Nk65536 (256 rows, two CTAs a tile): 157 us, 2100 cycles a tile, the
+// way from a tile's O to the next one's start.  d = 64: 129 us.
 //
 // CTA (640 threads): warps 0..3 and 4..7 softmax, a row per thread, alternate tiles;
 // warps 8..11 and 12..15 add up O in registers, half a row per thread (one warpgroup
 // alone held the next product up: 182 us for B2 H32 Hkv8 Nt64 Nk65536), the first of
 // them brings q's parts; warp 16 TMA producer, warp 17 issues S and owns TMEM, warp 18
-// issues O, warp 19 the tree's table.  TMEM: three S of 128 columns (S of tile x + 2 is formed while tile x's
-// weights, over its S, still wait for their product) and O.  The tiles of all units
-// form one list that is cut into equal runs (fa_runs.cuh), and a CTA's products run on
-// from unit to unit.
+// issues O, warp 19 the tree's table.  TMEM: three S of 128 columns (S of tile x + 2 is
+// formed while tile x's weights, over its S, still wait for their product) and O.  The
+// tiles of all units form one list that is cut into equal runs (fa_runs.cuh), and a
+// CTA's products run on from unit to unit.
 
 #include <cstdint>
 

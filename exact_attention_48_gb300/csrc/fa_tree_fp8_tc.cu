@@ -74,10 +74,10 @@ struct LayoutTc {
   static constexpr int kCols = C < 16 ? C : 16;           // of a softmax warpgroup
   static constexpr int kHalves = C / kCols, kAtWork = kGroups / kHalves;  // warpgroups of a tile, tiles at work
   static constexpr uint32_t kTile = kKeys * D;         // a K or V tile
-  // Slots of K and of V: as many as buffers, so that the barrier of a product tells of its operand's slot as well (a
-  // commit of its own for it costs the issuers: B16 H16 T32 Nk16384 203 us for 215, five slots of V and all).  V tiles are asked for kLag tiles after their K: S^T runs about so far ahead of O^T, and a V
-  // tile that came with its K would hold its slot meanwhile.
   static constexpr int kBufs = 4;                      // of S^T, and of O^T
+  // Slots of K and of V: as many as buffers, so that the barrier of a product tells of its operand's slot as well (a
+  // commit of its own for that: B16 H16 T32 Nk16384, full caches, 215 us for 203).  V tiles are asked for kLag tiles
+  // after their K: S^T runs about so far ahead of O^T, and a V tile that came with its K would hold its slot meanwhile.
   static constexpr int kSlots = kBufs, kLag = 3;
   static constexpr uint32_t kTmem = 2 * kBufs * 2 * C;
   static_assert(kTmem <= 512, "TMEM columns");
@@ -98,15 +98,15 @@ struct LayoutTc {
   static constexpr uint32_t kOffRange = kOffJump + 128;
   static constexpr uint32_t kOffScan = kOffRange + 48;                    // warps' sums
   static constexpr uint32_t kOffMost = kOffScan + 24 * 8;                 // [2][softmax warps][kCols] greatest e, in turn
-  static constexpr uint32_t kOffBase = kOffMost + 2 * kSoftmaxWarps * kCols * 4;  // [softmax warps][2][kCols]: 8 - m, l's factor
+  static constexpr uint32_t kOffBase = kOffMost + 2 * kSoftmaxWarps * kCols * 4;   // [softmax warps][2][kCols]: 8 - m, l's factor
   static constexpr uint32_t kOffTileM = kOffBase + kSoftmaxWarps * 2 * kCols * 4;  // [kTiles][C] m and the greatest vs
   static constexpr uint32_t kOffAdd = kOffTileM + kTiles * (C + 4) * 4;   // [4 warps][C]: factors of O
   static constexpr uint32_t kOffL = kOffAdd + 4 * C * 4;                  // [softmax warps][kCols] l, and [groups][kCols] its base
   static constexpr uint32_t kOffLm = kOffL + kSoftmaxWarps * kCols * 4;
   static constexpr uint32_t kOffRow = kOffLm + kGroups * kCols * 4;           // [kSegs][C] rows' factors
   static constexpr uint32_t kOffBar = kOffRow + kSegs * C * 4;
-  // k_full[slots], v_full[slots], s_full[bufs], s_free[bufs], pv_done[bufs], o_empty[bufs], p_ready[bufs], q_full[2], q_empty[2],
-  // mask_full, mask_empty, l_full, l_empty, drain[2]
+  // k_full[slots], v_full[slots], s_full[bufs], s_free[bufs], pv_done[bufs], o_empty[bufs], p_ready[bufs], q_full[2],
+  // q_empty[2], mask_full, mask_empty, l_full, l_empty, drain[2]
   static constexpr int kNumBars = 2 * kSlots + 5 * kBufs + 10;
   static constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;            // TMEM address, abort flag
   static constexpr uint32_t kSmall = (kOffMisc + 16 + 15) / 16 * 16;
