@@ -19,7 +19,7 @@
 // cluster barrier a window lets the first of them write a window's scales only when
 // all have read them.  The next window's rows and the list after it are on their way
 // meanwhile (a later window's sources lie behind the rows written here).  B16 Hkv16 16384 to
-// 8192 rows d128 301 us; B1 Hkv2 131072 to 65536 rows 246 us, 1214 with a CTA a head.
+// 8192 rows d128 300 us; B1 Hkv2 131072 to 65536 rows 159 us, 1214 with a CTA a head.
 
 #include <cstdint>
 
@@ -135,13 +135,13 @@ __device__ __forceinline__ void meet(int log2_cluster) {
 constexpr int kSlideItems = 4;  // rows of a thread
 
 // In place.  grid: x = (head, K or V, rank in the cluster).  A row takes t = 2^lt threads
-// of a CTA, a window 1024 / t rows.
-template <int D>
-__global__ void __launch_bounds__(kThreads, 4) fa_compact_fp8_slide_kernel(const Compact8Params p, int windows,
-                                                                        int log2_cluster) {
-  constexpr int kLogPieces = D == 128 ? 3 : 2, kMostBlocks = 1024 / 16;
+// of a CTA, a window 4 T / t rows.
+template <int D, int T>
+__global__ void __launch_bounds__(T, 1024 / T) fa_compact_fp8_slide_kernel(const Compact8Params p, int windows,
+                                                                           int log2_cluster) {
+  constexpr int kLogPieces = D == 128 ? 3 : 2, kMostBlocks = T * kSlideItems / 16;
   __shared__ uint32_t most[3][kMostBlocks], moved[3][kMostBlocks];  // used in turn
-  const int tid = threadIdx.x, lt = kLogPieces - log2_cluster, step = kThreads >> lt, window = step * kSlideItems;
+  const int tid = threadIdx.x, lt = kLogPieces - log2_cluster, step = T >> lt, window = step * kSlideItems;
   const int rank = blockIdx.x & ((1 << log2_cluster) - 1), of = blockIdx.x >> log2_cluster;
   const int tensor = of & 1, bh = of >> 1, b = bh / p.Hkv, h = bh - b * p.Hkv;
   const int c = (rank << lt) + (tid & ((1 << lt) - 1)), first = tid >> lt;  // column piece, row of the window
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kThreads, 4) fa_compact_fp8_slide_kernel(const
   const long long shared_blk = (base > 0 ? base : 0) >> p.block_log2;            // rows before base in it stay, and count
   const int *kept = p.kept + b * p.kept_b + h * p.kept_h;
   const Side x = side_of(p, tensor, b, h);
-  for (int i = tid; i < kMostBlocks; i += kThreads) most[0][i] = moved[0][i] = 0u;
+  for (int i = tid; i < kMostBlocks; i += T) most[0][i] = moved[0][i] = 0u;
 
   // The rows that move to the thread's rows of window i: an old row, or -1.
   int from[kSlideItems];
@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 4) fa_compact_fp8_slide_kernel(const
     __syncthreads();  // the counts are zero
     read(i + 1);
     list(i + 2);
-    for (int j = tid; j < kMostBlocks; j += kThreads) most[next_turn][j] = moved[next_turn][j] = 0u;
+    for (int j = tid; j < kMostBlocks; j += T) most[next_turn][j] = moved[next_turn][j] = 0u;
 #pragma unroll
     for (int it = 0; it < kSlideItems; ++it) {
       const int row = it * step + first;
@@ -222,25 +222,34 @@ __global__ void __launch_bounds__(kThreads, 4) fa_compact_fp8_slide_kernel(const
 
 }  // namespace
 
-template <int D>
-static cudaError_t launch_slide(const Compact8Params &p, cudaStream_t stream) {
-  const long long heads = static_cast<long long>(p.B) * p.Hkv * 2;
-  // some two CTAs an SM, where a window has rows for them
-  int lc = 0;
-  while ((16 << (lc + 1)) <= D && heads << (lc + 1) <= 304 && p.M > (kThreads * kSlideItems * 16 / D) << lc) ++lc;
-  const int window = (kThreads * kSlideItems * 16 / D) << lc;
+template <int D, int T>
+static cudaError_t launch_slide(const Compact8Params &p, int log2_cluster, cudaStream_t stream) {
+  const int window = (T * kSlideItems * 16 / D) << log2_cluster;
   const int windows = static_cast<int>((static_cast<long long>(p.M) + (p.base ? kWindow - 1 : 0) + window - 1) / window);
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(heads << lc));  // (heads below 2^25)
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long long>(p.B) * p.Hkv * 2 << log2_cluster));  // (below 2^26)
+  cfg.blockDim = dim3(T);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 1u << lc;
+  attr[0].val.clusterDim.x = 1u << log2_cluster;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = lc ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, fa_compact_fp8_slide_kernel<D>, p, windows, lc);
+  cfg.numAttrs = log2_cluster ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, fa_compact_fp8_slide_kernel<D, T>, p, windows, log2_cluster);
+}
+
+// Some two CTAs an SM at most, where a window has rows for them; where that leaves SMs idle, CTAs of 1024 threads, whose
+// windows are four times as long (a window takes some 4 us, whatever it holds: B1 Hkv2 131072 to 65536 rows 159 us, 246
+// with 256).
+template <int D>
+static cudaError_t launch_slide(const Compact8Params &p, cudaStream_t stream) {
+  const long long heads = static_cast<long long>(p.B) * p.Hkv * 2;
+  constexpr int kWindow256 = kThreads * kSlideItems * 16 / D;
+  int lc = 0;
+  while ((16 << (lc + 1)) <= D && heads << (lc + 1) <= 304 && p.M > kWindow256 << lc) ++lc;
+  return heads << lc <= 152 && p.M > kWindow256 << lc ? launch_slide<D, 1024>(p, lc, stream)
+                                                      : launch_slide<D, kThreads>(p, lc, stream);
 }
 
 cudaError_t launch_compact8(const Compact8Params &p, cudaStream_t stream) {
