@@ -13,14 +13,15 @@
 // cycles each, 1440 cycles of a tile of 128 keys and 128 rows, as many as its share of
 // the HBM traffic takes (1400).  A softmax takes a warp some 700 instructions.
 // B2 H32 Hkv8 Nt64 Nk65536 (256 rows, two CTAs a tile): 157 us, 2100 cycles a tile, the
-// way from a tile's O to the next one's start.  d = 64: 129 us.
+// way from a tile's O to the next one's start.  d = 64: 127 us (129 with two warpgroups of
+// softmax and one O), the way of a tile through its S: product, softmax, product.
 //
-// CTA (640 threads): warps 0..3 and 4..7 softmax, a row per thread, alternate tiles;
-// warps 8..11 and 12..15 add up O in registers, half a row per thread (one warpgroup
-// alone held the next product up: 182 us for B2 H32 Hkv8 Nt64 Nk65536), the first of
-// them brings q's parts; warp 16 TMA producer, warp 17 issues S and owns TMEM, warp 18
+// CTA (640 threads): two warpgroups of softmax (three at d = 64), a row per thread, which
+// take the tiles in turn; two (one) that add up O in registers, 64 columns of a row per
+// thread (at d = 128 one alone held the next product up: 182 us for B2 H32 Hkv8 Nt64
+// Nk65536), the first of them brings q's parts; warp 16 TMA producer, warp 17 issues S and owns TMEM, warp 18
 // issues O, warp 19 the tree's table.  TMEM: three S of 128 columns (S of tile x + 2 is
-// formed while tile x's weights, over its S, still wait for their product) and O.  The
+// formed while tile x's weights, over its S, still wait for their product) and O, or two O of 64.  The
 // tiles of all units form one list that is cut into equal runs (fa_runs.cuh), and a
 // CTA's products run on from unit to unit.
 
@@ -36,22 +37,28 @@ namespace {
 
 constexpr int kRows = 128;
 constexpr int kThreads = 640;
-constexpr int kWarpAdd = 8, kWarpProducer = 16, kWarpS = 17, kWarpO = 18, kWarpMask = 19;
+constexpr int kWarpProducer = 16, kWarpS = 17, kWarpO = 18, kWarpMask = 19;
 constexpr float kMoveBy = 8.0f;   // a running maximum moves only when exceeded by more (log2 units)
 constexpr float kLift = 8.0f;     // weights reach 2^kLift
 constexpr float kLn2 = 0.69314718055994530942f;
 // Register split: 640 threads launched with 96 each.
 constexpr uint32_t kRegsSoftmax = 104, kRegsAdd = 104, kRegsControl = 64;
-static_assert(256 * kRegsSoftmax + 256 * kRegsAdd + 128 * kRegsControl <= kThreads * 96, "register split");
+static_assert(kRegsSoftmax == kRegsAdd && 512 * kRegsSoftmax + 128 * kRegsControl <= kThreads * 96, "register split");
 static_assert(kRegsSoftmax >= 96 && kRegsAdd >= 96 && kRegsControl <= 96, "setmaxnreg goes up or down only");
 
 template <int D>
 struct LayoutRows {
+  // Four warpgroups: of softmax, and to add up O, 64 columns each.
+  static constexpr int kAdd = D / 64, kSoft = 4 - kAdd, kWarpAdd = 4 * kSoft;
   static constexpr uint32_t kTile = kKeys * D;         // a K or V tile, or one part of q
   // V tiles are asked for kLag tiles after their K (S runs about so far ahead of O).
   static constexpr int kLag = 2;
   static constexpr int kBufs = 3;                      // of S, and slots of K and of V
   static constexpr uint32_t kTmem = 512, kO = kBufs * 128;
+  static constexpr int kOs = (kTmem - kO) / D;         // O buffers: 1, or 2 at d = 64
+  // A tile's maxima are kept for 8 tiles: tile x + 8's come after S of it, so after O of tile x + 5, which waits for tile
+  // x + 5 - kOs' sums, tile x's among them.
+  static constexpr int kTiles = 8;
   static constexpr uint32_t kQ = 2 * kTile;            // both parts; two segments' in turn
   // first the small things, then (1 KB aligned) the ring and q
   static constexpr uint32_t kOffBits = 0;
@@ -59,15 +66,15 @@ struct LayoutRows {
   static constexpr uint32_t kOffJump = kOffDead + 16;
   static constexpr uint32_t kOffRange = kOffJump + 128;
   static constexpr uint32_t kOffScan = kOffRange + 48;             // 20 warps' sums
-  static constexpr uint32_t kOffScale = kOffScan + 20 * 8;         // [8 warps][3][8]: a tile's scales
-  static constexpr uint32_t kOffTileM = kOffScale + 8 * 24 * 4;    // [4 tiles][128] m, and [4] the greatest vs
-  static constexpr uint32_t kOffTileV = kOffTileM + 4 * kRows * 4;
-  static constexpr uint32_t kOffL = kOffTileV + 16;                // [2][128] l, [2][128] its base
-  static constexpr uint32_t kOffRow = kOffL + 4 * kRows * 4;       // [3 segments][128] rows' factors
+  static constexpr uint32_t kOffScale = kOffScan + 20 * 8;         // [softmax warps][3][8]: a tile's scales
+  static constexpr uint32_t kOffTileM = kOffScale + kWarpAdd * 24 * 4;    // [tiles][128] m, and [tiles] the greatest vs
+  static constexpr uint32_t kOffTileV = kOffTileM + kTiles * kRows * 4;
+  static constexpr uint32_t kOffL = kOffTileV + kTiles * 4;              // [kSoft][128] l, [kSoft][128] its base
+  static constexpr uint32_t kOffRow = kOffL + 2 * kSoft * kRows * 4;       // [3 segments][128] rows' factors
   static constexpr uint32_t kOffBar = kOffRow + 3 * kRows * 4;
-  // k_full[3], v_full[3], s_full[3], p_ready[3], pv_done[3], q_full[2], o_empty, mask_full, mask_empty, l_full, l_empty,
-  // drain[2]
-  static constexpr int kNumBars = 5 * kBufs + 2 + 7;
+  // k_full[3], v_full[3], s_full[3], p_ready[3], pv_done[3], q_full[2], o_empty[2], mask_full, mask_empty, l_full,
+  // l_empty, drain[2]
+  static constexpr int kNumBars = 5 * kBufs + 2 + 8;
   static constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;     // TMEM address, abort flag
   static constexpr uint32_t kSmall = (kOffMisc + 16 + 15) / 16 * 16;
   static constexpr uint32_t kRing = 2 * kBufs * kTile;
@@ -81,7 +88,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     fa_tree_fp8_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                             const Tree8Params p) {
   using L = LayoutRows<D>;
-  constexpr int NB = L::kBufs, kLag = L::kLag;
+  constexpr int NB = L::kBufs, NO = L::kOs, kLag = L::kLag, W = L::kSoft, kWarpAdd = L::kWarpAdd;
+  constexpr int kCols = 64;  // of O, a thread
   extern __shared__ uint8_t smem_raw[];
   uint8_t *small = smem_raw;
   uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + L::kSmall + 1023) &
@@ -92,14 +100,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   RunStart *run = reinterpret_cast<RunStart *>(small + L::kOffRange);
   auto floats = [&](uint32_t off) { return reinterpret_cast<float *>(small + off); };
   float *tile_m = floats(L::kOffTileM), *tile_v = floats(L::kOffTileV), *row_f = floats(L::kOffRow);
-  float *sum_l = floats(L::kOffL), *sum_m = sum_l + 2 * kRows;
+  float *sum_l = floats(L::kOffL), *sum_m = sum_l + L::kSoft * kRows;
   uint64_t *k_full = reinterpret_cast<uint64_t *>(small + L::kOffBar), *v_full = k_full + NB;
   // Tile x of the run uses slot, buffer and barrier number x % 3 of each kind (a p_ready for each warpgroup would not do:
   // a warpgroup may be through with its next tile before the issuer has looked); s_full tells that K's slot is free as
   // well, pv_done that V's and S's are.  No wait can find its barrier two phases on: what would complete the next phase
   // waits for what the waiter does after this one.
   uint64_t *s_full = v_full + NB, *p_ready = s_full + NB, *pv_done = p_ready + NB, *q_full = pv_done + NB;
-  uint64_t *o_empty = q_full + 2, *mask_full = o_empty + 1, *mask_empty = mask_full + 1;
+  uint64_t *o_empty = q_full + 2, *mask_full = o_empty + 2, *mask_empty = mask_full + 1;
   uint64_t *l_full = mask_empty + 1, *l_empty = l_full + 1, *drain = l_empty + 1;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(small + L::kOffMisc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(small + L::kOffMisc + 4);
@@ -120,13 +128,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], warps);
+      mbar_init(&o_empty[i], L::kAdd * warps);
       mbar_init(&drain[i], 1);
     }
-    mbar_init(o_empty, 2 * warps);
     mbar_init(mask_full, 1);
     mbar_init(mask_empty, 4 * warps);
-    mbar_init(l_full, 2 * warps);
-    mbar_init(l_empty, 2 * warps);
+    mbar_init(l_full, W * warps);
+    mbar_init(l_empty, L::kAdd * warps);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -242,15 +250,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t buf = 0, ph = 0;  // buffer and slot, their phase
       for (uint32_t y = 0; y < total; ++y) {
         if (!(mbar_wait_both(&v_full[buf], ph, kSiteVFull, &p_ready[buf], ph, kSitePReady, ctl) &&
-              mbar_wait(o_empty, (y & 1) ^ 1, ctl, kSiteDqEmpty)))
+              mbar_wait(&o_empty[y % NO], ((y / NO) & 1) ^ 1, ctl, kSiteDqEmpty)))
           break;
         tc_fence_after();
         const uint64_t dv = desc_add(dT, buf * L::kTile);
-        const uint32_t tp = tmem + buf * 128;
+        const uint32_t tp = tmem + buf * 128, to = tmem + L::kO + y % NO * D;
 #pragma unroll
         for (int kk = 0; kk < kKeys / 32; ++kk) {
-          mma_ts_f8(tmem + L::kO, tp + kk * 16, desc_add(dv, kk * 32 * D), kIdO, kk > 0 ? 1u : 0u);
-          mma_ts_f8(tmem + L::kO, tp + kk * 16 + 8, desc_add(dv, kk * 32 * D), kIdO, 1u);
+          mma_ts_f8(to, tp + kk * 16, desc_add(dv, kk * 32 * D), kIdO, kk > 0 ? 1u : 0u);
+          mma_ts_f8(to, tp + kk * 16 + 8, desc_add(dv, kk * 32 * D), kIdO, 1u);
         }
         tc_commit(&pv_done[buf]);
         if (++buf == NB) {
@@ -275,11 +283,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // (no rows: q's rows here stay what they are, and only rows that nothing reads come of them)
     regs_increase<kRegsAdd>();
   } else if (warp >= kWarpAdd) {
-    // ------------------------------------------------------------ O added up, half a row per thread; q's parts
+    // ------------------------------------------------------------ O added up, 64 columns of a row per thread; q's parts
     regs_increase<kRegsAdd>();
     const int r = (warp & 3) * 32 + lane, row = first_row + r;
     const bool first = warp < kWarpAdd + 4;
-    const int c0 = first ? 0 : D / 2;
+    const int c0 = first ? 0 : kCols;
     const bool used = r < rows;
     const int node = used ? row % p.Nt : -1, gh = used ? row / p.Nt : 0;
     // q of segment `seg`, into the buffer of the segment before the last one (whose products are all done: this
@@ -327,9 +335,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             wk.tail ? make_int4(-1, 0, 0, 0)
                     : make_int4(wk.b, wk.hk, c, static_cast<int>(divide((wk.u0 + wk.tiles) * run->runs - 1, run->total)));
       if (more && (more = wn.next())) load_q(wn, seg + 1);
-      float o[D / 2];
+      float o[kCols];
 #pragma unroll
-      for (int y = 0; y < D / 2; ++y) o[y] = 0.0f;
+      for (int y = 0; y < kCols; ++y) o[y] = 0.0f;
       float M = -INFINITY;
       for (int kt = wk.k0; ok && kt < wk.k1; ++kt, ++x) {
         if (!(ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[buf], ph, ctl, kSitePvDone)))) break;
@@ -338,17 +346,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           ph ^= 1;
         }
         tc_fence_after();
-        const float m = tile_m[(x & 3) * kRows + r], vs = tile_v[x & 3];
+        const float m = tile_m[x % L::kTiles * kRows + r], vs = tile_v[x % L::kTiles];
         const bool move = m > M + kMoveBy;
         if (__any_sync(0xffffffffu, move)) {
           const float a = move ? ex2(M - m) : 1.0f;  // (0 at first)
           if (move) M = m;
 #pragma unroll
-          for (int y = 0; y < D / 2; ++y) o[y] *= a;
+          for (int y = 0; y < kCols; ++y) o[y] *= a;
         }
         const float f = m == -INFINITY ? 0.0f : ex2(m - M) * vs;
         const float2 ff = make_float2(f, f);
-        const uint32_t tO = tmem + L::kO + lane_base + c0;
+        const uint32_t tO = tmem + L::kO + x % NO * D + lane_base + c0;
         auto gather = [&](const uint32_t (&w)[16], int q) {
 #pragma unroll
           for (int y = 0; y < 16; y += 2) {
@@ -359,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         };
 #pragma unroll
-        for (int q = 0; q < D / 2; q += 32) {
+        for (int q = 0; q < kCols; q += 32) {
           uint32_t wa[16], wb[16];
           tmem_ld16(tO + q, wa);
           tmem_ld16(tO + q + 16, wb);
@@ -369,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           gather(wb, q + 16);
         }
         tc_fence_before();
-        warp_arrive(o_empty);
+        warp_arrive(&o_empty[x % NO]);
       }
       // ---- the segment's result
       if (ok && wk.masked()) ok = __all_sync(0xffffffffu, mbar_wait(mask_full, nmask & 1, ctl, kSiteMaskFull));
@@ -377,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok && used) {
         float l = 0.0f;
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
+        for (int w = 0; w < W; ++w) {
           const float m = sum_m[w * kRows + r], v = sum_l[w * kRows + r];
           l += m == -INFINITY ? v : v * ex2(m - M);
         }
@@ -390,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (first) p.lse[(static_cast<long long>(wk.b) * p.H + h) * p.Nt + node] = any ? lse2 * kLn2 : -INFINITY;
           uint4 *dst = reinterpret_cast<uint4 *>(p.o + wk.b * p.so.b + h * p.so.h + node * p.so.n + c0);
 #pragma unroll
-          for (int y = 0; y < D / 2; y += 8)
+          for (int y = 0; y < kCols; y += 8)
             dst[y / 8] = any ? make_uint4(pack_bf16x2(o[y] * inv, o[y + 1] * inv), pack_bf16x2(o[y + 2] * inv, o[y + 3] * inv),
                                           pack_bf16x2(o[y + 4] * inv, o[y + 5] * inv),
                                           pack_bf16x2(o[y + 6] * inv, o[y + 7] * inv))
@@ -400,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (first) p.part_lse[at] = padding ? INFINITY : lse2;
           float4 *dst = reinterpret_cast<float4 *>(p.part_o + at * D + c0);
 #pragma unroll
-          for (int y = 0; y < D / 2; y += 4)
+          for (int y = 0; y < kCols; y += 4)
             dst[y / 4] = any ? make_float4(o[y] * inv, o[y + 1] * inv, o[y + 2] * inv, o[y + 3] * inv)
                              : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         }
@@ -438,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         vs = j < wk.len ? v_scale[j >> p.block_log2] : 0.0f;
       };
       if (y0 < x + n) fetch(wk.k0 + static_cast<int>(y0 - x));
-      for (; ok && y0 < x + n; y0 += 2) {
+      for (; ok && y0 < x + n; y0 += W) {
         const int kt = wk.k0 + static_cast<int>(y0 - x);
         const float vmax = warp_max_f32(vs);
         const float lr = vs > 0.0f ? fmaxf(lg2(vs) - lg2(vmax), -100.0f) : 0.0f;
@@ -449,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           sc[16 + lane] = ex2(-lr);
         }
         __syncwarp();
-        if (y0 + 2 < x + n) fetch(kt + 2);
+        if (y0 + W < x + n) fetch(kt + W);
         const bool masked = kt * kKeys + kKeys > from;
         if (masked && !have_mask) {
           if (!(ok = __all_sync(0xffffffffu, mbar_wait(mask_full, nmask & 1, ctl, kSiteMaskFull)))) break;
@@ -549,8 +557,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           lm = m;
         }
         l += lt == 0.0f ? 0.0f : lt * (m == -INFINITY ? 1.0f : ex2(m - lm));
-        tile_m[(y0 & 3) * kRows + r] = m;
-        if (r == 0) tile_v[y0 & 3] = vmax;
+        tile_m[y0 % L::kTiles * kRows + r] = m;
+        if (r == 0) tile_v[y0 % L::kTiles] = vmax;
         if (masked) {
           // V rows that no query row sees become zeros (0 * NaN is NaN)
           if (!(ok = __all_sync(0xffffffffu, mbar_wait(&v_full[buf], bph, ctl, kSiteVFull)))) break;
@@ -565,13 +573,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
         warp_arrive(&p_ready[buf]);
-        buf += 2;
+        buf += W;
         if (buf >= NB) {
           buf -= NB;
           bph ^= 1;
         }
       }
-      if (!ok && y0 < x + n) y0 += (x + n - y0 + 1) / 2 * 2;
+      if (!ok && y0 < x + n) y0 += (x + n - y0 + W - 1) / W * W;
       x += n;
       if (ok && wk.masked() && !have_mask)
         ok = __all_sync(0xffffffffu, mbar_wait(mask_full, nmask & 1, ctl, kSiteMaskFull));
