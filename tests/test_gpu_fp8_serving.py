@@ -33,7 +33,7 @@ def example():
     return next(b for b in blocks if "fa_fwd_tree_fp8" in b)
 
 
-class Checker:
+class Held:
     """The package, each call of the step held against its definition."""
 
     def __init__(self):
@@ -126,7 +126,7 @@ PARENTS = [[-1, 0, 0, 1, 1, 2, 3, 5], [-1, 0, 0, 0, 0, 4, -2, -2], [-2, -1, 0, 1
 def test_the_step(d, H, Hkv):
     B, Nk, Nt = 3, 400, 8
     g, names = setting(700 + d + H, B, H, Hkv, Nk, Nt, d, [130, 63, 200])
-    names["fa"], lens = Checker(), ref.ints([130, 63, 200])
+    names["fa"], lens = Held(), ref.ints([130, 63, 200])
     code, accepted = compile(example(), "example", "exec"), 0
     for step in range(6):
         names.update(draws(g, B, H, Hkv, Nt, d, lens, PARENTS, depths(PARENTS)))

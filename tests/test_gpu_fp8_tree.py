@@ -123,6 +123,28 @@ def test_long_and_many_units():
     run(g, 200, 2, 1, 1, 400, 128, 64, lens=[(b * 7) % 400 + 1 for b in range(200)], heads=[(b, 0) for b in range(0, 200, 11)])
 
 
+@pytest.mark.parametrize("d,H,Nt", [(64, 2, 1), (128, 4, 3), (128, 20, 2)])
+def test_more_sequences_than_threads(d, H, Nt):
+    g = ref.gen(2030 + d + H)
+    lens = [(b * 37) % 140 for b in range(3001)]
+    run(g, 3001, H, 1, Nt, 139, d, 32, lens=lens, heads=[(b, 0) for b in list(range(0, 3001, 250)) + [1, 2, 3, 2999, 3000]])
+
+
+def test_k_and_v_laid_out_differently():
+    """Strides of their own for q, k, v and o, scales apart: the same bits as packed tensors."""
+    g = ref.gen(2031)
+    for d, G, Nt in ((64, 2, 3), (128, 3, 7), (128, 8, 9)):
+        q = ref.draw(g, 2, 2 * G, Nt, d, "bnhd")
+        k, ks = r8.cache(g, 2, 2, 1300, d, 32, "bnhd")
+        v, vs = r8.cache(g, 2, 2, 1300, d, 32, "pitch")
+        o = torch.zeros(2, Nt, 2 * G, d + 8, device="cuda", dtype=torch.bfloat16).transpose(1, 2)[..., :d]
+        par, lens = tree_of(g, 2, Nt), ref.ints([1300, 900])
+        want = fa_fwd_tree_fp8(q.contiguous(), k.contiguous(), v.contiguous(), ks, vs, par, lens, block=32)
+        got = fa_fwd_tree_fp8(q, k, v, ks, vs, par, lens, block=32, o=o)
+        assert got[0] is o and torch.equal(o, want[0]) and torch.equal(got[1], want[1])
+        assert not bool(o.as_strided((2, Nt, 2 * G, 8), (Nt * 2 * G * (d + 8), 2 * G * (d + 8), d + 8, 1), d).any())
+
+
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("G,Nt", [(8, 1), (3, 3), (1, 7), (4, 4), (17, 1), (2, 16), (1, 33), (4, 16), (5, 13), (2, 64), (43, 3), (8, 40)])
 def test_rows_of_a_group(G, Nt, d):
