@@ -150,7 +150,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool has_run = find_run<kThreads>(p, c, run, reinterpret_cast<long long *>(small + L::kOffScan));
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  if (p.cuts && !p.cuts_by_unit && group == 0 && threadIdx.x == 0) p.cuts[c] = make_int4(-1, 0, 0, 0);
+  // (the thread that writes the cuts below writes this one, so that the two stores have an order)
+  if (p.cuts && !p.cuts_by_unit && group == 0 && threadIdx.x == kWarpAdd * 32) p.cuts[c] = make_int4(-1, 0, 0, 0);
   if (!has_run) {
     if (warp == kWarpS) tmem_dealloc(tmem, L::kTmem);
     return;
