@@ -305,4 +305,12 @@ __device__ __forceinline__ uint32_t visible(const uint32_t *bits, int i, bool li
   return __funnelshift_r(lo, hi, f & 31);
 }
 
+// Some node sees one of 16 rows, the first of which is node f of the tree (or before it).
+__device__ __forceinline__ bool slice_seen(const uint32_t *dead, int f) {
+  if (f < 0) return true;
+  if (f >= 128) return false;
+  const int w = f >> 5;
+  return (__funnelshift_r(~dead[w], w < 3 ? ~dead[w + 1] : 0u, f & 31) & 0xffffu) != 0u;
+}
+
 }  // namespace fa

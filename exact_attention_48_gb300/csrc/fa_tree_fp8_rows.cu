@@ -449,6 +449,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (y0 < x + n) fetch(wk.k0 + static_cast<int>(y0 - x));
       for (; ok && y0 < x + n; y0 += W) {
         const int kt = wk.k0 + static_cast<int>(y0 - x);
+        const bool masked = kt * kKeys + kKeys > from;
+        if (masked && !have_mask) {
+          if (!(ok = __all_sync(0xffffffffu, mbar_wait(mask_full, nmask & 1, ctl, kSiteMaskFull)))) break;
+          have_mask = true;
+        }
+        // (scales of rows that no node sees may be anything)
+        if (masked && !slice_seen(dead, kt * kKeys + (lane & 7) * 16 - from)) ks = vs = 0.0f;
         const float vmax = warp_max_f32(vs);
         const float lr = vs > 0.0f ? fmaxf(lg2(vs) - lg2(vmax), -100.0f) : 0.0f;
         __syncwarp();
@@ -459,11 +466,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         if (y0 + W < x + n) fetch(kt + W);
-        const bool masked = kt * kKeys + kKeys > from;
-        if (masked && !have_mask) {
-          if (!(ok = __all_sync(0xffffffffu, mbar_wait(mask_full, nmask & 1, ctl, kSiteMaskFull)))) break;
-          have_mask = true;
-        }
         if (!(ok = __all_sync(0xffffffffu, mbar_wait(&s_full[buf], bph, ctl, kSiteSFull)))) break;
         tc_fence_after();
         const float f = row_f[seg % 3 * kRows + r];  // (written before the products of this segment were issued)

@@ -517,15 +517,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (; y0 < x + n; y0 += W) {  // (a warp that gave up still meets the others)
         const int kt = wk.k0 + static_cast<int>(y0 - x);
         const uint32_t buf = y0 % NB;
-        // log2 of this value's scale over the tile's greatest (vanishing ones count as 2^-100 of it), and its inverse
-        const float kn = ks, vmax = warp_max_f32(v8), own = __shfl_sync(0xffffffffu, v8, (key >> 4) & 7);
-        const float lr = own > 0.0f ? fmaxf(lg2(own) - lg2(vmax), -100.0f) : 0.0f, inv = ex2(-lr);
-        if (y0 + W < x + n) fetch(kt + W);
         const bool masked = kt * kKeys + kKeys > from;
         if (ok && masked && !have_mask) {
           ok = __all_sync(0xffffffffu, mbar_wait(mask_full, nmask & 1, ctl, kSiteMaskFull));
           have_mask = true;
         }
+        // (scales of rows that no node sees may be anything)
+        if (masked && !slice_seen(dead, kt * kKeys + (lane & 7) * 16 - from)) v8 = 0.0f;
+        // log2 of this value's scale over the tile's greatest (vanishing ones count as 2^-100 of it), and its inverse
+        const float kn = ks, vmax = warp_max_f32(v8), own = __shfl_sync(0xffffffffu, v8, (key >> 4) & 7);
+        const float lr = own > 0.0f ? fmaxf(lg2(own) - lg2(vmax), -100.0f) : 0.0f, inv = ex2(-lr);
+        if (y0 + W < x + n) fetch(kt + W);
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&s_full[buf], (y0 / NB) & 1, ctl, kSiteSFull));
         if (!ok) {
           named_barrier(1 + wg, 128);

@@ -476,7 +476,8 @@ FA_API fa_status_t fa_cache_compact(const void *k, const int64_t *k_strides, con
  * (e4m3 is a floating type: a scale between two powers of two would gain
  * nothing, and a block is given another one by a shift of its exponents.)  The
  * conventions of the operators around the cache above hold for these calls too.
- * A scale none of whose rows is in use may hold anything.
+ * A scale none of whose rows is in use may hold anything; to fa_fwd_tree_fp8 the
+ * rows of padding nodes are not.
  */
 
 /*
