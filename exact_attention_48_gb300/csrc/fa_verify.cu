@@ -14,12 +14,12 @@
 // A sequence's row is cut over a cluster of CTAs, which add their sums through
 // distributed shared memory; all of them know every sum and take the same decisions.
 // Without a draft's row a rejection changes one value of R, so that one pass a node
-// gives all its sums.
+// gives its sums, but for those below a sixteenth of what was last added up.
 //
 // Precision.  Which token a number falls on is decided by a sum over the whole
-// vocabulary, so R and S are pairs of fp32 (hi + lo, about 48 bits), and so are the
-// comparisons: fp64 runs at a sixty-fourth of the fp32 rate here, 256 cycles for one
-// addition of a 512-thread CTA.
+// vocabulary, so R and S are pairs of fp32 (hi + lo, about 48 bits; 44 where S is a
+// difference), and so are the comparisons: fp64 runs at a sixty-fourth of the fp32 rate
+// here, 256 cycles for one addition of a 512-thread CTA.
 
 #include <cooperative_groups.h>
 #include <cstdint>
@@ -231,7 +231,8 @@ __global__ void __launch_bounds__(kThreads, 2) fa_verify_kernel(const VerifyPara
   };
 
   if (rank == 0 && tid == 0) accepted[0] = 0;
-  int have = 0;  // sums[0 .. have] are known
+  int have = 0;        // sums[0 .. have] are known
+  float added = 0.0f;  // the last of them that was added up
   for (int w = 0; w < kMaxNodes / 32; ++w) {
     // the children of the node among nodes 32 w .. 32 w + 31 (those of an accepted one come after it)
     uint32_t kids = __ballot_sync(0xffffffffu, s.parent[32 * w + lane] == node && 32 * w + lane > 0);
@@ -239,11 +240,14 @@ __global__ void __launch_bounds__(kThreads, 2) fa_verify_kernel(const VerifyPara
       const int i = 32 * w + __ffs(kids) - 1;
       kids &= kids - 1;
       if (k > have) {
-        Pair all;
-        if (!drafted && have > 0)
-          all = minus(s.sums[k - 1], s.taken);  // (k - 1 children were tried with a sum of this node's row)
-        else
+        // without a draft's row the rejected token is all that has gone; what is left is added up anew where it is a small
+        // part of the last sum, whose 48 bits it would not keep (or even turn negative)
+        Pair all{0.0f, 0.0f};
+        if (!drafted && have > 0) all = minus(s.sums[k - 1], s.taken);  // (k - 1 children were tried with a sum of this row)
+        if (drafted || have == 0 || !(all.hi >= 0.0625f * added)) {
           all = sum_rest();
+          added = all.hi;
+        }
         if (tid == 0) s.sums[k] = all;
         __syncthreads();
         have = k;

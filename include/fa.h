@@ -574,7 +574,7 @@ FA_API fa_status_t fa_cache_compact_fp8(const void *k, const int64_t *k_strides,
  *   counts    : int32 [B], how many; 0 for padding
  *   next_token: int32 [B]; -1 for padding
  *   1 <= Nt <= 128; V <= 2^30
- * Sums are taken to about 48 bits, so that a number decides as in the formulas.
+ * Sums are taken to about 44 bits, so that a number decides as in the formulas.
  */
 FA_API fa_status_t fa_tree_verify(const int *parents, int64_t parents_stride, const int *tokens,
                                   int64_t tokens_stride, const float *target, int64_t target_b_stride,
