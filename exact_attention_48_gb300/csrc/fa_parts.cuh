@@ -15,6 +15,8 @@ __device__ __forceinline__ float lg2(float x) {
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// 2^x / l, |x| up to 128 and l up to fp32's greatest: between the factors nothing leaves the range that the result is in.
+__device__ __forceinline__ float quotient(float x, float l) { return ex2(0.5f * x) * (1.0f / l) * ex2(0.5f * x); }
 // Four values as their two e4m3 parts.  (From fp32: the conversions of f16 pairs take several instructions each.)
 __device__ __forceinline__ void parts_of(float a, float b, float c, float d, uint32_t *hi, uint32_t *lo) {
   const uint32_t h = pack_e4m3x4(a, b, c, d);

@@ -16,11 +16,13 @@ constexpr float kLn2 = 0.69314718055994530942f;
 
 // Merge the partial results of units cut by a run's end:
 //   O = sum 2^(lse_s - M) O_s / sum 2^(lse_s - M).
+// (O_s up to bf16's greatest, of at most 152 runs: added up as 2^-8 of themselves.)
 // WARPS warps take one row of one cut unit, dealing the runs out among themselves
 // (a run's row is one coalesced read) and adding up in a fixed order: eight where a
 // unit is cut into many runs, one where it is cut into two or three (B16 H16 Nt32:
 // 4864 rows, 15 us with eight).
 constexpr int kMergeWarps = 8;
+constexpr float kAddAs = 0.00390625f;
 
 // +inf, the mark of padding, before NaN, and NaN before every other value.
 __device__ __forceinline__ float merge_max(float a, float b) {
@@ -56,9 +58,10 @@ __global__ void __launch_bounds__(kMergeWarps * 32) fa_tree_fp8_merge_kernel(con
     const float mn = merge_max(m, s);
     const float fa = m == mn ? 1.0f : (m == -INFINITY ? 0.0f : ex2(m - mn));
     const float fb = s == -INFINITY ? 0.0f : (s == mn ? 1.0f : ex2(s - mn));
+    const float fo = fb * kAddAs;
     l = l * fa + fb;
 #pragma unroll
-    for (int y = 0; y < kCols; ++y) o[y] = o[y] * fa + v[y] * fb;
+    for (int y = 0; y < kCols; ++y) o[y] = o[y] * fa + v[y] * fo;
     m = mn;
   }
   const int node = r % p.Nt, h = hk * p.G + r / p.Nt;
@@ -67,7 +70,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) fa_tree_fp8_merge_kernel(con
   if constexpr (WARPS == 1) {
     const bool any = m != -INFINITY && m != INFINITY;  // +inf: padding
 #pragma unroll
-    for (int y = 0; y < kCols; ++y) dst[y * 32 + lane] = __float2bfloat16(any ? o[y] / l : 0.0f);
+    for (int y = 0; y < kCols; ++y) dst[y * 32 + lane] = __float2bfloat16(any ? o[y] / l * (1.0f / kAddAs) : 0.0f);
     if (lane == 0) *lse = any ? (m + log2f(l)) * kLn2 : -INFINITY;
     return;
   }
@@ -90,7 +93,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) fa_tree_fp8_merge_kernel(con
     out += sh_o[w][threadIdx.x] * f;
   }
   const bool any = M != -INFINITY && M != INFINITY;
-  dst[threadIdx.x] = __float2bfloat16(any ? out / sum : 0.0f);
+  dst[threadIdx.x] = __float2bfloat16(any ? out / sum * (1.0f / kAddAs) : 0.0f);
   if (threadIdx.x == 0) *lse = any ? (M + log2f(sum)) * kLn2 : -INFINITY;
 }
 

@@ -67,9 +67,8 @@ struct LayoutRows {
   static constexpr uint32_t kOffRange = kOffJump + 128;
   static constexpr uint32_t kOffScan = kOffRange + 48;             // 20 warps' sums
   static constexpr uint32_t kOffScale = kOffScan + 20 * 8;         // [softmax warps][3][8]: a tile's scales
-  static constexpr uint32_t kOffTileM = kOffScale + kWarpAdd * 24 * 4;    // [tiles][128] m, and [tiles] the greatest vs
-  static constexpr uint32_t kOffTileV = kOffTileM + kTiles * kRows * 4;
-  static constexpr uint32_t kOffL = kOffTileV + kTiles * 4;              // [kSoft][128] l, [kSoft][128] its base
+  static constexpr uint32_t kOffTileM = kOffScale + kWarpAdd * 24 * 4;   // [tiles][128] m + log2 vs_max
+  static constexpr uint32_t kOffL = kOffTileM + kTiles * kRows * 4;      // [kSoft][128] l, [kSoft][128] its base
   static constexpr uint32_t kOffRow = kOffL + 2 * kSoft * kRows * 4;       // [3 segments][128] rows' factors
   static constexpr uint32_t kOffBar = kOffRow + 3 * kRows * 4;
   // k_full[3], v_full[3], s_full[3], p_ready[3], pv_done[3], q_full[2], o_empty[2], mask_full, mask_empty, l_full,
@@ -99,7 +98,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t *dead = reinterpret_cast<uint32_t *>(small + L::kOffDead);
   RunStart *run = reinterpret_cast<RunStart *>(small + L::kOffRange);
   auto floats = [&](uint32_t off) { return reinterpret_cast<float *>(small + off); };
-  float *tile_m = floats(L::kOffTileM), *tile_v = floats(L::kOffTileV), *row_f = floats(L::kOffRow);
+  float *tile_m = floats(L::kOffTileM), *row_f = floats(L::kOffRow);
   float *sum_l = floats(L::kOffL), *sum_m = sum_l + L::kSoft * kRows;
   uint64_t *k_full = reinterpret_cast<uint64_t *>(small + L::kOffBar), *v_full = k_full + NB;
   // Tile x of the run uses slot, buffer and barrier number x % 3 of each kind (a p_ready for each warpgroup would not do:
@@ -339,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float o[kCols];
 #pragma unroll
       for (int y = 0; y < kCols; ++y) o[y] = 0.0f;
-      float M = -INFINITY;
+      float A = -INFINITY;  // O is relative to 2^A
       for (int kt = wk.k0; ok && kt < wk.k1; ++kt, ++x) {
         if (!(ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[buf], ph, ctl, kSitePvDone)))) break;
         if (++buf == NB) {
@@ -347,15 +346,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           ph ^= 1;
         }
         tc_fence_after();
-        const float m = tile_m[x % L::kTiles * kRows + r], vs = tile_v[x % L::kTiles];
-        const bool move = m > M + kMoveBy;
+        const float m = tile_m[x % L::kTiles * kRows + r];
+        const bool move = m > A + kMoveBy;
         if (__any_sync(0xffffffffu, move)) {
-          const float a = move ? ex2(M - m) : 1.0f;  // (0 at first)
-          if (move) M = m;
+          const float a = move ? ex2(A - m) : 1.0f;  // (0 at first)
+          if (move) A = m;
 #pragma unroll
           for (int y = 0; y < kCols; ++y) o[y] *= a;
         }
-        const float f = m == -INFINITY ? 0.0f : ex2(m - M) * vs;
+        const float f = m == -INFINITY ? 0.0f : ex2(m - A);
         const float2 ff = make_float2(f, f);
         const uint32_t tO = tmem + L::kO + x % NO * D + lane_base + c0;
         auto gather = [&](const uint32_t (&w)[16], int q) {
@@ -384,7 +383,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok && wk.masked()) ok = __all_sync(0xffffffffu, mbar_wait(mask_full, nmask & 1, ctl, kSiteMaskFull));
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(l_full, seg & 1, ctl, kSiteLseFull));
       if (ok && used) {
-        float l = 0.0f;
+        float l = 0.0f, M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < W; ++w) M = fmaxf(M, sum_m[w * kRows + r]);
 #pragma unroll
         for (int w = 0; w < W; ++w) {
           const float m = sum_m[w * kRows + r], v = sum_l[w * kRows + r];
@@ -392,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const bool padding = wk.tail && ((dead[node >> 5] >> (node & 31)) & 1u);
         const bool any = l != 0.0f && !padding;
-        const float inv = any ? 1.0f / l : 0.0f;
+        const float inv = any ? quotient(A - M, l) : 0.0f;
         const float lse2 = any ? (M == -INFINITY ? 0.0f : M) - kLift + log2f(l) : -INFINITY;
         const int h = wk.hk * p.G + gh;
         if (wk.whole()) {
@@ -560,8 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           lm = m;
         }
         l += lt == 0.0f ? 0.0f : lt * (m == -INFINITY ? 1.0f : ex2(m - lm));
-        tile_m[y0 % L::kTiles * kRows + r] = m;
-        if (r == 0) tile_v[y0 % L::kTiles] = vmax;
+        tile_m[y0 % L::kTiles * kRows + r] = m + lg2(vmax);
         if (masked) {
           // V rows that no query row sees become zeros (0 * NaN is NaN)
           if (!(ok = __all_sync(0xffffffffu, mbar_wait(&v_full[buf], bph, ctl, kSiteVFull)))) break;

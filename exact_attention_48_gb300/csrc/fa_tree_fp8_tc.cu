@@ -11,9 +11,10 @@
 // Scales.  A score is scale * ks * (q . codes).  A value's scale goes into its
 // weight: with r_j = vs_j / (the tile's greatest vs), e_j = t_j + log2 r_j (t_j the
 // score in log2 units) and m = max e_j over the tile's 128 keys,
-//     P_j = 2^(e_j - m + 8),   O += vs_max 2^(m - M - 8) (P codes),
-//     l  += 2^(m - M - 8) sum P_j / r_j,
-// so a tile's weights always reach up to 2^8, whatever the running maximum M is:
+//     P_j = 2^(e_j - m + 8),   O += 2^(m + log2 vs_max - A - 8) (P codes),
+//     l  += 2^(m - M - 8) sum P_j / r_j,   o = 2^(A - M) O / l,
+// with references of their own for l and O: M near the greatest m and A near the greatest
+// m + log2 vs_max, so that neither sum leaves fp32's range with any scales.  So a tile's weights always reach up to 2^8, whatever the running maximum M is:
 // e4m3's second part ends at 2^-10, 2^-18 of the tile's greatest weighted value,
 // and a long flat tail beside one sharp key keeps its weight.  That takes a fresh
 // O^T a tile, which a warpgroup adds to fp32 registers.
@@ -99,8 +100,8 @@ struct LayoutTc {
   static constexpr uint32_t kOffScan = kOffRange + 48;                    // warps' sums
   static constexpr uint32_t kOffMost = kOffScan + 24 * 8;                 // [2][softmax warps][kCols] greatest e, in turn
   static constexpr uint32_t kOffBase = kOffMost + 2 * kSoftmaxWarps * kCols * 4;   // [softmax warps][2][kCols]: 8 - m, l's factor
-  static constexpr uint32_t kOffTileM = kOffBase + kSoftmaxWarps * 2 * kCols * 4;  // [kTiles][C] m and the greatest vs
-  static constexpr uint32_t kOffAdd = kOffTileM + kTiles * (C + 4) * 4;   // [4 warps][C]: factors of O
+  static constexpr uint32_t kOffTileM = kOffBase + kSoftmaxWarps * 2 * kCols * 4;  // [kTiles][C] m + log2 vs_max
+  static constexpr uint32_t kOffAdd = kOffTileM + kTiles * C * 4;         // [4 warps][C]: factors of O
   static constexpr uint32_t kOffL = kOffAdd + 4 * C * 4;                  // [softmax warps][kCols] l, and [groups][kCols] its base
   static constexpr uint32_t kOffLm = kOffL + kSoftmaxWarps * kCols * 4;
   static constexpr uint32_t kOffRow = kOffLm + kGroups * kCols * 4;           // [kSegs][C] rows' factors
@@ -395,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         p.cuts[p.cuts_by_unit ? wk.b * p.Hkv + wk.hk : c] =
             wk.tail ? make_int4(-1, 0, 0, 0)
                     : make_int4(wk.b, wk.hk, c, static_cast<int>(divide((wk.u0 + wk.tiles) * run->runs - 1, run->total)));
-      float o[C], M = -INFINITY;
+      float o[C], A = -INFINITY;  // O is relative to 2^A
 #pragma unroll
       for (int r = 0; r < C; ++r) o[r] = 0.0f;
       for (int kt = wk.k0; ok && kt < wk.k1; ++kt, ++x) {
@@ -403,12 +404,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[buf], (x / NB) & 1, ctl, kSitePvDone)))) break;
         tc_fence_after();
         // the factor of the column that this lane looks after
-        const float *tm = tile_m + x % L::kTiles * (C + 4), vs = tm[C];
-        const float m = tm[mine];
-        const bool move = m > M + kMoveBy;
-        const float alpha = move ? ex2(M - m) : 1.0f;  // (0 at first)
-        if (move) M = m;
-        fac[mine] = m == -INFINITY ? 0.0f : ex2(m - M) * vs;
+        const float m = tile_m[x % L::kTiles * C + mine];
+        const bool move = m > A + kMoveBy;
+        const float alpha = move ? ex2(A - m) : 1.0f;  // (0 at first)
+        if (move) A = m;
+        fac[mine] = m == -INFINITY ? 0.0f : ex2(m - A);
         __syncwarp();
         if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
@@ -438,7 +438,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const long long slot = (static_cast<long long>(blockIdx.x) * 2 + (wk.k0 == 0 ? 1 : 0)) * C;
       if (ok) {
         const int row = first_row + mine;
-        float l = 0.0f;
+        float l = 0.0f, M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < L::kAtWork; ++w) M = fmaxf(M, sum_m[(w * L::kHalves + mine / kCols) * kCols + mine % kCols]);
 #pragma unroll
         for (int w = 0; w < 4 * L::kAtWork; ++w) {
           const int wg = (w >> 2) * L::kHalves + mine / kCols, col = mine % kCols;
@@ -448,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int row_node = row < unit_rows ? row % p.Nt : 0;
         const bool padding = wk.tail && ((dead[row_node >> 5] >> (row_node & 31)) & 1u);
         const bool any = l != 0.0f && !padding;
-        fac[mine] = any ? 1.0f / l : 0.0f;
+        fac[mine] = any ? quotient(A - M, l) : 0.0f;
         if (warp == kWarpAdd && lane < C && row < unit_rows) {
           const float lse2 = any ? (M == -INFINITY ? 0.0f : M) - kLift + log2f(l) : -INFINITY;
           const int h = wk.hk * p.G + row / p.Nt;
@@ -584,8 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (move) lm = m;
         base[mine] = kLift - (m == -INFINITY ? 0.0f : m);
         base[kCols + mine] = m == -INFINITY ? 0.0f : ex2(m - lm);
-        if ((warp & 3) == 0) tile_m[y0 % L::kTiles * (C + 4) + c0 + mine] = m;
-        if ((warp & 3) == 0 && lane == 0) tile_m[y0 % L::kTiles * (C + 4) + C] = vmax;
+        if ((warp & 3) == 0) tile_m[y0 % L::kTiles * C + c0 + mine] = m + lg2(vmax);
         __syncwarp();
         if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
