@@ -17,7 +17,8 @@
 // the CTA.  B4 H32 Hkv8 N4001 d128 (360 MB, 53 us at the copy rate): one head ahead in
 // registers 104 us, three in shared memory 92 (issue slots: 380 instructions a piece,
 // many of them addresses); one of the three tensors a CTA, addresses stepped from
-// head to head and infinities looked for by the greatest value alone 76, 0.70 of that rate.  A CTA
+// head to head and infinities looked for by the greatest value alone 76, 0.70 of that rate (64
+// registers, so that 1024 threads fit an SM; 44 to 52 bytes of spills stored, 32 to 36 loaded).  A CTA
 // works out its tokens' angles itself (some 50 instructions each): with as few CTAs as
 // fill the SMs B16 H16 Hkv1 N1500 d64 takes 23 us, with four times as many 29.
 

@@ -11,6 +11,7 @@
 // 64 of them an SM keep loads in flight.  B16 Hkv16 16384 to 8192 rows d128 (1.1 GB) 164 us,
 // 0.98 of the copy bandwidth (blocks of 128 rows: 174); a CTA a window of 128 rows with
 // the blocks' greatest scales found in shared memory took 209, both tensors in a CTA 324.
+// (32 registers; at d = 128 28 bytes of spills stored, 36 loaded.)
 //
 // In place a destination row may be the source of an earlier destination only (kept
 // ascends and kept[i] >= i), so a head's windows of K or V go in order.  Columns do
@@ -19,7 +20,9 @@
 // cluster barrier a window lets the first of them write a window's scales only when
 // all have read them.  The next window's rows and the list after it are on their way
 // meanwhile (a later window's sources lie behind the rows written here).  B16 Hkv16 16384 to
-// 8192 rows d128 300 us; B1 Hkv2 131072 to 65536 rows 159 us, 1214 with a CTA a head.
+// 8192 rows d128 292 us; B1 Hkv2 131072 to 65536 rows 158 us, 1214 with a CTA a head; B1
+// Hkv8 328 us.  The bf16 cache's move (fa_cache_compact.cu) takes 363, 103 and 119 for twice
+// the bytes: a head's slices have no scale in common there and need not meet.
 
 #include <cstdint>
 

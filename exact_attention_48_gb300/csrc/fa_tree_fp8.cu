@@ -128,11 +128,14 @@ constexpr int kWholeTiles = 8;
 //                                           168 (16)
 //                       d = 64              110 (8)     224
 //                                           135 (16)
-//   B2 H32 Hkv8 T5 Nk100001, d = 128         87 (32)    114
+//   B2 H32 Hkv8 T5 Nk100001, d = 128         86 (32)    114
 //                            d = 64          82 (32)     96
-//   B16 H16 T32 Nk16384, d = 128            203 (32)    264
+//   B16 H16 T32 Nk16384, d = 128            207 (32)    264
 //                        d = 64             187 (32)    224
 //   B2 H32 Hkv8 T64 Nk65536, d = 128        405 (64)    157
+// Runs: as many as fill the SMs with a CTA for each of the unit's groups.  77 to 151 groups
+// (9729 query rows of a cache head and more) make one run, and leave up to half of the
+// SMs without a CTA; not measured.
 Tree8Plan plan_tree8(int B, int H, int Hkv, int Nt, int Nk, int d) {
   Tree8Plan pl{};
   const int rows = H / Hkv * Nt;  // (below 2^31: H < 2^24, Nt <= 128)

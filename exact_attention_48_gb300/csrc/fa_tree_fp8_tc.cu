@@ -14,23 +14,26 @@
 //     P_j = 2^(e_j - m + 8),   O += 2^(m + log2 vs_max - A - 8) (P codes),
 //     l  += 2^(m - M - 8) sum P_j / r_j,   o = 2^(A - M) O / l,
 // with references of their own for l and O: M near the greatest m and A near the greatest
-// m + log2 vs_max, so that neither sum leaves fp32's range with any scales.  So a tile's weights always reach up to 2^8, whatever the running maximum M is:
-// e4m3's second part ends at 2^-10, 2^-18 of the tile's greatest weighted value,
-// and a long flat tail beside one sharp key keeps its weight.  That takes a fresh
-// O^T a tile, which a warpgroup adds to fp32 registers.
+// m + log2 vs_max, so that neither sum leaves fp32's range, whatever the scales are.  A
+// tile's weights always reach up to 2^8: e4m3's second part ends at 2^-10, 2^-18 of the
+// tile's greatest weighted value, and a long flat tail beside one sharp key keeps its
+// weight.  That takes a fresh O^T a tile, which a warpgroup adds to fp32 registers.
+// vs_max is taken over the slices of 16 keys that some row sees; r_j is 2^-100 at least
+// (1 / r_j has to stay in fp32).
 //
 // Rounding.  A row of q is divided by a power of two so that its greatest value lies
 // in (224, 448]; bf16's 8 bits are 4 + 4, so its parts are exact but where the second
 // falls below e4m3's least step: off by at most 2^-10, 2^-17.8 of the row's greatest
 // value.  A weight is rounded to its parts likewise: off by at most 2^-9 of itself, or
-// 2^-10 with its tile's greatest at 2^8.  Scores, maxima, sums and O are fp32.
+// 2^-10 with its tile's greatest at 2^8; l adds up the unrounded weights.  Scores, maxima,
+// sums and O are fp32.
 //
 // What bounds it.  HBM, 2 d bytes a key: a 128-key tile takes an SM 1400 cycles of its
 // share of the traffic at d = 128, its products some 560 (a tcgen05 instruction takes 60 or
 // more whatever its N) and its softmax about 10 issue slots a row and warp.  Up to 8
 // rows: B16 H16 T1 Nk16384 (1.1 GB) 162 us, 0.98 of the copy bandwidth.  32 rows: B16 H16
-// T32 Nk16384 (lengths of three quarters on average, 0.8 GB) 171 us, 0.72, and B2 H32 Hkv8
-// T5 Nk100001 (0.4 GB) 89 us, 0.68, where a run of 82 tiles has a start, an end and a
+// T32 Nk16384 (lengths of three quarters on average, 0.8 GB) 176 us, 0.70, and B2 H32 Hkv8
+// T5 Nk100001 (0.4 GB) 86 us, 0.70, where a run of 82 tiles has a start, an end and a
 // second launch to pay for: 63 % of the issue slots, and the way of a tile through
 // its softmax (1750 cycles a tile).  d = 64: a tile has half the bytes and takes the same
 // steps, 110 us for the first (0.54 GB), 187 for the second's shape with full caches.
@@ -61,7 +64,9 @@ constexpr float kLn2 = 0.69314718055994530942f;
 // control warps.  A softmax warpgroup takes 16 columns of a tile: with 32 columns two
 // share a tile (one with all 32 would need 112 registers, and code that does not stay in
 // the instruction cache: three of them took 1830 cycles a tile).  Registers: launched
-// with kRegsLaunch a thread, split by setmaxnreg.
+// with kRegsLaunch a thread, split by setmaxnreg; that many is what the compiler keeps to
+// in every role, and it spills for it: 152 to 160 bytes stored (340 to 368 loaded) with 16 and
+// 32 columns, 88 to 100 (196 to 208) with 8.
 constexpr int kGroups = 4, kSoftmaxWarps = 4 * kGroups, kThreads = 128 * (kGroups + 2);
 constexpr int kWarpAdd = kSoftmaxWarps, kWarpProducer = kWarpAdd + 4, kWarpS = kWarpProducer + 1;
 constexpr int kWarpO = kWarpProducer + 2, kWarpQ = kWarpProducer + 3;
@@ -493,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int W = L::kAtWork;
     const int wg = warp >> 2, key = threadIdx.x & 127, mine = lane & (kCols - 1);
     const int c0 = wg % L::kHalves * kCols;  // its first column
-        float *base = floats(L::kOffBase) + warp * 2 * kCols;  // 8 - m, then l's factor
+    float *base = floats(L::kOffBase) + warp * 2 * kCols;  // 8 - m, then l's factor
     uint32_t x = 0, seg = 0, nmask = 0;  // tiles before the segment, segments, masked ones
     uint32_t y0 = wg / L::kHalves;       // this warpgroup's next tile of the run
     bool ok = true;
@@ -623,8 +628,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (masked) {
-          // V rows that no query row sees become zeros (0 * NaN is NaN).  (The buffer's number is worked out anew here: one
-          // more register for it above is spilled, 215 us for 203.)
+          // V rows that no query row sees become zeros (0 * NaN is NaN).  (The buffer's number is worked out anew here: kept
+          // from above it is one more register spilled in the loop, 215 us for 203.)
           if (!(ok = __all_sync(0xffffffffu, mbar_wait(&v_full[y0 % NB], (y0 / NB) & 1, ctl, kSiteVFull)))) continue;
           if (c0 == 0 && (node >= p.Nt || (node >= 0 && ((dead[node >> 5] >> (node & 31)) & 1u)))) {
             uint4 *v = reinterpret_cast<uint4 *>(ring_v + (y0 % NB) * L::kTile + key * D);

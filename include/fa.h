@@ -511,7 +511,8 @@ FA_API fa_status_t fa_rope_append_fp8(const void *q, const int64_t *q_strides, c
  * of that); scores, sums and o are fp32.  A weight is off by at most 2^-9 of itself,
  * or, times its value's scale, 2^-18 of the greatest such product among the 128 rows
  * that it is worked on with; there a value's scale below 2^-100 of the greatest one
- * counts as 2^-100 of it.  A row of q that is not finite gives NaN.
+ * counts as 2^-100 of it.  o is divided by the sum of the weights as they were before
+ * that rounding (fa_fwd_tree's by the sum of the rounded ones).  A row of q that is not finite gives NaN.
  */
 FA_API size_t fa_tree_fp8_workspace_bytes(int B, int H, int Hkv, int Nt, int Nk, int d);
 
