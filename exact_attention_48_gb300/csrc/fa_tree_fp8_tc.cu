@@ -21,8 +21,8 @@
 // vs_max is taken over the slices of 16 keys that some row sees; r_j is 2^-100 at least
 // (1 / r_j has to stay in fp32).
 //
-// Rounding.  A row of q is divided by a power of two so that its greatest value lies
-// in (224, 448]; bf16's 8 bits are 4 + 4, so its parts are exact but where the second
+// Rounding.  A row of q is divided by a power of two (2^-100 or more) so that its greatest
+// value lies in (224, 448]; bf16's 8 bits are 4 + 4, so its parts are exact but where the second
 // falls below e4m3's least step: off by at most 2^-10, 2^-17.8 of the row's greatest
 // value.  A weight is rounded to its parts likewise: off by at most 2^-9 of itself, or
 // 2^-10 with its tile's greatest at 2^8; l adds up the unrounded weights.  Scores, maxima,

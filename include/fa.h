@@ -507,8 +507,8 @@ FA_API fa_status_t fa_rope_append_fp8(const void *q, const int64_t *q_strides, c
  * scores that are not finite and the workspace as there.  parents may be NULL: the
  * last Nt rows are a chain, each of which sees the rows up to its own (Nt = 1: one
  * new token; several: the causal decode).  The products run on the codes, q to
- * 2^-17.8 of a row's greatest magnitude (exactly, where its values are within 2^9
- * of that); scores, sums and o are fp32.  A weight is off by at most 2^-9 of itself,
+ * 2^-17.8 of a row's greatest magnitude, or of 2^-91 where that is less (exactly,
+ * where its values are within 2^9 of that); scores, sums and o are fp32.  A weight is off by at most 2^-9 of itself,
  * or, times its value's scale, 2^-18 of the greatest such product among the 128 rows
  * that it is worked on with; there a value's scale below 2^-100 of the greatest one
  * counts as 2^-100 of it.  o is divided by the sum of the weights as they were before
